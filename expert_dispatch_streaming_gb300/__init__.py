@@ -31,7 +31,8 @@ GATING = {"softmax_renorm": 0, "softmax": 1, "sigmoid_bias_renorm": 2}
 MOE_W_BF16 = 0
 MOE_W_INT4_G128 = 1
 MOE_W_NVFP4 = 2
-WDTYPE = {"bf16": 0, "int4_g128": 1, "nvfp4": 2}
+MOE_W_FP8_B128 = 3
+WDTYPE = {"bf16": 0, "int4_g128": 1, "nvfp4": 2, "fp8_b128": 3}
 
 
 class MoEError(RuntimeError):
@@ -115,10 +116,14 @@ _SIGS = {
     "moe_bundle_bytes": (_sz, [_i, _i, _i]),
     "moe_pack_bundle": (_i, [_i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
     "moe_pack_bundle_nvfp4": (_i, [_i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "moe_pack_bundle_fp8": (_i, [_i, _i, _vp, _vp, _vp, _vp, _vp]),
+    "moe_pack_bundle_fp8_device": (_i, [_i, _i, _vp, _vp, _vp, _vp, _vp, _vp]),
     "moe_checksum64": (C.c_uint64, [_vp, _sz]),
     "moe_route_workspace_size": (_sz, [_i, _i, _i, _i]),
     "moe_route_topk": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _f,
                             _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "moe_route_topk_grouped": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _f,
+                                    _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
     "moe_route_topk_static": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _f,
                                    _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
     "moe_route_static_error": (_i, [C.POINTER(C.c_int32), _vp]),
@@ -126,6 +131,13 @@ _SIGS = {
     "moe_grouped_swiglu_workspace_size": (_sz, [_i, _i, _i, _i, _i]),
     "moe_grouped_swiglu": (_i, [_vp, _vp, C.POINTER(_vp), _i, _i, _i, _i, _i, _vp, _vp, _sz,
                                 _vp]),
+    "moe_quantize_fp8": (_i, [_vp, _vp, _i, _i, _i, _vp, _vp, _vp]),
+    "moe_grouped_gemm_fp8_workspace_size": (_sz, [_i, _i, _i, _i]),
+    "moe_grouped_gemm_fp8": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp, _vp, _sz,
+                                  _vp]),
+    "moe_grouped_swiglu_fp8_workspace_size": (_sz, [_i, _i, _i, _i]),
+    "moe_grouped_swiglu_fp8": (_i, [_vp, _vp, _vp, C.POINTER(_vp), _i, _i, _i, _i, _vp, _vp,
+                                    _sz, _vp]),
     "moe_combine": (_i, [_vp, _vp, _vp, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _f, _vp]),
     "moe_expert_cache_create": (_i, [C.POINTER(moe_expert_cache_config), C.POINTER(_vp),
                                      C.POINTER(C.c_int64)]),
@@ -247,6 +259,21 @@ def moe_pack_bundle_nvfp4(H, I, wg, wu, wd, sg, su, sd, gs, dst) -> None:
                                       ptr(sd), ptr(gs), ptr(dst)), "moe_pack_bundle_nvfp4")
 
 
+def moe_pack_bundle_fp8(H, I, w_gate_up, s_gate_up, w_down, s_down, dst) -> None:
+    """w_gate_up [2I][H], w_down [H][I]: E4M3 bytes (weight rows); s_gate_up [2I/128][H/128],
+    s_down [H/128][I/128]: float32.  Host arrays."""
+    _check(_lib.moe_pack_bundle_fp8(H, I, ptr(w_gate_up), ptr(s_gate_up), ptr(w_down),
+                                    ptr(s_down), ptr(dst)), "moe_pack_bundle_fp8")
+
+
+def moe_pack_bundle_fp8_device(H, I, w_gate_up, s_gate_up, w_down, s_down, dst,
+                               stream=None) -> None:
+    """moe_pack_bundle_fp8 from device tensors into a device bundle."""
+    _check(_lib.moe_pack_bundle_fp8_device(H, I, ptr(w_gate_up), ptr(s_gate_up), ptr(w_down),
+                                           ptr(s_down), ptr(dst), stream_handle(stream)),
+           "moe_pack_bundle_fp8_device")
+
+
 def moe_checksum64(data, nbytes) -> int:
     return _lib.moe_checksum64(ptr(data), nbytes)
 
@@ -264,6 +291,19 @@ def moe_route_topk(x, w_r, logit_bias, sel_bias, w_gate, forced_ids, T, H, E, k,
                                ptr(pos), ptr(src), ptr(logits), ptr(shared_gate),
                                ptr(tie_flags), ptr(ws), ws_bytes, stream_handle(stream)),
            "moe_route_topk")
+
+
+def moe_route_topk_grouped(x, w_r, logit_bias, sel_bias, w_gate, T, H, E, k, n_group, topk_group,
+                           gating, scale, ids, w, counts, offsets, pos, src, logits, shared_gate,
+                           tie_flags, ws, ws_bytes, stream=None) -> None:
+    """moe_route_topk with the k experts taken from the topk_group best of n_group groups."""
+    _check(_lib.moe_route_topk_grouped(ptr(x), ptr(w_r), ptr(logit_bias), ptr(sel_bias),
+                                       ptr(w_gate), T, H, E, k, n_group, topk_group,
+                                       GATING.get(gating, gating), float(scale), ptr(ids),
+                                       ptr(w), ptr(counts), ptr(offsets), ptr(pos), ptr(src),
+                                       ptr(logits), ptr(shared_gate), ptr(tie_flags), ptr(ws),
+                                       ws_bytes, stream_handle(stream)),
+           "moe_route_topk_grouped")
 
 
 def moe_route_topk_static(x, w_r, logit_bias, sel_bias, w_gate, forced_ids, T, H, E, k, gating,
@@ -293,6 +333,47 @@ def moe_permute(x, src, T, k, H, x_perm, stream=None) -> None:
 
 def moe_grouped_swiglu_workspace_size(max_rows, E, H, I, wdtype) -> int:
     return _lib.moe_grouped_swiglu_workspace_size(max_rows, E, H, I, WDTYPE.get(wdtype, wdtype))
+
+
+def bundle_table(bundles):
+    """The host array of device bundle pointers the grouped calls take, built once for calls
+    that repeat (they also accept any sequence of tensors / addresses)."""
+    if isinstance(bundles, C.Array):
+        return bundles
+    return (C.c_void_p * len(bundles))(*[ptr(b) for b in bundles])
+
+
+def moe_quantize_fp8(x, src, T, k, H, q, scale, stream=None) -> None:
+    """bf16 rows x [T][H] -> E4M3 q and fp32 scale per 128 columns; with src [T*k], gathered:
+    row p from x[src[p] // k]."""
+    _check(_lib.moe_quantize_fp8(ptr(x), ptr(src), T, k, H, ptr(q), ptr(scale),
+                                 stream_handle(stream)), "moe_quantize_fp8")
+
+
+OUT_DTYPE = {"bf16": 0, "fp32": 1}
+
+
+def moe_grouped_gemm_fp8_workspace_size(max_rows, E, N, K) -> int:
+    return _lib.moe_grouped_gemm_fp8_workspace_size(max_rows, E, N, K)
+
+
+def moe_grouped_gemm_fp8(xq, x_scale, w, w_scale, offsets, E, N, K, max_rows, out, y, ws, ws_bytes,
+                         stream=None) -> None:
+    """out: 'bf16' or 'fp32' (the type of y)."""
+    _check(_lib.moe_grouped_gemm_fp8(ptr(xq), ptr(x_scale), ptr(w), ptr(w_scale), ptr(offsets), E,
+                                     N, K, max_rows, OUT_DTYPE.get(out, out), ptr(y), ptr(ws),
+                                     ws_bytes, stream_handle(stream)), "moe_grouped_gemm_fp8")
+
+
+def moe_grouped_swiglu_fp8_workspace_size(max_rows, E, H, I) -> int:
+    return _lib.moe_grouped_swiglu_fp8_workspace_size(max_rows, E, H, I)
+
+
+def moe_grouped_swiglu_fp8(xq, x_scale, offsets, bundles, E, H, I, max_rows, y_perm, ws, ws_bytes,
+                           stream=None) -> None:
+    _check(_lib.moe_grouped_swiglu_fp8(ptr(xq), ptr(x_scale), ptr(offsets), bundle_table(bundles),
+                                       E, H, I, max_rows, ptr(y_perm), ptr(ws), ws_bytes,
+                                       stream_handle(stream)), "moe_grouped_swiglu_fp8")
 
 
 def moe_grouped_swiglu(x_perm, offsets, bundles, E, H, I, wdtype, max_rows, y_perm, ws, ws_bytes,

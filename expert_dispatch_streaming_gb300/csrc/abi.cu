@@ -50,6 +50,43 @@ static bool valid_route_shape(int T, int H, int E, int k) {
          k <= std::min(E, kMaxK);
 }
 
+// groups of equal size, and enough experts in the taken ones for k
+static bool valid_groups(int E, int k, int n_group, int take) {
+  return n_group >= 1 && n_group <= kMaxGroups && E % n_group == 0 && take >= 1 &&
+         take <= n_group && k <= take * (E / n_group);
+}
+
+// moe_route_topk and moe_route_topk_grouped (n_group = 0: no groups)
+static int route_topk(const uint16_t* x, const float* w_r, const float* logit_bias,
+                      const float* sel_bias, const uint16_t* w_gate, const int32_t* forced_ids,
+                      int T, int H, int E, int k, int n_group, int take, int gating, float scale,
+                      int32_t* ids, float* w, int32_t* counts, int32_t* offsets, int32_t* pos,
+                      int32_t* src, float* logits, float* shared_gate, int32_t* tie_flags,
+                      void* ws, size_t ws_bytes, void* stream) {
+  MOE_REQUIRE(valid_route_shape(T, H, E, k));
+  MOE_REQUIRE(gating >= 0 && gating <= 2);
+  MOE_REQUIRE(counts && offsets && ws);
+  MOE_REQUIRE(T == 0 || (x && w_r && ids && w && pos && src));
+  MOE_REQUIRE(!w_gate || shared_gate);
+  const RoutePlan rp = plan_route(T, H, E, k, w_gate != nullptr);
+  WsCursor c(ws, ws_bytes);
+  int32_t* err = c.take<int32_t>(64);
+  RouteScratch s{};
+  route_scratch(c, rp, T, E, &s);
+  MOE_REQUIRE(c.ok());
+  // the error word (first 4 bytes of ws) starts every call at zero; only the tensor-core
+  // router's bounded waits (T >= 256) can set it
+  MOE_CUDA_TRY(cudaMemsetAsync(err, 0, sizeof(int32_t), (cudaStream_t)stream));
+  RouteArgs a{};
+  a.x = x; a.w_r = w_r; a.logit_bias = logit_bias; a.sel_bias = sel_bias; a.w_gate = w_gate;
+  a.forced = forced_ids; a.T = T; a.H = H; a.E = E; a.k = k; a.gating = gating;
+  a.scale = scale; a.ids = ids; a.counts = counts; a.offsets = offsets; a.pos = pos;
+  a.src = src; a.tie_flags = tie_flags; a.w = w; a.logits = logits;
+  a.shared_gate = shared_gate; a.x_perm = nullptr; a.err = err;
+  a.n_group = n_group; a.take = take;
+  return launch_route(a, rp, s, (cudaStream_t)stream);
+}
+
 // ------------------------------------------------------------------ layer plan
 struct LayerScratch {
   RouteScratch rs;
@@ -93,7 +130,7 @@ static GemmArgs gemm_args(const moe_bundle_layout& lay, int wdtype, bool fused, 
 }
 
 static int make_plan(const moe_layer* L, int T, LayerPlan* P) {
-  if (!L || !valid_route_shape(T, L->H, L->E, L->k) || L->I <= 0 || L->I % 128 ||
+  if (!L || L->wdtype == MOE_W_FP8_B128 || !valid_route_shape(T, L->H, L->E, L->k) || L->I <= 0 || L->I % 128 ||
       L->H % 128 || L->Is < 0 || L->Is % 128)
     return MOE_ERR_INVALID_ARG;
   if (moe_bundle_layout_of(L->H, L->I, L->wdtype, &P->lay) != MOE_OK) return MOE_ERR_INVALID_ARG;
@@ -312,27 +349,21 @@ int moe_route_topk(const uint16_t* x, const float* w_r, const float* logit_bias,
                    int32_t* counts, int32_t* offsets, int32_t* pos, int32_t* src,
                    float* logits, float* shared_gate, int32_t* tie_flags, void* ws,
                    size_t ws_bytes, void* stream) {
-  MOE_REQUIRE(valid_route_shape(T, H, E, k));
-  MOE_REQUIRE(gating >= 0 && gating <= 2);
-  MOE_REQUIRE(counts && offsets && ws);
-  MOE_REQUIRE(T == 0 || (x && w_r && ids && w && pos && src));
-  MOE_REQUIRE(!w_gate || shared_gate);
-  const RoutePlan rp = plan_route(T, H, E, k, w_gate != nullptr);
-  WsCursor c(ws, ws_bytes);
-  int32_t* err = c.take<int32_t>(64);
-  RouteScratch s{};
-  route_scratch(c, rp, T, E, &s);
-  MOE_REQUIRE(c.ok());
-  // the error word (first 4 bytes of ws) starts every call at zero; only the tensor-core
-  // router's bounded waits (T >= 256) can set it
-  MOE_CUDA_TRY(cudaMemsetAsync(err, 0, sizeof(int32_t), (cudaStream_t)stream));
-  RouteArgs a{};
-  a.x = x; a.w_r = w_r; a.logit_bias = logit_bias; a.sel_bias = sel_bias; a.w_gate = w_gate;
-  a.forced = forced_ids; a.T = T; a.H = H; a.E = E; a.k = k; a.gating = gating;
-  a.scale = scale; a.ids = ids; a.counts = counts; a.offsets = offsets; a.pos = pos;
-  a.src = src; a.tie_flags = tie_flags; a.w = w; a.logits = logits;
-  a.shared_gate = shared_gate; a.x_perm = nullptr; a.err = err;
-  return launch_route(a, rp, s, (cudaStream_t)stream);
+  return route_topk(x, w_r, logit_bias, sel_bias, w_gate, forced_ids, T, H, E, k, 0, 0, gating,
+                    scale, ids, w, counts, offsets, pos, src, logits, shared_gate, tie_flags, ws,
+                    ws_bytes, stream);
+}
+
+int moe_route_topk_grouped(const uint16_t* x, const float* w_r, const float* logit_bias,
+                           const float* sel_bias, const uint16_t* w_gate, int T, int H, int E,
+                           int k, int n_group, int topk_group, int gating, float scale,
+                           int32_t* ids, float* w, int32_t* counts, int32_t* offsets,
+                           int32_t* pos, int32_t* src, float* logits, float* shared_gate,
+                           int32_t* tie_flags, void* ws, size_t ws_bytes, void* stream) {
+  MOE_REQUIRE(valid_route_shape(T, H, E, k) && valid_groups(E, k, n_group, topk_group));
+  return route_topk(x, w_r, logit_bias, sel_bias, w_gate, nullptr, T, H, E, k, n_group,
+                    topk_group, gating, scale, ids, w, counts, offsets, pos, src, logits,
+                    shared_gate, tie_flags, ws, ws_bytes, stream);
 }
 
 int moe_permute(const uint16_t* x, const int32_t* src, int T, int k, int H, uint16_t* x_perm,
@@ -345,7 +376,8 @@ int moe_permute(const uint16_t* x, const int32_t* src, int T, int k, int H, uint
 
 size_t moe_grouped_swiglu_workspace_size(int max_rows, int E, int H, int I, int wdtype) {
   moe_bundle_layout lay;
-  if (max_rows < 0 || E <= 0 || E > kMaxExperts || moe_bundle_layout_of(H, I, wdtype, &lay))
+  if (max_rows < 0 || E <= 0 || E > kMaxExperts || wdtype == MOE_W_FP8_B128 ||
+      moe_bundle_layout_of(H, I, wdtype, &lay))
     return 0;
   WsCursor c(nullptr, 0);
   c.take<int32_t>(64);
@@ -373,7 +405,7 @@ int moe_grouped_swiglu(const uint16_t* x_perm, const int32_t* offsets,
                        int max_rows, uint16_t* y_perm, void* ws, size_t ws_bytes,
                        void* stream) {
   moe_bundle_layout lay;
-  MOE_REQUIRE(E > 0 && E <= kMaxExperts && max_rows >= 0);
+  MOE_REQUIRE(E > 0 && E <= kMaxExperts && max_rows >= 0 && wdtype != MOE_W_FP8_B128);
   MOE_REQUIRE(moe_bundle_layout_of(H, I, wdtype, &lay) == MOE_OK);
   if (max_rows == 0) return MOE_OK;
   MOE_REQUIRE(x_perm && offsets && bundles && y_perm && ws);

@@ -127,6 +127,21 @@ bool pack_tiled_nvfp4(const uint8_t* codes, const uint8_t* scales, size_t K, siz
   return ok;
 }
 
+// Tiled E4M3 image of the row-major codes w [rows][K]: tiles of 128 rows x 128 k, tile (mt, kt)
+// at (mt * K/128 + kt) * 16384 bytes, row r's 16-byte chunk c at r*128 + ((c ^ (r & 7)) << 4):
+// the 128-byte-swizzled K-major layout the tensor cores read.  Returns false on a NaN code.
+bool pack_tiled_fp8(const uint8_t* w, size_t rows, size_t K, uint8_t* dst) {
+  bool ok = true;
+  for (size_t n = 0; n < rows; ++n)
+    for (size_t c = 0; c < K / 16; ++c) {
+      const uint8_t* s = w + n * K + 16 * c;
+      for (size_t j = 0; j < 16; ++j) ok &= (s[j] & 0x7F) != 0x7F;
+      uint8_t* tile = dst + ((n / 128) * (K / 128) + c / 8) * 16384;
+      std::memcpy(tile + (n % 128) * 128 + (((c % 8) ^ (n & 7)) << 4), s, 16);
+    }
+  return ok;
+}
+
 }  // namespace
 
 extern "C" {
@@ -153,6 +168,12 @@ int moe_bundle_layout_of(int H, int I, int wdtype, moe_bundle_layout* out) {
     L.down_scale_offset = L.down_offset + 8192;
     L.global_scale_offset = r256(L.down_offset + (h / 128) * (i / 128) * 9216);
     L.total_bytes = r256(L.global_scale_offset + 3 * sizeof(float));
+  } else if (wdtype == MOE_W_FP8_B128) {
+    L.gate_up_offset = 0;
+    L.down_offset = 2 * i * h;
+    L.gate_up_scale_offset = 3 * i * h;
+    L.down_scale_offset = r256(L.gate_up_scale_offset + (2 * i / 128) * (h / 128) * sizeof(float));
+    L.total_bytes = r256(L.down_scale_offset + (h / 128) * (i / 128) * sizeof(float));
   } else {
     return MOE_ERR_INVALID_ARG;
   }
@@ -168,8 +189,8 @@ size_t moe_bundle_bytes(int H, int I, int wdtype) {
 int moe_pack_bundle(int H, int I, int wdtype, const void* wg, const void* wu, const void* wd,
                     const uint16_t* sg, const uint16_t* su, const uint16_t* sd, void* dst) {
   moe_bundle_layout L;
-  if (wdtype == MOE_W_NVFP4 || moe_bundle_layout_of(H, I, wdtype, &L) != MOE_OK || !wg || !wu ||
-      !wd || !dst)
+  if (wdtype == MOE_W_NVFP4 || wdtype == MOE_W_FP8_B128 ||
+      moe_bundle_layout_of(H, I, wdtype, &L) != MOE_OK || !wg || !wu || !wd || !dst)
     return MOE_ERR_INVALID_ARG;
   char* b = static_cast<char*>(dst);
   std::memset(b, 0, L.total_bytes);
@@ -209,6 +230,24 @@ int moe_pack_bundle_nvfp4(int H, int I, const uint8_t* wg, const uint8_t* wu, co
   ok &= pack_tiled_nvfp4(wu, su, h, i, b + L.gate_up_offset + half);
   ok &= pack_tiled_nvfp4(wd, sd, i, h, b + L.down_offset);
   std::memcpy(b + L.global_scale_offset, gs, 3 * sizeof(float));
+  return ok ? MOE_OK : MOE_ERR_INVALID_ARG;
+}
+
+int moe_pack_bundle_fp8(int H, int I, const uint8_t* w_gate_up, const float* s_gate_up,
+                        const uint8_t* w_down, const float* s_down, void* dst) {
+  moe_bundle_layout L;
+  if (moe_bundle_layout_of(H, I, MOE_W_FP8_B128, &L) != MOE_OK || !w_gate_up || !s_gate_up ||
+      !w_down || !s_down || !dst)
+    return MOE_ERR_INVALID_ARG;
+  uint8_t* b = static_cast<uint8_t*>(dst);
+  std::memset(b, 0, L.total_bytes);
+  const size_t h = H, i = I, n_gu = (2 * i / 128) * (h / 128), n_dn = (h / 128) * (i / 128);
+  bool ok = pack_tiled_fp8(w_gate_up, 2 * i, h, b + L.gate_up_offset);
+  ok &= pack_tiled_fp8(w_down, h, i, b + L.down_offset);
+  for (size_t j = 0; j < n_gu; ++j) ok &= std::isfinite(s_gate_up[j]);
+  for (size_t j = 0; j < n_dn; ++j) ok &= std::isfinite(s_down[j]);
+  std::memcpy(b + L.gate_up_scale_offset, s_gate_up, n_gu * sizeof(float));
+  std::memcpy(b + L.down_scale_offset, s_down, n_dn * sizeof(float));
   return ok ? MOE_OK : MOE_ERR_INVALID_ARG;
 }
 

@@ -1,0 +1,71 @@
+// FP8 (E4M3) expert path: host interface and shared device helpers (internal to libmoe).
+//
+// A quantised block of up to 128 values x holds codes q = e4m3(x * (448 / amax)) and the fp32
+// scale s = amax / 448, amax = max(largest |x| of the block, 2^-96): E4M3's largest value is 448,
+// so the block's largest element lands on it, and the floor keeps s a normal number (a block of
+// zeros has zero codes).  A NaN stays a NaN code and does not move its block's scale; an
+// infinity makes s infinite, so its block reads NaN.
+#pragma once
+#include <cuda_fp8.h>
+
+#include "expert_ffn.cuh"
+
+namespace moe {
+
+constexpr int kFp8Block = 128;          // elements per scale
+constexpr float kFp8Max = 448.f;
+constexpr float kFp8MinAmax = 0x1p-96f;
+constexpr int kFp8TileBytes = 16384;    // 128 rows x 128 k
+
+// Four floats times inv -> four E4M3 codes (round to nearest even, saturating).
+__device__ __forceinline__ uint32_t fp8_pack4(float a, float b, float c, float d, float inv) {
+  const uint32_t lo =
+      __nv_cvt_float2_to_fp8x2(make_float2(a * inv, b * inv), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi =
+      __nv_cvt_float2_to_fp8x2(make_float2(c * inv, d * inv), __NV_SATFINITE, __NV_E4M3);
+  return lo | (hi << 16);
+}
+
+inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+inline bool aligned256(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 255u) == 0; }
+
+// One grouped product over FP8 operands:
+//   acc[row][n] = sum_b xs[row][b] ws_e[n / 128][b] sum_{k in block b} xq[row][k] w_e[n][k]
+// fused: w_e = gate rows 0..N-1 and up rows N..2N-1; h = silu(gate) * up is quantised per row
+//        and 128 columns into hq / hs;  else y = acc rounded to bf16, or kept in fp32.
+struct Fp8Args {
+  const uint8_t* xq;          // [max_rows][K] E4M3
+  const float* xs;            // [max_rows][ceil(K / 128)]
+  const int32_t* offsets;     // device [E+1], or NULL: one group of max_rows rows
+  int E, N, K, max_rows;
+  bool fused, y_f32;
+  // weights: bundles (host table or device table) with the section's codes at w_off and its
+  // scales at s_off, or plain row-major w [E][N][K] with ws [E][ceil(N/128)][ceil(K/128)]
+  const BundleTable* tab;
+  const void* const* dev_tab;
+  size_t w_off, s_off;
+  const uint8_t* w;
+  const float* ws;
+  // the experts to run: a device list, a host list (host_n >= 0), or all of them
+  const int32_t* active;
+  const int32_t* n_active;
+  int host_n;
+  const int32_t* host_ids;
+  uint8_t* hq;                // [max_rows][N]
+  float* hs;                  // [max_rows][N / 128]
+  void* y;                    // [max_rows][N] bf16 or fp32
+};
+
+struct Fp8Plan {
+  size_t part_elems, counter_elems;
+};
+
+// counters must be zero on entry and are zero again when the launch has finished
+Fp8Plan plan_fp8(const Fp8Args& a);
+int launch_fp8(const Fp8Args& a, const Fp8Plan& pl, float* part, int32_t* counters, int32_t* err,
+               cudaStream_t st);
+
+int launch_quantize_fp8(const uint16_t* x, const int32_t* src, int rows, int k, int T, int H,
+                        uint8_t* q, float* scale, cudaStream_t st);
+
+}  // namespace moe

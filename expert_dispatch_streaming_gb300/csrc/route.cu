@@ -495,7 +495,7 @@ int launch_route(const RouteArgs& a, const RoutePlan& r, const RouteScratch& s,
       MOE_COUNT_LAUNCH();
       MOE_LAUNCH_CHECK();
     }
-    if (r.small) {
+    if (r.small && !a.n_group) {
       GateParams p{};
       p.part = s.part; p.S = r.S; p.C = r.C; p.ldp = r.C;
       p.x = a.x; p.w_r = a.w_r; p.w_rT = nullptr; p.logit_bias = a.logit_bias;
@@ -529,7 +529,10 @@ int launch_route(const RouteArgs& a, const RoutePlan& r, const RouteScratch& s,
     p.forced = a.forced; p.T = a.T; p.H = a.H; p.E = a.E; p.k = a.k; p.mode = a.gating;
     p.scale = a.scale; p.ids = a.ids; p.w = a.w; p.logits = a.logits;
     p.shared_gate = a.shared_gate; p.tie_flags = a.tie_flags; p.hist = s.hist;
-    if (a.T <= kGateCtaMaxT && (a.E > kGateWarpMaxE || a.T < kGateWarpMinT)) {
+    if (a.n_group) {
+      const int rr = launch_gate_group(p, a.n_group, a.take, st);
+      if (rr != MOE_OK) return rr;
+    } else if (a.T <= kGateCtaMaxT && (a.E > kGateWarpMaxE || a.T < kGateWarpMinT)) {
       const int ctas = std::min(a.T, kGateCtasPerSm * sm_count());
       MOE_LAUNCH_PDL(gate_cta_kernel, dim3(ctas), dim3(kMaxExperts), 0, st, p);
     } else {
@@ -541,8 +544,10 @@ int launch_route(const RouteArgs& a, const RoutePlan& r, const RouteScratch& s,
       else if (a.E <= 128) MOE_LAUNCH_PDL(gate_topk_kernel<4>, grid, block, 0, st, p);
       else MOE_LAUNCH_PDL(gate_topk_kernel<EC>, grid, block, 0, st, p);
     }
-    MOE_COUNT_LAUNCH();
-    MOE_LAUNCH_CHECK();
+    if (!a.n_group) {
+      MOE_COUNT_LAUNCH();
+      MOE_LAUNCH_CHECK();
+    }
   }
   MOE_LAUNCH_PDL(scan_kernel, dim3(1), dim3(kMaxExperts), 0, st, s.hist, r.ntiles, a.E,
                  a.counts, a.offsets, s.base, s.active, s.n_active, s.shared_meta, a.T);

@@ -76,12 +76,16 @@ struct RouteArgs {
   float *w, *logits, *shared_gate;
   uint16_t* x_perm;  // nullable: fused gather into expert order
   int32_t* err;      // device error word (bounded waits of the tensor-core router)
+  int n_group, take; // group-limited selection: `take` of n_group groups; 0 = no groups
 };
 
 RoutePlan plan_route(int T, int H, int E, int k, bool has_gate);
 size_t route_scratch(WsCursor& c, const RoutePlan& r, int T, int E, RouteScratch* out);
 int launch_route(const RouteArgs& a, const RoutePlan& r, const RouteScratch& s,
                  cudaStream_t st);
+// Group-limited gating of p.T tokens (csrc/route_group.cu).
+constexpr int kMaxGroups = 32;
+int launch_gate_group(const GateParams& p, int n_group, int take, cudaStream_t st);
 int launch_gather(const uint16_t* x, const int32_t* src, int rows, int k, int H,
                   uint16_t* x_perm, cudaStream_t st);
 

@@ -108,8 +108,10 @@ enum moe_gating {
 enum moe_wdtype {
   MOE_W_BF16 = 0,      /* bf16 weights                                                   */
   MOE_W_INT4_G128 = 1, /* symmetric INT4 codes + one bf16 scale per 128 reduction elements */
-  MOE_W_NVFP4 = 2      /* NVFP4: FP4 E2M1 codes, one FP8 E4M3 scale per 16 reduction
+  MOE_W_NVFP4 = 2,     /* NVFP4: FP4 E2M1 codes, one FP8 E4M3 scale per 16 reduction
                           elements, one fp32 scale per matrix (gate, up, down)            */
+  MOE_W_FP8_B128 = 3   /* FP8 E4M3 codes, one fp32 scale per 128 x 128 block of weight rows
+                          and reduction elements; multiplied with FP8 activations         */
 };
 
 /* ------------------------------------------------------------------ expert bundles
@@ -146,12 +148,17 @@ enum moe_wdtype {
  *         bits).  The codes are followed by each row's 8 E4M3 block scales (k = 16b..16b+15
  *         of the tile) at 8192 + 8r + b.  The three fp32 matrix scales (gate, up, down)
  *         follow the down section at global_scale_offset.
- *   gate_up_scale_offset / down_scale_offset give the scale block of the section's first tile.
+ *   fp8:  tiles of 128 rows x 128 k (16384 B), one E4M3 code per byte: row r's 16-byte chunk c
+ *         (k = 16c..16c+15 of the tile) at r*128 + ((c ^ (r % 8)) * 16), the same image as bf16
+ *         in bytes.  The fp32 scales follow the down section: gate/up [2I/128][H/128] at
+ *         gate_up_scale_offset, down [H/128][I/128] at down_scale_offset (row tile, k tile).
+ *   gate_up_scale_offset / down_scale_offset give the scale block of the section's first tile
+ *   (INT4, NVFP4) or the section's scale array (FP8).
  * Constraints: H and I multiples of 128.  */
 typedef struct moe_bundle_layout {
   size_t total_bytes;
   size_t gate_up_offset, down_offset;               /* weights or codes               */
-  size_t gate_up_scale_offset, down_scale_offset;   /* INT4 / NVFP4, else 0           */
+  size_t gate_up_scale_offset, down_scale_offset;   /* INT4 / NVFP4 / FP8, else 0     */
   size_t global_scale_offset;                       /* NVFP4: 3 fp32, else 0          */
 } moe_bundle_layout;
 
@@ -185,6 +192,22 @@ int moe_pack_bundle(int H, int I, int wdtype, const void* wg, const void* wu, co
 int moe_pack_bundle_nvfp4(int H, int I, const uint8_t* wg, const uint8_t* wu, const uint8_t* wd,
                           const uint8_t* sg, const uint8_t* su, const uint8_t* sd,
                           const float* gs, void* dst);
+
+/* Packs one FP8 expert into a host bundle `dst` of moe_bundle_bytes(H, I, MOE_W_FP8_B128) bytes.
+ * The weights come as weight rows (see above), the form FP8 checkpoints store them in; a
+ * weight is W[n][k] = E4M3(code) * scale[n / 128][k / 128].
+ *  w_gate_up: [2I][H] E4M3 bytes, rows 0..I-1 gate, I..2I-1 up; s_gate_up: [2I/128][H/128] fp32
+ *  w_down:    [H][I] E4M3 bytes;                                s_down:    [H/128][I/128] fp32
+ * Host only, synchronous.  Returns MOE_ERR_INVALID_ARG on a NaN code (0x7F, 0xFF) or a scale
+ * that is not finite. */
+int moe_pack_bundle_fp8(int H, int I, const uint8_t* w_gate_up, const float* s_gate_up,
+                        const uint8_t* w_down, const float* s_down, void* dst);
+/* The same from device tensors into a device bundle, by kernels on `stream` (asynchronous; for
+ * experts that stay resident).  Pointers 16-byte aligned.  NaN codes and non-finite scales are
+ * copied as they are. */
+int moe_pack_bundle_fp8_device(int H, int I, const uint8_t* w_gate_up, const float* s_gate_up,
+                               const uint8_t* w_down, const float* s_down, void* dst,
+                               void* stream);
 
 /* FNV-1a 64-bit hash of `bytes` bytes of host memory (the checksum expert caches verify). */
 uint64_t moe_checksum64(const void* data, size_t bytes);
@@ -236,6 +259,31 @@ int moe_route_topk(const uint16_t* x, const float* w_r, const float* logit_bias,
                    int32_t* ids, float* w, int32_t* counts, int32_t* offsets, int32_t* pos,
                    int32_t* src, float* logits, float* shared_gate, int32_t* tie_flags,
                    void* ws, size_t ws_bytes, void* stream);
+
+/* moe_route_topk_grouped -- moe_route_topk with group-limited selection.
+ *
+ * The E experts form n_group groups of E / n_group consecutive experts.  With c[e] the selection
+ * score of moe_route_topk (the logit incl. logit_bias; SIGMOID_BIAS_RENORM: sigmoid(logit) +
+ * sel_bias), a token's group score is the sum of the two largest c of the group
+ * (SIGMOID_BIAS_RENORM; the one c of a one-expert group) or the largest c (softmax modes).  The
+ * topk_group groups of largest score are taken, ties to the lower group; the k experts are the
+ * largest c inside them, ties to the lower expert.  Weights, scale, dispatch outputs and their
+ * order are those of moe_route_topk (SOFTMAX normalises over all E experts, taken or not).
+ * A NaN score counts as -infinity.  A token whose chosen experts all have zero weight (every
+ * expert open to it masked by a logit_bias of -infinity) gets weights 0, and still k ids.
+ * Exact selection as in moe_route_topk, for groups and for experts: scores within the fp32
+ * error margin of a boundary are re-scored; tie_flags: 1 = re-scored at either boundary, 2 =
+ * the re-scored gap of either was below 1e-6.
+ * Arguments, outputs and workspace (moe_route_workspace_size(T, H, E, k)) as in moe_route_topk,
+ * without forced ids.
+ * Limits: those of moe_route_topk, 1 <= n_group <= 32 dividing E, 1 <= topk_group <= n_group,
+ * k <= topk_group * E / n_group; MOE_ERR_INVALID_ARG otherwise.  The pages describe no groups. */
+int moe_route_topk_grouped(const uint16_t* x, const float* w_r, const float* logit_bias,
+                           const float* sel_bias, const uint16_t* w_gate, int T, int H, int E,
+                           int k, int n_group, int topk_group, int gating, float scale,
+                           int32_t* ids, float* w, int32_t* counts, int32_t* offsets,
+                           int32_t* pos, int32_t* src, float* logits, float* shared_gate,
+                           int32_t* tie_flags, void* ws, size_t ws_bytes, void* stream);
 
 /* moe_route_topk_static -- moe_route_topk without a workspace, for callers that cannot
  * allocate device memory.  The pages describe no counterpart; it exists for callers such as a
@@ -306,6 +354,62 @@ size_t moe_grouped_swiglu_workspace_size(int max_rows, int E, int H, int I, int 
 int moe_grouped_swiglu(const uint16_t* x_perm, const int32_t* offsets,
                        const void* const* bundles, int E, int H, int I, int wdtype,
                        int max_rows, uint16_t* y_perm, void* ws, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------ FP8 rows and products
+ * FP8 rows: E4M3 codes q [rows][H] (one byte each) with fp32 scales [rows][ceil(H / 128)], the
+ * value being E4M3(q[r][h]) * scale[r][h / 128].
+ *
+ * moe_quantize_fp8 -- quantises bf16 rows, gathering them into expert order on the way when
+ * `src` is given: row p comes from x[src[p] / k], p in [0, T*k) (moe_permute's gather); with
+ * src NULL row p is x[p], p in [0, T), and k is ignored.
+ *  x device [T][H] bf16; src device [T*k] int32 or NULL; q device [rows][H]; scale device
+ *  [rows][ceil(H / 128)] fp32.  H a multiple of 16; x and q 16-byte aligned.
+ * Per row and block of 128 columns (the last one may be shorter), in fp32:
+ *   amax = max(largest |x|, 2^-96), q = e4m3(x * (448 / amax)), scale = amax / 448,
+ * rounded to nearest even.  A NaN becomes a NaN code and leaves its block's scale alone; a block
+ * with an infinity gets an infinite scale and reads NaN.  A row whose src lies outside [0, T*k)
+ * is written as zeros.
+ * "Running 35B MoE Models on 8GB GPUs ...", "Technical Insight" names FP8 checkpoints; the
+ * format is the one DeepSeek-V3-shaped FP8 checkpoints are published in. */
+int moe_quantize_fp8(const uint16_t* x, const int32_t* src, int T, int k, int H, uint8_t* q,
+                     float* scale, void* stream);
+
+/* moe_grouped_gemm_fp8 -- for every expert e with rows [offsets[e], offsets[e+1]):
+ *   y[row][n] = sum over blocks b of 128 k:  x_scale[row][b] * w_scale[e][n / 128][b] *
+ *               sum_{k in b} E4M3(xq[row][k]) * E4M3(w[e][n][k])
+ * with fp32 sums, one block's products summed before its scales are applied.
+ *  xq, x_scale device FP8 rows [max_rows][K] (moe_quantize_fp8)
+ *  w        device [E][N][K] E4M3 (weight rows, as checkpoints store them), w_scale device
+ *           [E][ceil(N/128)][ceil(K/128)] fp32; blocks at the ends of N and K may be shorter
+ *  offsets  device [E+1] int32 (from moe_route_topk), or NULL with E == 1: one dense product of
+ *           max_rows rows
+ *  y        device [max_rows][N], bf16 (out_f32 = 0, rounded once) or fp32 (out_f32 = 1); rows
+ *           outside every expert's range are left as they are
+ *  max_rows upper bound of offsets[E]; ranges reaching outside [0, max_rows) are clipped and
+ *           error 8 is recorded (moe_workspace_error)
+ *  ws       device scratch of moe_grouped_gemm_fp8_workspace_size(max_rows, E, N, K) bytes,
+ *           256-byte aligned
+ * Limits: 1 <= E <= 256, N >= 1, K a multiple of 16; xq, w, y 16-byte aligned.
+ * A NaN or infinite product (NaN codes, infinite scales) reaches the rows it belongs to only. */
+size_t moe_grouped_gemm_fp8_workspace_size(int max_rows, int E, int N, int K);
+int moe_grouped_gemm_fp8(const uint8_t* xq, const float* x_scale, const uint8_t* w,
+                         const float* w_scale, const int32_t* offsets, int E, int N, int K,
+                         int max_rows, int out_f32, void* y, void* ws, size_t ws_bytes,
+                         void* stream);
+
+/* moe_grouped_swiglu_fp8 -- moe_grouped_swiglu on FP8 rows and MOE_W_FP8_B128 bundles: per expert
+ *   h = silu(x Wg) * (x Wu) in fp32, quantised to FP8 rows as moe_quantize_fp8 does (directly
+ *   from fp32), y_perm = bf16(h Wd), both products as in moe_grouped_gemm_fp8.
+ *  xq, x_scale device FP8 rows [max_rows][H] in expert order; offsets device [E+1];
+ *  bundles HOST array [E] of device pointers (NULL allowed for experts without rows);
+ *  y_perm device [max_rows][H] bf16; max_rows, error word and clipping as above;
+ *  ws device scratch of moe_grouped_swiglu_fp8_workspace_size(max_rows, E, H, I) bytes,
+ *  256-byte aligned.
+ * Limits: E <= 256, H and I multiples of 128. */
+size_t moe_grouped_swiglu_fp8_workspace_size(int max_rows, int E, int H, int I);
+int moe_grouped_swiglu_fp8(const uint8_t* xq, const float* x_scale, const int32_t* offsets,
+                           const void* const* bundles, int E, int H, int I, int max_rows,
+                           uint16_t* y_perm, void* ws, size_t ws_bytes, void* stream);
 
 /* ------------------------------------------------------------------ step 6: combine
  * out[t] = bf16( sum_{j<k} w[t][j] * y_perm[pos[t][j]] + g_t * shared[t] ), fp32 inside,
