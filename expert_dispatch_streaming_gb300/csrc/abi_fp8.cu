@@ -15,7 +15,7 @@ namespace {
 
 bool fp8_shape(int E, int N, int K, int max_rows) {
   return E > 0 && E <= kMaxExperts && N > 0 && K > 0 && K % 16 == 0 && max_rows >= 0 &&
-         N <= (1 << 24) && K <= (1 << 24);
+         N <= (1 << 24) && K <= (1 << 24) && (long long)E * N < (1LL << 31);
 }
 
 Fp8Args gemm_args_fp8(int E, int N, int K, int max_rows) {
