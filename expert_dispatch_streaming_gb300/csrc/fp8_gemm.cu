@@ -22,6 +22,7 @@
 //              row-major weight; four stages;
 //   warp 1     MMA issuer: four tcgen05.mma (K = 32 each) per step into one of two 256-column
 //              TMEM buffers;
+//   warp 2     scale factors: xs * ws per token and weight tile of each step, to shared memory;
 //   warps 4-11 two warps per TMEM lane quarter, 64 columns of each weight tile per thread: per
 //              step, tcgen05.ld and a packed fp32 multiply-add by xs * ws into 128 accumulators
 //              (they take the registers warps 0-3 give up).
@@ -42,7 +43,7 @@ namespace moe {
 namespace {
 
 constexpr uint64_t kWaitNs = 2000000000ull;
-constexpr int kStages = 4;
+constexpr int kStages = 3;
 constexpr int kABytes = kFp8TileBytes, kBBytes = 2 * kFp8TileBytes;
 constexpr int kStageBytes = kABytes + kBBytes;
 constexpr int kThreads = 384;
@@ -58,14 +59,19 @@ struct alignas(16) Ctl {
   uint64_t full[kStages], empty[kStages], tfull[2], tempty[2], pair[4];
   uint32_t tmem;
   int last[4];
-  int pref[kMaxExperts + 1];
+  int pref[kMaxExperts + 1];    // tiles before the a-th expert run
+  int row0[kMaxExperts], rows[kMaxExperts], id[kMaxExperts];   // its rows and id
   float amax[2][2][128];
+  float2 f[2][128];             // per TMEM buffer and token: xs * ws of the two weight tiles
 };
-constexpr int kSmem = kStages * kStageBytes + 1024 + (int)sizeof(Ctl);
+// Output rows on their way out: per epilogue warp two boxes of 32 rows x 128 bytes.
+constexpr int kBox = 4096, kOutBytes = 8 * 2 * kBox;
+constexpr int kSmem = kStages * kStageBytes + kOutBytes + 1024 + (int)sizeof(Ctl);
 static_assert(kSmem <= 232448, "over the 227 KB shared-memory limit of a CTA");
 
 struct Fp8Params {
   CUtensorMap tm_x, tm_x32;     // token rows [max_rows][K], boxes of 128 / 32 rows x 128 bytes
+  CUtensorMap tm_out;           // y (or hq): boxes of 32 rows x 128 (hq: 64) bytes
   CUtensorMap tm_w;             // row-major weights [E * N][K], boxes of 128 x 128 bytes
   const float* xs;
   const int32_t* offsets;
@@ -99,33 +105,54 @@ __device__ __forceinline__ uint64_t globaltimer() {
 __device__ __forceinline__ void mbar_init(uint64_t* bar, uint32_t count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(count));
 }
-__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+// One arrival of the warp: lane 0, by predicate (a branch would cost a reconvergence).
+__device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
+  asm volatile(
+      "{\n.reg .pred q;\nsetp.eq.s32 q, %1, 0;\n"
+      "@q mbarrier.arrive.shared::cta.b64 _, [%0];\n}\n" ::"r"(smem_u32(bar)),
+      "r"(lane)
+      : "memory");
 }
 __device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)),
                "r"(bytes)
                : "memory");
 }
-__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
+// One try of lane 0 only, by predicate: 32 lanes polling one barrier are 32 operations on it.
+__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity, int lane) {
   uint32_t ok;
   asm volatile(
-      "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-      "selp.u32 %0, 1, 0, p;\n}\n"
+      "{\n.reg .pred p, q;\nsetp.eq.s32 q, %3, 0;\nsetp.ne.s32 p, 0, 0;\n"
+      "@q mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}\n"
       : "=r"(ok)
-      : "r"(bar), "r"(parity)
+      : "r"(bar), "r"(parity), "r"(lane)
       : "memory");
   return ok != 0;
 }
-// Bounded wait of a converged warp (every lane polls, votes decide: the warp never diverges).
-__device__ __forceinline__ bool warp_wait(uint64_t* b, uint32_t parity, int32_t* err, int code) {
+// The same without suspending the thread, for a look ahead of the wait.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity, int lane) {
+  uint32_t ok;
+  asm volatile(
+      "{\n.reg .pred p, q;\nsetp.eq.s32 q, %3, 0;\nsetp.ne.s32 p, 0, 0;\n"
+      "@q mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity), "r"(lane)
+      : "memory");
+  return ok != 0;
+}
+// Bounded wait of a converged warp (votes decide: the warp never diverges); `early`: the result of
+// a look at this phase already taken, whose latency other work has covered.
+__device__ __forceinline__ bool warp_wait(uint64_t* b, uint32_t parity, int32_t* err, int code,
+                                          bool early = false) {
   const uint32_t bar = smem_u32(b);
-  if (__all_sync(0xffffffffu, mbar_try(bar, parity))) return true;
+  const int lane = threadIdx.x & 31;
+  if (__any_sync(0xffffffffu, early)) return true;
+  if (__any_sync(0xffffffffu, mbar_try(bar, parity, lane))) return true;
   const uint64_t t0 = globaltimer();
   for (uint32_t i = 1;; ++i) {
-    if (__all_sync(0xffffffffu, mbar_try(bar, parity))) return true;
+    if (__any_sync(0xffffffffu, mbar_try(bar, parity, lane))) return true;
     if ((i & 255) == 0 && __any_sync(0xffffffffu, globaltimer() - t0 > kWaitNs)) {
-      if ((threadIdx.x & 31) == 0) atomicExch(err, code);
+      if (lane == 0) atomicExch(err, code);
       return false;
     }
   }
@@ -198,33 +225,21 @@ __device__ __forceinline__ void tmem_ld32_nw(uint32_t taddr, uint32_t (&r)[32]) 
         "=r"(r[31])
       : "r"(taddr));
 }
-// Waits for this thread's TMEM loads; the registers are tied to the wait so that no use of them
-// is scheduled above it.
-__device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.wait::ld.sync.aligned;"
-      : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
-        "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]),
-        "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]),
-        "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
-        "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]),
-        "+r"(r[31])
-      :
-      : "memory");
+__device__ __forceinline__ void tmem_wait_ld() {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
-// acc[2i], acc[2i+1] += v[2i], v[2i+1] times f, as packed fp32 pairs
-__device__ __forceinline__ void fma32(uint64_t* acc, const uint32_t (&v)[32], uint64_t f) {
+// acc[i] += v[i] * f, two at a time (fma.rn.f32x2: one issue slot).  Volatile, as the load and its
+// wait are, so that no use of v moves above the wait.  The pairs are put together inside the
+// asm: accumulators kept as 64-bit values make the compiler copy every operand each step
+// (measured, 128 columns by two warps per scheduler: 613 clocks against 345).
+__device__ __forceinline__ void fma32(float* acc, const uint32_t (&v)[32], uint64_t f) {
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    uint64_t p;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "r"(v[2 * i]), "r"(v[2 * i + 1]));
-    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc[i]) : "l"(p), "l"(f));
-  }
-}
-__device__ __forceinline__ float2 unpack(uint64_t v) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-  return r;
+  for (int i = 0; i < 16; ++i)
+    asm volatile(
+        "{\n.reg .b64 t, a;\nmov.b64 t, {%2, %3};\nmov.b64 a, {%0, %1};\n"
+        "fma.rn.f32x2 a, t, %4, a;\nmov.b64 {%0, %1}, a;\n}\n"
+        : "+f"(acc[2 * i]), "+f"(acc[2 * i + 1])
+        : "r"(v[2 * i]), "r"(v[2 * i + 1]), "l"(f));
 }
 __device__ __forceinline__ uint64_t pack(float a, float b) {
   uint64_t r;
@@ -251,49 +266,156 @@ __device__ __forceinline__ bool expert_rows(const Fp8Params& p, int e, int& r0, 
 
 // The CTA's share of the steps: whole tiles CTA, CTA + G, ... or one range of all tiles' steps.
 struct Walk {
-  int KB, U, G, u, lo, hi;
-  long long pos, end;
+  int KB, U, G, u, lo, hi, left;   // left: steps (cut) still to do
   bool cut;
   __device__ __forceinline__ Walk(int U_, int KB_) : KB(KB_), U(U_), G(gridDim.x) {
     cut = U < kRangeTiles * G;
     const long long W = (long long)U * KB;
     if (cut && W < G) G = (int)W;               // no empty ranges
-    if ((int)blockIdx.x >= G) {
-      pos = end = 0;
-      return;
+    lo = hi = left = 0;
+    u = U;
+    if ((int)blockIdx.x >= G) return;
+    u = blockIdx.x;
+    if (cut) {
+      const long long pos = blockIdx.x * W / G;
+      u = (int)(pos / KB);
+      lo = (int)(pos - (long long)u * KB);
+      left = (int)((blockIdx.x + 1) * W / G - pos);
     }
-    pos = cut ? (long long)blockIdx.x * W / G : (long long)blockIdx.x * KB;
-    end = cut ? (long long)(blockIdx.x + 1) * W / G : W;
+    u -= cut ? 1 : G;                           // next() steps on to the first
+    hi = lo;
   }
   __device__ __forceinline__ bool next() {
-    if (pos >= end) return false;
-    u = (int)(pos / KB);
-    lo = (int)(pos - (long long)u * KB);
-    hi = cut ? (int)min((long long)KB, lo + (end - pos)) : KB;
-    pos += cut ? hi - lo : (long long)G * KB;
-    return true;
+    if (cut) {
+      if (left <= 0) return false;
+      ++u;
+      lo = hi == KB ? 0 : hi;
+      hi = min(KB, lo + left);
+      left -= hi - lo;
+      return true;
+    }
+    u += G;
+    lo = 0;
+    hi = KB;
+    return u < U;
   }
 };
 
 struct Tile {
   int e, nt, r0, rows;
 };
-__device__ __forceinline__ Tile tile_of(const Fp8Params& p, const int* pref, int n_act, int u) {
+__device__ __forceinline__ Tile tile_of(const Ctl& c, int n_act, int u) {
   int lo = 0, hi = n_act - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (pref[mid] <= u) lo = mid;
+    if (c.pref[mid] <= u) lo = mid;
     else hi = mid - 1;
   }
   Tile t;
-  t.e = expert_of(p, lo);
-  int r0, r1;
-  expert_rows(p, t.e, r0, r1);
-  const int mts = (r1 - r0 + 127) >> 7, rem = u - pref[lo];
-  t.nt = rem / mts;
-  t.r0 = r0 + (rem - t.nt * mts) * 128;
-  t.rows = min(128, r1 - t.r0);
+  t.e = c.id[lo];
+  const int n = c.rows[lo], mts = (n + 127) >> 7, rem = u - c.pref[lo];
+  t.nt = mts == 1 ? rem : rem / mts;
+  const int mt = rem - t.nt * mts;
+  t.r0 = c.row0[lo] + mt * 128;
+  t.rows = min(128, n - mt * 128);
   return t;
+}
+
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, int c0, int c1, uint32_t src) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+          reinterpret_cast<uint64_t>(map)),
+      "r"(c0), "r"(c1), "r"(src)
+      : "memory");
+}
+__device__ __forceinline__ void bulk_commit() {
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+// This thread's stores have read their shared memory (all: have also been written).
+__device__ __forceinline__ void bulk_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+}
+__device__ __forceinline__ void bulk_wait_all() {
+  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
+__device__ __forceinline__ void proxy_fence() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// Rows 32 q .. of the tile x 64 columns from `col` on leave from the box `st` (32 rows of kRow
+// bytes, 16-byte piece i of row l at i ^ l's swizzle): one TMA store, which runs while the next
+// tile's steps do, when all 32 rows exist; else coalesced stores of those that do (a box would
+// reach into the next expert's rows).  (Stored from registers, a lane's 16 bytes a time, a tile
+// took 9,000 clocks in which the tensor cores waited; by coalesced stores 4,300; by one bulk copy
+// per row 6,000.)
+template <int kRow>
+__device__ __forceinline__ void store_box(const CUtensorMap* map, uint8_t* dst, size_t pitch,
+                                          const uint8_t* st, int col, int row, int have, int bytes,
+                                          int lane) {
+  constexpr int kPer = kRow / 16;
+  proxy_fence();
+  __syncwarp();
+  if (have >= 32) {
+    if (lane == 0) {
+      tma_store_2d(map, col, row, smem_u32(st));
+      bulk_commit();
+    }
+  } else {
+#pragma unroll 1
+    for (int at = lane; at < have * kPer; at += 32) {
+      const int l = at / kPer, i = at % kPer;
+      if (16 * i < bytes)
+        *reinterpret_cast<uint4*>(dst + l * pitch + 16 * i) = *reinterpret_cast<const uint4*>(
+            st + l * kRow + ((i ^ (kRow == 128 ? l % 8 : (l >> 1) % 4)) << 4));
+    }
+  }
+}
+
+// A warp's 32 rows of y: 64 columns of the tile's first weight block (acc[0..63]) and 64 of the
+// second, through its two boxes.  Rows that are not 16-byte aligned are stored element by
+// element, the lanes side by side along one row after another.
+template <bool F32>
+__device__ __forceinline__ void store_y(const Fp8Params& p, uint8_t* box, const float (&acc)[128],
+                                        int row, int n0, int half, int have, int lane) {
+  constexpr int kElem = F32 ? 4 : 2, kCols = 128 / kElem;   // columns of a box
+  const bool vec = (p.N * kElem) % 16 == 0;
+  const size_t pitch = (size_t)p.N * kElem;
+#pragma unroll
+  for (int b = 0; b < 128 / kCols; ++b) {
+    const int c0 = b * kCols, w = c0 / 64, col = n0 + 128 * w + 64 * half + c0 % 64;
+    uint8_t* st = box + (b & 1) * kBox;
+    if ((b & 1) == 0) {                       // both boxes free again
+      if (lane == 0) bulk_wait_read();
+      __syncwarp();
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float* v = acc + c0 + i * (16 / kElem);
+      const uint4 o =
+          F32 ? make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                           __float_as_uint(v[3]))
+              : make_uint4(float2_to_bf16x2(v[0], v[1]), float2_to_bf16x2(v[2], v[3]),
+                           float2_to_bf16x2(v[F32 ? 0 : 4], v[F32 ? 0 : 5]),
+                           float2_to_bf16x2(v[F32 ? 0 : 6], v[F32 ? 0 : 7]));
+      *reinterpret_cast<uint4*>(st + lane * 128 + ((i ^ (lane & 7)) << 4)) = o;
+    }
+    const int left = min(kCols, p.N - col);   // columns of these that exist
+    uint8_t* y = static_cast<uint8_t*>(p.y) + row * pitch + (size_t)col * kElem;
+    if (left <= 0) continue;
+    if (vec) {
+      store_box<128>(&p.tm_out, y, pitch, st, col, row, have, left * kElem, lane);
+    } else {
+      __syncwarp();
+#pragma unroll 1
+      for (int l = 0; l < min(have, 32); ++l)
+        for (int k = lane; k < left; k += 32) {
+          const uint8_t* e = st + l * 128 + (((k * kElem / 16) ^ (l & 7)) << 4) + k * kElem % 16;
+          if (F32) reinterpret_cast<float*>(y + l * pitch)[k] = *reinterpret_cast<const float*>(e);
+          else reinterpret_cast<uint16_t*>(y + l * pitch)[k] = *reinterpret_cast<const uint16_t*>(e);
+        }
+    }
+  }
+  __syncwarp();
 }
 
 // FUSED: N = columns of h (gate rows 0..N-1, up rows N..2N-1).  PLAIN: row-major weights by TMA.
@@ -302,7 +424,8 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
-  Ctl& c = *reinterpret_cast<Ctl*>(smem + kStages * kStageBytes);
+  uint8_t* out = smem + kStages * kStageBytes;
+  Ctl& c = *reinterpret_cast<Ctl*>(out + kOutBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_trigger();
   if (threadIdx.x == 0) {
@@ -311,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
       mbar_init(&c.empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
-      mbar_init(&c.tfull[b], 1);
+      mbar_init(&c.tfull[b], 2);   // the MMAs and the factors
       mbar_init(&c.tempty[b], 8);
     }
     for (int q = 0; q < 4; ++q) mbar_init(&c.pair[q], 2);
@@ -333,8 +456,12 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
       int cnt = 0;
       if (a < n_act) {
         int r0, r1;
-        if (expert_rows(p, expert_of(p, a), r0, r1)) atomicExch(p.err, 8);
+        const int e = expert_of(p, a);
+        if (expert_rows(p, e, r0, r1)) atomicExch(p.err, 8);
         cnt = p.NT * ((r1 - r0 + 127) >> 7);
+        c.row0[a] = r0;
+        c.rows[a] = r1 - r0;
+        c.id[a] = e;
       }
       int incl = cnt;
 #pragma unroll
@@ -361,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
     uint32_t phase = 0;
     bool ok = true;
     while (ok && wk.next()) {
-      const Tile t = tile_of(p, c.pref, n_act, wk.u);
+      const Tile t = tile_of(c, n_act, wk.u);
       const int nsub = t.rows > 96 ? 0 : (t.rows + 31) >> 5;
       const int n0 = t.nt * (FUSED ? 128 : 256);
       const bool two = FUSED || n0 + 128 < p.N;
@@ -399,52 +526,51 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
+    // always 256 columns, so that it needs nothing of a tile but its steps (where a tile has one
+    // weight tile only, the second's columns take what the stage held and are not stored)
+    const uint32_t idesc = idesc_e4m3(128, kAccCols);
     int stage = 0, buf = 0;
     uint32_t phase = 0, tphase = 0;
-    bool ok = true;
+    bool ok = true, e1 = false, e2 = false;
     while (ok && wk.next()) {
-      const Tile t = tile_of(p, c.pref, n_act, wk.u);
-      const int left = FUSED ? 256 : p.N - t.nt * 256;
-      const uint32_t idesc = idesc_e4m3(128, min(256, (left + 15) & ~15));
       for (int kb = wk.lo; kb < wk.hi; ++kb) {
-        if (!(ok = warp_wait(&c.tempty[buf], tphase ^ 1, p.err, 2))) break;
-        if (!(ok = warp_wait(&c.full[stage], phase, p.err, 3))) break;
+        if (!(ok = warp_wait(&c.tempty[buf], tphase ^ 1, p.err, 2, e1))) break;
+        if (!(ok = warp_wait(&c.full[stage], phase, p.err, 3, e2))) break;
         const uint32_t sa = smem_u32(smem + stage * kStageBytes);
         const uint64_t da = sdesc_sw128(sa), db = sdesc_sw128(sa + kABytes);
-        if (elect_one()) {
-          tc_fence_after();
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            mma_fp8(tmem + buf * kAccCols, da + 2 * j, db + 2 * j, idesc, j > 0);
-          mma_commit(&c.empty[stage]);
-          mma_commit(&c.tfull[buf]);
-        }
-        __syncwarp();
+        const uint32_t d = tmem + buf * kAccCols;
+        uint64_t *eb = &c.empty[stage], *tb = &c.tfull[buf];
         if (++stage == kStages) { stage = 0; phase ^= 1; }
         buf ^= 1;
         if (buf == 0) tphase ^= 1;
+        if (elect_one()) {
+          tc_fence_after();
+#pragma unroll
+          for (int j = 0; j < 3; ++j) mma_fp8(d, da + 2 * j, db + 2 * j, idesc, j > 0);
+        }
+        // the next step's barriers are looked at while these run: an issue waits for the one
+        // before it to start, so the pipe would drain during a look after the last one
+        e1 = mbar_test(&c.tempty[buf], tphase ^ 1, lane);
+        e2 = mbar_test(&c.full[stage], phase, lane);
+        if (elect_one()) {
+          mma_fp8(d, da + 6, db + 6, idesc, 1);
+          mma_commit(eb);
+          mma_commit(tb);
+        }
+        __syncwarp();
       }
     }
-  } else if (warp >= 4) {
-    // ------------------------------------------------------------ scaling and epilogue
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsHigh));
-    const int q = warp & 3, half = (warp - 4) >> 2, r = q * 32 + lane;
-    int buf = 0, flip = 0;
-    uint32_t tphase = 0, pphase = 0;
+  } else if (warp == 2) {
+    // ------------------------------------------------------------ scale factors
+    // per step: xs * ws of every token and weight tile into the TMEM buffer's slot; the loads
+    // of a step are issued while its buffer is still in use
+    int buf = 0;
+    uint32_t tphase = 0;
     bool ok = true;
-    // the two warps of a lane quarter meet (bounded, as every wait)
-    auto meet = [&]() -> bool {
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&c.pair[q]);
-      const bool w = warp_wait(&c.pair[q], pphase, p.err, 5);
-      pphase ^= 1;
-      return w;
-    };
     while (ok && wk.next()) {
-      const Tile t = tile_of(p, c.pref, n_act, wk.u);
-      const int n0 = t.nt * (FUSED ? 128 : 256);
-      const bool two = FUSED || n0 + 128 < p.N, here = q * 32 < t.rows, mine = r < t.rows;
-      const int NB = (p.N + 127) >> 7;
+      const Tile t = tile_of(c, n_act, wk.u);
+      const int n0 = t.nt * (FUSED ? 128 : 256), NB = (p.N + 127) >> 7;
+      const bool two = FUSED || n0 + 128 < p.N;
       const float* sw0;
       if (PLAIN) {
         sw0 = p.ws + ((size_t)t.e * NB + (n0 >> 7)) * KB;
@@ -453,47 +579,88 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
         sw0 = reinterpret_cast<const float*>(b + p.s_off) + (size_t)(n0 >> 7) * KB;
       }
       const float* sw1 = two ? sw0 + (size_t)(FUSED ? NB : 1) * KB : sw0;
-      const float* sx = p.xs + (size_t)(t.r0 + (mine ? r : 0)) * KB;
-      uint64_t acc[64];   // pairs of columns: 32 of the first weight tile, 32 of the second
-#pragma unroll
-      for (int i = 0; i < 64; ++i) acc[i] = 0;
-      float x = __ldg(sx + wk.lo), a = __ldg(sw0 + wk.lo), b = __ldg(sw1 + wk.lo);
+      const float* sx = p.xs + (size_t)(t.r0 + lane) * KB;
+      const size_t step = (size_t)32 * KB;
       for (int kb = wk.lo; kb < wk.hi; ++kb) {
-        const float f0 = x * a, f1 = x * b;
-        if (kb + 1 < wk.hi) {
-          x = __ldg(sx + kb + 1);
-          a = __ldg(sw0 + kb + 1);
-          b = __ldg(sw1 + kb + 1);
-        }
-        if (!(ok = warp_wait(&c.tfull[buf], tphase, p.err, 4))) break;
-        if (here) {
-          tc_fence_after();
-          const uint32_t ta = tmem + ((uint32_t)(q * 32) << 16) + buf * kAccCols + half * 64;
-          uint32_t v[32], v2[32];
-          tmem_ld32_nw(ta, v);
-          tmem_wait_ld(v);
-          tmem_ld32_nw(ta + 32, v2);
-          const uint64_t p0 = pack(f0, f0), p1 = pack(f1, f1);
-          fma32(acc, v, p0);
-          tmem_wait_ld(v2);
-          if (two) tmem_ld32_nw(ta + 128, v);
-          fma32(acc + 16, v2, p0);
-          if (two) {
-            tmem_wait_ld(v);
-            tmem_ld32_nw(ta + 160, v2);
-            fma32(acc + 32, v, p1);
-            tmem_wait_ld(v2);
-            fma32(acc + 48, v2, p1);
-          }
-          tc_fence_before();
-          __syncwarp();
-        }
-        if (lane == 0) mbar_arrive(&c.tempty[buf]);
+        const float a = __ldg(sw0 + kb), b = __ldg(sw1 + kb);
+        float x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = lane + 32 * i < t.rows ? __ldg(sx + i * step + kb) : 0.f;
+        if (!(ok = warp_wait(&c.tempty[buf], tphase ^ 1, p.err, 6))) break;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c.f[buf][lane + 32 * i] = make_float2(x[i] * a, x[i] * b);
+        __syncwarp();
+        warp_arrive(&c.tfull[buf], lane);
         buf ^= 1;
         if (buf == 0) tphase ^= 1;
       }
+    }
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------ scaling and epilogue
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsHigh));
+    const int q = warp & 3, half = (warp - 4) >> 2, r = q * 32 + lane;
+    uint8_t* box = out + (warp - 4) * 2 * kBox;
+    int buf = 0, flip = 0;
+    uint32_t tphase = 0, pphase = 0;
+    bool ok = true;
+    // the two warps of a lane quarter meet (bounded, as every wait)
+    auto meet = [&]() -> bool {
+      __syncwarp();
+      warp_arrive(&c.pair[q], lane);
+      const bool w = warp_wait(&c.pair[q], pphase, p.err, 5);
+      pphase ^= 1;
+      return w;
+    };
+    while (ok && wk.next()) {
+      const Tile t = tile_of(c, n_act, wk.u);
+      const int n0 = t.nt * (FUSED ? 128 : 256);
+      const bool here = q * 32 < t.rows, mine = r < t.rows;
+      const int NB = (p.N + 127) >> 7;
+      float acc[128];   // 64 columns of the first weight tile, 64 of the second
+#pragma unroll
+      for (int i = 0; i < 128; ++i) acc[i] = 0.f;
+      if (!here) {
+        // no token of the tile on this warp's lanes: only pass the buffers on
+        for (int kb = wk.lo; kb < wk.hi; ++kb) {
+          if (!(ok = warp_wait(&c.tfull[buf], tphase, p.err, 4))) break;
+          warp_arrive(&c.tempty[buf], lane);
+          buf ^= 1;
+          if (buf == 0) tphase ^= 1;
+        }
+        continue;
+      }
+      bool early = false;
+      for (int kb = wk.lo; kb < wk.hi; ++kb) {
+        if (!(ok = warp_wait(&c.tfull[buf], tphase, p.err, 4, early))) break;
+        tc_fence_after();
+        const uint32_t ta = tmem + ((uint32_t)(q * 32) << 16) + buf * kAccCols + half * 64;
+        // straight-line: a condition around any part of it makes the compiler copy the
+        // accumulators every step.  (A missing second weight tile leaves old values in its
+        // columns, which are never stored.)  A chunk's load is in flight while the chunk before it
+        // is added; the buffer is handed back, and the next one tried, before the last chunk is.
+        uint32_t v[32], v2[32];
+        tmem_ld32_nw(ta, v);
+        const float2 f = c.f[buf][r];
+        const uint64_t f0 = pack(f.x, f.x), f1 = pack(f.y, f.y);
+        tmem_wait_ld();
+        tmem_ld32_nw(ta + 32, v2);
+        fma32(acc, v, f0);
+        tmem_wait_ld();
+        tmem_ld32_nw(ta + 128, v);
+        fma32(acc + 32, v2, f0);
+        tmem_wait_ld();
+        tmem_ld32_nw(ta + 160, v2);
+        fma32(acc + 64, v, f1);
+        tmem_wait_ld();
+        tc_fence_before();
+        __syncwarp();
+        warp_arrive(&c.tempty[buf], lane);
+        buf ^= 1;
+        if (buf == 0) tphase ^= 1;
+        early = mbar_test(&c.tfull[buf], tphase, lane);
+        fma32(acc + 96, v2, f1);
+      }
       if (!ok) break;
-      if (!here) continue;
       if (wk.lo > 0 || wk.hi < KB) {
         // a piece of the tile: its sums to this CTA's slot (0: begins inside the tile, 1: ends
         // inside it); the last piece's CTA adds them all in range order
@@ -502,10 +669,9 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
                     (size_t)r * 256 + half * 128;
         if (mine) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const float2 u0 = unpack(acc[2 * i]), u1 = unpack(acc[2 * i + 1]);
-            __stcg(reinterpret_cast<float4*>(mp) + i, make_float4(u0.x, u0.y, u1.x, u1.y));
-          }
+          for (int i = 0; i < 32; ++i)
+            __stcg(reinterpret_cast<float4*>(mp) + i,
+                   make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]));
         }
         const long long W = (long long)U * KB, first = (long long)wk.u * KB;
         const int c_lo = (int)(((first + 1) * wk.G - 1) / W);
@@ -523,7 +689,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
         if (!c.last[q]) continue;
         __threadfence();
 #pragma unroll
-        for (int i = 0; i < 64; ++i) acc[i] = 0;
+        for (int i = 0; i < 128; ++i) acc[i] = 0.f;
         if (mine) {
           for (int cc = c_lo; cc <= c_hi; ++cc) {
             const bool inside = (long long)cc * W / wk.G > first;
@@ -532,88 +698,52 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
               const float4 o = __ldcg(op + i);
-              const float2 u0 = unpack(acc[2 * i]), u1 = unpack(acc[2 * i + 1]);
-              acc[2 * i] = pack(u0.x + o.x, u0.y + o.y);
-              acc[2 * i + 1] = pack(u1.x + o.z, u1.y + o.w);
+              acc[4 * i] += o.x;
+              acc[4 * i + 1] += o.y;
+              acc[4 * i + 2] += o.z;
+              acc[4 * i + 3] += o.w;
             }
           }
         }
       }
-      const size_t row = (size_t)t.r0 + r;
+      const size_t row0 = (size_t)t.r0 + q * 32;     // the warp's first row, and how many exist
+      const int have = t.rows - q * 32;
       if (FUSED) {
-        // h over the gate pairs; the row's largest |h| over both warps' 64 columns
+        // h over the gate sums; the row's largest |h| over both warps' 64 columns
         float m = 0.f;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const float2 g = unpack(acc[i]), u = unpack(acc[32 + i]);
-          const float h0 = silu_mul(g.x, u.x), h1 = silu_mul(g.y, u.y);
-          m = fmaxf(m, fmaxf(fabsf(h0), fabsf(h1)));
-          acc[i] = pack(h0, h1);
+        for (int i = 0; i < 64; ++i) {
+          acc[i] = silu_mul(acc[i], acc[64 + i]);
+          m = fmaxf(m, fabsf(acc[i]));
         }
         c.amax[flip][half][r] = m;
         if (!(ok = meet())) break;
         m = fmaxf(fmaxf(m, c.amax[flip][half ^ 1][r]), kFp8MinAmax);
         flip ^= 1;
-        if (mine) {
-          const float inv = __fdiv_rn(kFp8Max, m);
-          uint4* dst = reinterpret_cast<uint4*>(p.hq + row * p.N + n0 + half * 64);
+        const float inv = __fdiv_rn(kFp8Max, m);
+        if (lane == 0) bulk_wait_read();
+        __syncwarp();
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t o[4];
+        for (int i = 0; i < 4; ++i) {
+          uint32_t o[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float2 u0 = unpack(acc[8 * i + 2 * j]), u1 = unpack(acc[8 * i + 2 * j + 1]);
-              o[j] = fp8_pack4(u0.x, u0.y, u1.x, u1.y, inv);
-            }
-            dst[i] = make_uint4(o[0], o[1], o[2], o[3]);
+          for (int j = 0; j < 4; ++j) {
+            const float* h = acc + 16 * i + 4 * j;
+            o[j] = fp8_pack4(h[0], h[1], h[2], h[3], inv);
           }
-          if (half == 0) p.hs[row * NB + (n0 >> 7)] = __fdiv_rn(m, kFp8Max);
+          *reinterpret_cast<uint4*>(box + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4)) =
+              make_uint4(o[0], o[1], o[2], o[3]);
         }
-      } else if (mine) {
-#pragma unroll
-        for (int w = 0; w < 2; ++w) {
-          const int col = n0 + 128 * w + 64 * half;
-          const int left = p.N - col;             // columns from `col` on
-          const size_t at = row * p.N + col;
-          if (p.y_f32) {
-            float* y = static_cast<float*>(p.y) + at;
-            const bool vec = (p.N & 3) == 0;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float2 u0 = unpack(acc[32 * w + 2 * i]), u1 = unpack(acc[32 * w + 2 * i + 1]);
-              if (vec) {
-                if (4 * i < left)
-                  reinterpret_cast<float4*>(y)[i] = make_float4(u0.x, u0.y, u1.x, u1.y);
-              } else {
-                if (4 * i < left) y[4 * i] = u0.x;
-                if (4 * i + 1 < left) y[4 * i + 1] = u0.y;
-                if (4 * i + 2 < left) y[4 * i + 2] = u1.x;
-                if (4 * i + 3 < left) y[4 * i + 3] = u1.y;
-              }
-            }
-          } else {
-            uint16_t* y = static_cast<uint16_t*>(p.y) + at;
-            const bool vec = (p.N & 7) == 0;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              uint32_t o[4];
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const float2 u = unpack(acc[32 * w + 4 * i + j]);
-                o[j] = float2_to_bf16x2(u.x, u.y);
-              }
-              if (vec) {
-                if (8 * i < left) reinterpret_cast<uint4*>(y)[i] = make_uint4(o[0], o[1], o[2], o[3]);
-              } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                  if (8 * i + j < left) y[8 * i + j] = (uint16_t)(o[j >> 1] >> (16 * (j & 1)));
-              }
-            }
-          }
-        }
+        const int col = n0 + half * 64;
+        store_box<64>(&p.tm_out, p.hq + row0 * p.N + col, p.N, box, col, (int)row0, have, 64, lane);
+        __syncwarp();
+        if (mine && half == 0) p.hs[(row0 + lane) * NB + (n0 >> 7)] = __fdiv_rn(m, kFp8Max);
+      } else {
+        if (p.y_f32) store_y<true>(p, box, acc, (int)row0, n0, half, have, lane);
+        else store_y<false>(p, box, acc, (int)row0, n0, half, have, lane);
       }
     }
+    if (lane == 0) bulk_wait_all();
   }
 
   tc_fence_before();
@@ -639,16 +769,22 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 }
 
 // Map of byte rows [rows][K] with boxes of box_rows x 128 bytes, 128-byte swizzle; reads past K
-// or the last row give zeros.
-bool encode_rows(CUtensorMap* m, const uint8_t* base, int K, size_t rows, int box_rows) {
+// or the last row give zeros, writes there are dropped.  elem: bytes of an element (what
+// coordinates count in); box_bytes = 64: 64-byte rows and swizzle.
+bool encode_rows(CUtensorMap* m, const void* base, size_t K, size_t rows, int box_rows,
+                 int elem = 1, int box_bytes = 128) {
   auto enc = encode_fn();
   if (!enc) return false;
   cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows};
-  cuuint64_t strides[1] = {(cuuint64_t)K};
-  cuuint32_t box[2] = {128, (cuuint32_t)box_rows};
+  cuuint64_t strides[1] = {(cuuint64_t)(K * elem)};
+  cuuint32_t box[2] = {(cuuint32_t)(box_bytes / elem), (cuuint32_t)box_rows};
   cuuint32_t estr[2] = {1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(base), dims, strides, box,
-             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+  return enc(m,
+             elem == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                       : elem == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                   : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
+             2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             box_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
          CUDA_SUCCESS;
 }
@@ -685,6 +821,10 @@ int launch_fp8(const Fp8Args& a, const Fp8Plan&, float* part, int32_t* counters,
   if (!encode_rows(&p.tm_x, a.xq, a.K, a.max_rows, 128) ||
       !encode_rows(&p.tm_x32, a.xq, a.K, a.max_rows, 32) ||
       (a.w && !encode_rows(&p.tm_w, a.w, a.K, (size_t)a.E * a.N, 128)))
+    return MOE_ERR_INVALID_ARG;
+  const int elem = a.fused ? 1 : a.y_f32 ? 4 : 2;
+  if ((size_t)a.N * elem % 16 == 0 &&
+      !encode_rows(&p.tm_out, a.fused ? a.hq : a.y, a.N, a.max_rows, 32, elem, a.fused ? 64 : 128))
     return MOE_ERR_INVALID_ARG;
   p.xs = a.xs; p.offsets = a.offsets; p.E = a.E; p.N = a.N; p.K = a.K;
   p.KB = ceil_div(a.K, 128); p.NT = a.fused ? a.N / 128 : ceil_div(a.N, 256);
