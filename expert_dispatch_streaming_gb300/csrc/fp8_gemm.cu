@@ -20,8 +20,8 @@
 //              not full in boxes of 32 rows) and 32 KB of weights: two bundle tiles by bulk copy
 //              (each is stored as its swizzled shared-memory image), or two TMA boxes of a
 //              row-major weight; four stages;
-//   warp 1     MMA issuer: four tcgen05.mma (K = 32 each) per step into one of two 256-column
-//              TMEM buffers;
+//   warps 1, 3 MMA issuers, one per 256-column TMEM buffer: four tcgen05.mma (K = 32 each) per
+//              step, the steps in turn;
 //   warp 2     scale factors: xs * ws per token and weight tile of each step, to shared memory;
 //   warps 4-11 two warps per TMEM lane quarter, 64 columns of each weight tile per thread: per
 //              step, tcgen05.ld and a packed fp32 multiply-add by xs * ws into 128 accumulators
@@ -56,7 +56,7 @@ constexpr int kAccCols = 256, kTmemCols = 512;
 constexpr int kRangeTiles = 4;
 
 struct alignas(16) Ctl {
-  uint64_t full[kStages], empty[kStages], tfull[2], tempty[2], pair[4];
+  uint64_t full[kStages], empty[kStages], tfull[2], tempty[2], pair[4], drain[2];
   uint32_t tmem;
   int last[4];
   int pref[kMaxExperts + 1];    // tiles before the a-th expert run
@@ -67,6 +67,7 @@ struct alignas(16) Ctl {
 // Output rows on their way out: per epilogue warp two boxes of 32 rows x 128 bytes.
 constexpr int kBox = 4096, kOutBytes = 8 * 2 * kBox;
 constexpr int kSmem = kStages * kStageBytes + kOutBytes + 1024 + (int)sizeof(Ctl);
+static_assert(kStages == 3, "the MMA issuers' order of waits covers a stage's use three steps back");
 static_assert(kSmem <= 232448, "over the 227 KB shared-memory limit of a CTA");
 
 struct Fp8Params {
@@ -438,6 +439,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
       mbar_init(&c.tempty[b], 8);
     }
     for (int q = 0; q < 4; ++q) mbar_init(&c.pair[q], 2);
+    for (int b = 0; b < 2; ++b) mbar_init(&c.drain[b], 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) {
@@ -484,7 +486,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
   if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLow));
   if (warp == 0) {
     // ------------------------------------------------------------ producer
-    int stage = 0;
+    int stage = 0, issued = 0;
     uint32_t phase = 0;
     bool ok = true;
     while (ok && wk.next()) {
@@ -522,43 +524,55 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
         }
         __syncwarp();
         if (++stage == kStages) { stage = 0; phase ^= 1; }
+        ++issued;
       }
     }
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer
-    // always 256 columns, so that it needs nothing of a tile but its steps (where a tile has one
-    // weight tile only, the second's columns take what the stage held and are not stored)
+    // after a failed wait, copies may still be on their way to this CTA's shared memory: wait
+    // (bounded) for the last of each stage
+    for (int i = 0; !ok && i < min(issued, kStages); ++i) {
+      if (--stage < 0) { stage = kStages - 1; phase ^= 1; }
+      warp_wait(&c.full[stage], phase, p.err, 1);
+    }
+  } else if (warp == 1 || warp == 3) {
+    // ------------------------------------------------------------ MMA issuers
+    // warp 1 takes the even steps (TMEM buffer 0), warp 3 the odd ones (buffer 1): an issuer's
+    // waits and loop run while the other's products do.  Always 256 columns, so that nothing of
+    // a tile is needed but its steps (where a tile has one weight tile only, the second's
+    // columns take what the stage held and are not stored).
     const uint32_t idesc = idesc_e4m3(128, kAccCols);
-    int stage = 0, buf = 0;
+    const int buf = warp >> 1;
+    const uint32_t d = tmem + buf * kAccCols;
+    int stage = 0, turn = 0;
     uint32_t phase = 0, tphase = 0;
-    bool ok = true, e1 = false, e2 = false;
+    bool ok = true;
     while (ok && wk.next()) {
-      for (int kb = wk.lo; kb < wk.hi; ++kb) {
-        if (!(ok = warp_wait(&c.tempty[buf], tphase ^ 1, p.err, 2, e1))) break;
-        if (!(ok = warp_wait(&c.full[stage], phase, p.err, 3, e2))) break;
-        const uint32_t sa = smem_u32(smem + stage * kStageBytes);
-        const uint64_t da = sdesc_sw128(sa), db = sdesc_sw128(sa + kABytes);
-        const uint32_t d = tmem + buf * kAccCols;
-        uint64_t *eb = &c.empty[stage], *tb = &c.tfull[buf];
-        if (++stage == kStages) { stage = 0; phase ^= 1; }
-        buf ^= 1;
-        if (buf == 0) tphase ^= 1;
-        if (elect_one()) {
-          tc_fence_after();
+      for (int kb = wk.lo; kb < wk.hi; ++kb, turn ^= 1) {
+        if (turn == buf) {
+          // In this order: once the buffer is back, step s - 2 has been through the epilogue, and
+          // so has s - 3, the stage's last use, which the other issuer waited for.  Looked at
+          // before that, the stage's barrier may still be two phases behind, where its parity
+          // reads as complete.
+          if (!(ok = warp_wait(&c.tempty[buf], tphase ^ 1, p.err, 2))) break;
+          if (!(ok = warp_wait(&c.full[stage], phase, p.err, 3))) break;
+          const uint32_t sa = smem_u32(smem + stage * kStageBytes);
+          const uint64_t da = sdesc_sw128(sa), db = sdesc_sw128(sa + kABytes);
+          if (elect_one()) {
+            tc_fence_after();
 #pragma unroll
-          for (int j = 0; j < 3; ++j) mma_fp8(d, da + 2 * j, db + 2 * j, idesc, j > 0);
+            for (int j = 0; j < 4; ++j) mma_fp8(d, da + 2 * j, db + 2 * j, idesc, j > 0);
+            mma_commit(&c.empty[stage]);
+            mma_commit(&c.tfull[buf]);
+          }
+          __syncwarp();
+          tphase ^= 1;
         }
-        // the next step's barriers are looked at while these run: an issue waits for the one
-        // before it to start, so the pipe would drain during a look after the last one
-        e1 = mbar_test(&c.tempty[buf], tphase ^ 1, lane);
-        e2 = mbar_test(&c.full[stage], phase, lane);
-        if (elect_one()) {
-          mma_fp8(d, da + 6, db + 6, idesc, 1);
-          mma_commit(eb);
-          mma_commit(tb);
-        }
-        __syncwarp();
+        if (++stage == kStages) { stage = 0; phase ^= 1; }
       }
+    }
+    if (!ok) {   // after a failed wait: the products still running write TMEM until they end
+      if (elect_one()) mma_commit(&c.drain[buf]);
+      __syncwarp();
+      warp_wait(&c.drain[buf], 0, p.err, 7);
     }
   } else if (warp == 2) {
     // ------------------------------------------------------------ scale factors
