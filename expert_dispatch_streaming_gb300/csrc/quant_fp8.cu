@@ -5,37 +5,71 @@
 namespace moe {
 namespace {
 
-// One warp per row and 128-column block: a lane holds four columns.
+// A lane holds 16 consecutive columns (two 16-byte loads, one 16-byte store), eight lanes a block,
+// a warp 512 columns at a time; a warp takes one row's kCols columns, both halves' loads in
+// flight together.  Bound by memory: 2 bytes in (gathered rows mostly from L2: the codes are
+// stored with a streaming hint so that they do not push x out of it) and 1 byte out per value.
+// The largest magnitude of bf16 values is taken in bf16, which is exact and skips NaNs.
+constexpr int kCols = 1024;
+
+__device__ __forceinline__ uint32_t abs_max2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a & 0x7FFF7FFFu), "r"(b & 0x7FFF7FFFu));
+  return d;
+}
+
 __global__ void __launch_bounds__(256)
 quantize_fp8_kernel(const uint16_t* __restrict__ x, const int32_t* __restrict__ src, int rows,
                     int k, int T, int H, int nb, uint8_t* __restrict__ q,
                     float* __restrict__ scale) {
   pdl_trigger();
   pdl_wait();
+  const int parts = (H + kCols - 1) / kCols;
   const long long item = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
   const int lane = threadIdx.x & 31;
-  if (item >= (long long)rows * nb) return;
-  const int row = (int)(item / nb), b = (int)(item % nb), col = b * kFp8Block + 4 * lane;
+  if (item >= (long long)rows * parts) return;
+  const int row = (int)(item / parts), c0 = (int)(item % parts) * kCols + 16 * lane;
   int from = row;
   if (src) {
-    const int s = src[row];
+    const int s = __ldg(src + row);
     from = s >= 0 && s < T * k ? s / k : -1;   // outside [0, T k): a row of zeros
   }
-  float v[4] = {0.f, 0.f, 0.f, 0.f};
-  if (from >= 0 && col < H) {
-    const uint2 w = *reinterpret_cast<const uint2*>(x + (size_t)from * H + col);
-    const float2 a = bf16x2_to_float2(w.x), c = bf16x2_to_float2(w.y);
-    v[0] = a.x; v[1] = a.y; v[2] = c.x; v[3] = c.y;
-  }
-  float m = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
+  uint4 v[2][2];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  m = fmaxf(m, kFp8MinAmax);
-  const float inv = __fdiv_rn(kFp8Max, m);
-  if (col < H)
-    *reinterpret_cast<uint32_t*>(q + (size_t)row * H + col) =
-        fp8_pack4(v[0], v[1], v[2], v[3], inv);
-  if (lane == 0) scale[(size_t)row * nb + b] = __fdiv_rn(m, kFp8Max);
+  for (int h = 0; h < 2; ++h) {
+    const int col = c0 + 512 * h;
+    v[h][0] = v[h][1] = make_uint4(0u, 0u, 0u, 0u);
+    if (from >= 0 && col < H) {
+      const uint4* p = reinterpret_cast<const uint4*>(x + (size_t)from * H + col);
+      v[h][0] = __ldg(p);
+      v[h][1] = __ldg(p + 1);
+    }
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int col = c0 + 512 * h;
+    const uint32_t w[8] = {v[h][0].x, v[h][0].y, v[h][0].z, v[h][0].w,
+                           v[h][1].x, v[h][1].y, v[h][1].z, v[h][1].w};
+    uint32_t m2 = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m2 = abs_max2(m2, w[i]);
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) m2 = abs_max2(m2, __shfl_xor_sync(0xffffffffu, m2, o));
+    const float2 mf = bf16x2_to_float2(m2);
+    const float m = fmaxf(fmaxf(mf.x, mf.y), kFp8MinAmax);
+    const float inv = __fdiv_rn(kFp8Max, m);
+    uint32_t o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 a = bf16x2_to_float2(w[2 * i]), b = bf16x2_to_float2(w[2 * i + 1]);
+      o[i] = fp8_pack4(a.x, a.y, b.x, b.y, inv);
+    }
+    if (col < H) {
+      __stcs(reinterpret_cast<uint4*>(q + (size_t)row * H + col),
+             make_uint4(o[0], o[1], o[2], o[3]));
+      if ((lane & 7) == 0) scale[(size_t)row * nb + (col >> 7)] = __fdiv_rn(m, kFp8Max);
+    }
+  }
 }
 
 // Row-major codes [rows][K] -> the section's 128 x 128 tiles: row r's 16-byte chunk c of tile
@@ -57,7 +91,7 @@ int launch_quantize_fp8(const uint16_t* x, const int32_t* src, int rows, int k, 
                         uint8_t* q, float* scale, cudaStream_t st) {
   if (rows <= 0) return MOE_OK;
   const int nb = ceil_div(H, kFp8Block);
-  const long long items = (long long)rows * nb;
+  const long long items = (long long)rows * ceil_div(H, kCols);
   MOE_LAUNCH_PDL(quantize_fp8_kernel, dim3((unsigned)((items + 7) / 8)), dim3(256), 0, st, x, src,
                  rows, k, T, H, nb, q, scale);
   MOE_COUNT_LAUNCH();

@@ -495,13 +495,16 @@ int launch_route(const RouteArgs& a, const RoutePlan& r, const RouteScratch& s,
       MOE_COUNT_LAUNCH();
       MOE_LAUNCH_CHECK();
     }
-    if (r.small && !a.n_group) {
+    if (r.small) {
       GateParams p{};
       p.part = s.part; p.S = r.S; p.C = r.C; p.ldp = r.C;
       p.x = a.x; p.w_r = a.w_r; p.w_rT = nullptr; p.logit_bias = a.logit_bias;
       p.sel_bias = a.sel_bias; p.forced = a.forced; p.T = a.T; p.H = a.H; p.E = a.E; p.k = a.k;
       p.mode = a.gating; p.scale = a.scale; p.ids = a.ids; p.w = a.w; p.logits = a.logits;
       p.shared_gate = a.shared_gate; p.tie_flags = a.tie_flags; p.hist = nullptr;
+      if (a.n_group)
+        return launch_route_group_tail(p, a.n_group, a.take, a.counts, a.offsets, a.pos, a.src,
+                                       s.active, s.n_active, s.shared_meta, a.x_perm, st);
       MOE_LAUNCH_PDL(route_tail_kernel, dim3(1), dim3(kTailThreads), 0, st, p, a.counts,
                      a.offsets, a.pos, a.src, s.active, s.n_active, s.shared_meta, a.x_perm);
       MOE_COUNT_LAUNCH();

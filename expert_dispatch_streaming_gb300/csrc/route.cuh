@@ -86,6 +86,10 @@ int launch_route(const RouteArgs& a, const RoutePlan& r, const RouteScratch& s,
 // Group-limited gating of p.T tokens (csrc/route_group.cu).
 constexpr int kMaxGroups = 32;
 int launch_gate_group(const GateParams& p, int n_group, int take, cudaStream_t st);
+int launch_route_group_tail(const GateParams& p, int n_group, int take, int32_t* counts,
+                            int32_t* offsets, int32_t* pos, int32_t* src, int32_t* active,
+                            int32_t* n_active, int32_t* shared_meta, uint16_t* x_perm,
+                            cudaStream_t st);
 int launch_gather(const uint16_t* x, const int32_t* src, int rows, int k, int H,
                   uint16_t* x_perm, cudaStream_t st);
 

@@ -266,7 +266,75 @@ gate_group_kernel(GateParams p, int n_group, int take) {
   }
 }
 
+// Everything after the router product for a batch of at most kSmallT tokens in one CTA, as
+// route_tail_kernel: the slices of every logit summed (G lanes a logit, fixed order), one warp a
+// token gating, then the histogram, scan, ranks and tables (route_dispatch_block).
+constexpr int kTailWarps = 32;
+struct GroupTailSmem {
+  TailSmem tail;                 // (lrow / exact_s unused)
+  GroupSmem g[kSmallT];
+};
+__global__ void __launch_bounds__(kTailWarps * 32)
+route_group_tail_kernel(GateParams p, int n_group, int take, int32_t* __restrict__ counts,
+                        int32_t* __restrict__ offsets, int32_t* __restrict__ pos,
+                        int32_t* __restrict__ src, int32_t* __restrict__ active,
+                        int32_t* __restrict__ n_active, int32_t* __restrict__ shared_meta,
+                        uint16_t* __restrict__ x_perm) {
+  pdl_trigger();
+  pdl_wait();
+  extern __shared__ __align__(16) uint8_t raw_smem[];
+  GroupTailSmem& sm = *reinterpret_cast<GroupTailSmem*>(raw_smem);
+  constexpr int NT = kTailWarps * 32;
+  const int tid = threadIdx.x, warp = tid >> 5, T = p.T, C = p.C, E = p.E, S = p.S, n = T * C;
+  const size_t stride = (size_t)T * C;
+  int G = 32;
+  while (G > 1 && n * G > NT) G >>= 1;
+  const int per = NT / G, g = tid % G;
+  for (int li = tid / G; li < ((n + per - 1) / per) * per; li += per) {
+    float a[4] = {0.f, 0.f, 0.f, 0.f};
+    if (li < n) {
+      int sp = g, i = 0;
+#pragma unroll 4
+      for (; sp < S; sp += G, ++i) a[i & 3] += __ldcg(p.part + (size_t)sp * stride + li);
+    }
+    float v = (a[0] + a[1]) + (a[2] + a[3]);
+    for (int o = G >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (g == 0 && li < n) sm.tail.lg[li] = v;
+  }
+  for (int e = tid; e < kMaxExperts; e += NT) sm.tail.hist[e] = 0;
+  __syncthreads();
+  if (warp < T) {
+    GateParams q = p;
+    q.hist = sm.tail.hist;
+    const float* raw = sm.tail.lg + (size_t)warp * C;
+    if (E <= 64) gate_token_grouped<2>(q, n_group, take, warp, raw, sm.g[warp]);
+    else gate_token_grouped<EC>(q, n_group, take, warp, raw, sm.g[warp]);
+  }
+  __syncthreads();
+  route_dispatch_block<NT>(p.ids, T, p.k, E, counts, offsets, pos, src, active, n_active,
+                           shared_meta, x_perm, p.x, p.H, sm.tail);
+}
+
 }  // namespace
+
+int launch_route_group_tail(const GateParams& p, int n_group, int take, int32_t* counts,
+                            int32_t* offsets, int32_t* pos, int32_t* src, int32_t* active,
+                            int32_t* n_active, int32_t* shared_meta, uint16_t* x_perm,
+                            cudaStream_t st) {
+  static bool attr = false;
+  if (!attr) {
+    MOE_CUDA_TRY(cudaFuncSetAttribute(route_group_tail_kernel,
+                                      cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                      (int)sizeof(GroupTailSmem)));
+    attr = true;
+  }
+  MOE_LAUNCH_PDL(route_group_tail_kernel, dim3(1), dim3(kTailWarps * 32), sizeof(GroupTailSmem),
+                 st, p, n_group, take, counts, offsets, pos, src, active, n_active, shared_meta,
+                 x_perm);
+  MOE_COUNT_LAUNCH();
+  MOE_LAUNCH_CHECK();
+  return MOE_OK;
+}
 
 int launch_gate_group(const GateParams& p, int n_group, int take, cudaStream_t st) {
   GateParams q = p;
