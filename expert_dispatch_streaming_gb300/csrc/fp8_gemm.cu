@@ -47,13 +47,15 @@ constexpr int kStages = 3;
 constexpr int kABytes = kFp8TileBytes, kBBytes = 2 * kFp8TileBytes;
 constexpr int kStageBytes = kABytes + kBBytes;
 constexpr int kThreads = 384;
+static_assert(kThreads >= kMaxExperts, "a thread looks up each expert's rows");
 // Registers per thread after the split: warps 0-3 and warps 4-11 (128 * 40 + 256 * 232 = the
 // 384 * 168 the block is launched with).
 constexpr int kRegsLow = 40, kRegsHigh = 232;
 static_assert(128 * kRegsLow + 256 * kRegsHigh <= kThreads * 168, "within the launch's registers");
 constexpr int kAccCols = 256, kTmemCols = 512;
-// Tiles below this many per CTA are cut into equal ranges of steps.
-constexpr int kRangeTiles = 4;
+// Tiles are cut into equal ranges of steps when there are fewer than kRangeTiles per CTA and the
+// busiest CTA is thereby spared kJoinSteps steps, about what writing and joining the pieces costs.
+constexpr int kRangeTiles = 4, kJoinSteps = 5;
 
 struct alignas(16) Ctl {
   uint64_t full[kStages], empty[kStages], tfull[2], tempty[2], pair[4], drain[2];
@@ -76,7 +78,7 @@ struct Fp8Params {
   CUtensorMap tm_w;             // row-major weights [E * N][K], boxes of 128 x 128 bytes
   const float* xs;
   const int32_t* offsets;
-  int E, N, K, KB, NT, max_rows, RP;
+  int E, N, K, KB, NT, max_rows, quarters;
   BundleTable tab;
   const void* const* dev_tab;
   size_t w_off, s_off;
@@ -89,7 +91,7 @@ struct Fp8Params {
   float* hs;
   void* y;
   int y_f32;
-  float* part;                  // [CTAs][2][RP][256]
+  float* part;                  // [CTAs][2][quarters][2][32][32 lanes] groups of 4 columns
   int32_t* counters;            // [tiles][4], used when tiles are cut
   int32_t* err;
 };
@@ -270,8 +272,8 @@ struct Walk {
   int KB, U, G, u, lo, hi, left;   // left: steps (cut) still to do
   bool cut;
   __device__ __forceinline__ Walk(int U_, int KB_) : KB(KB_), U(U_), G(gridDim.x) {
-    cut = U < kRangeTiles * G;
     const long long W = (long long)U * KB;
+    cut = U < kRangeTiles * G && (long long)((U + G - 1) / G) * KB - W / G >= kJoinSteps;
     if (cut && W < G) G = (int)W;               // no empty ranges
     lo = hi = left = 0;
     u = U;
@@ -450,21 +452,20 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
   }
   pdl_wait();
   const int n_act = p.host_n >= 0 ? p.host_n : p.active ? *p.n_active : p.E;
+  // the experts' rows, a thread each (one memory latency), then the prefix of their tile counts
+  if ((int)threadIdx.x < n_act) {
+    int r0, r1;
+    const int a = threadIdx.x, e = expert_of(p, a);
+    if (expert_rows(p, e, r0, r1)) atomicExch(p.err, 8);
+    c.row0[a] = r0;
+    c.rows[a] = r1 - r0;
+    c.id[a] = e;
+  }
+  __syncthreads();
   if (warp == 2) {
-    // prefix of the experts' tile counts
     int carry = 0;
     for (int base = 0; base < n_act; base += 32) {
-      const int a = base + lane;
-      int cnt = 0;
-      if (a < n_act) {
-        int r0, r1;
-        const int e = expert_of(p, a);
-        if (expert_rows(p, e, r0, r1)) atomicExch(p.err, 8);
-        cnt = p.NT * ((r1 - r0 + 127) >> 7);
-        c.row0[a] = r0;
-        c.rows[a] = r1 - r0;
-        c.id[a] = e;
-      }
+      const int a = base + lane, cnt = a < n_act ? p.NT * ((c.rows[a] + 127) >> 7) : 0;
       int incl = cnt;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -678,13 +679,14 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
       if (wk.lo > 0 || wk.hi < KB) {
         // a piece of the tile: its sums to this CTA's slot (0: begins inside the tile, 1: ends
         // inside it); the last piece's CTA adds them all in range order
-        const size_t slot = (size_t)p.RP * 256;
-        float* mp = p.part + ((size_t)blockIdx.x * 2 + (wk.lo > 0 ? 0 : 1)) * slot +
-                    (size_t)r * 256 + half * 128;
+        // (per warp 32 groups of 4 columns x 32 lanes: a store covers 512 bytes in a row)
+        const size_t slot = (size_t)p.quarters * 2 * 1024;
+        float4* part = reinterpret_cast<float4*>(p.part) + (size_t)(q * 2 + half) * 1024 + lane;
         if (mine) {
+          float4* mp = part + ((size_t)blockIdx.x * 2 + (wk.lo > 0 ? 0 : 1)) * slot;
 #pragma unroll
           for (int i = 0; i < 32; ++i)
-            __stcg(reinterpret_cast<float4*>(mp) + i,
+            __stcg(mp + 32 * i,
                    make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]));
         }
         const long long W = (long long)U * KB, first = (long long)wk.u * KB;
@@ -707,11 +709,10 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
         if (mine) {
           for (int cc = c_lo; cc <= c_hi; ++cc) {
             const bool inside = (long long)cc * W / wk.G > first;
-            const float4* op = reinterpret_cast<const float4*>(
-                p.part + ((size_t)cc * 2 + (inside ? 0 : 1)) * slot + (size_t)r * 256 + half * 128);
+            const float4* op = part + ((size_t)cc * 2 + (inside ? 0 : 1)) * slot;
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
-              const float4 o = __ldcg(op + i);
+              const float4 o = __ldcg(op + 32 * i);
               acc[4 * i] += o.x;
               acc[4 * i + 1] += o.y;
               acc[4 * i + 2] += o.z;
@@ -819,10 +820,13 @@ int launch_variant(const Fp8Params& p, cudaStream_t st) {
 
 }  // namespace
 
+// lane quarters a tile can fill
+static int quarters_of(int max_rows) { return ceil_div(std::min(std::max(max_rows, 1), 128), 32); }
+
 Fp8Plan plan_fp8(const Fp8Args& a) {
   Fp8Plan pl{};
   const int G = sm_count();
-  pl.part_elems = (size_t)G * 2 * std::min(std::max(a.max_rows, 1), 128) * 256;
+  pl.part_elems = (size_t)G * 2 * quarters_of(a.max_rows) * 2 * 4096;
   pl.counter_elems = (size_t)4 * kRangeTiles * G;
   return pl;
 }
@@ -842,7 +846,7 @@ int launch_fp8(const Fp8Args& a, const Fp8Plan&, float* part, int32_t* counters,
     return MOE_ERR_INVALID_ARG;
   p.xs = a.xs; p.offsets = a.offsets; p.E = a.E; p.N = a.N; p.K = a.K;
   p.KB = ceil_div(a.K, 128); p.NT = a.fused ? a.N / 128 : ceil_div(a.N, 256);
-  p.max_rows = a.max_rows; p.RP = std::min(a.max_rows, 128);
+  p.max_rows = a.max_rows; p.quarters = quarters_of(a.max_rows);
   if (a.tab) p.tab = *a.tab;
   p.dev_tab = a.dev_tab; p.w_off = a.w_off; p.s_off = a.s_off; p.ws = a.ws;
   p.active = a.active; p.n_active = a.n_active; p.host_n = a.host_n;
