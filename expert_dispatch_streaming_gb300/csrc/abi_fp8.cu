@@ -109,6 +109,7 @@ int moe_grouped_swiglu_fp8(const uint8_t* xq, const float* x_scale, const int32_
   gu.w_off = lay.gate_up_offset; gu.s_off = lay.gate_up_scale_offset; gu.hq = hq; gu.hs = hs;
   const int r = launch_fp8(gu, pg, part, ctr, err, st);
   if (r != MOE_OK) return r;
+  dn.early = true;
   dn.xq = hq; dn.xs = hs; dn.offsets = offsets; dn.tab = &tab;
   dn.w_off = lay.down_offset; dn.s_off = lay.down_scale_offset; dn.y = y_perm;
   return launch_fp8(dn, pd, part, ctr, err, st);

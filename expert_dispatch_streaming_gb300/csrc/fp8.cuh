@@ -39,6 +39,8 @@ struct Fp8Args {
   const int32_t* offsets;     // device [E+1], or NULL: one group of max_rows rows
   int E, N, K, max_rows;
   bool fused, y_f32;
+  bool early;                 // the kernel before it on the stream is the product that writes xq
+                              // and xs, and nothing else this one reads (see fp8_gemm.cu)
   // weights: bundles (host table or device table) with the section's codes at w_off and its
   // scales at s_off, or plain row-major w [E][N][K] with ws [E][ceil(N/128)][ceil(K/128)]
   const BundleTable* tab;

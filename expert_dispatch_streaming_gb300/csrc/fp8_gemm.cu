@@ -68,6 +68,9 @@ struct alignas(16) Ctl {
 };
 // Output rows on their way out: per epilogue warp two boxes of 32 rows x 128 bytes.
 constexpr int kBox = 4096, kOutBytes = 8 * 2 * kBox;
+// Up to this many rows of a quarter are joined a row at a time by the whole warp (their sums fit
+// the warp's boxes: 512 bytes a row).
+constexpr int kFewRows = 2 * kBox / 512;
 constexpr int kSmem = kStages * kStageBytes + kOutBytes + 1024 + (int)sizeof(Ctl);
 static_assert(kStages == 3, "the MMA issuers' order of waits covers a stage's use three steps back");
 static_assert(kSmem <= 232448, "over the 227 KB shared-memory limit of a CTA");
@@ -90,7 +93,7 @@ struct Fp8Params {
   uint8_t* hq;
   float* hs;
   void* y;
-  int y_f32;
+  int y_f32, early;
   float* part;                  // [CTAs][2][quarters][2][32][32 lanes] groups of 4 columns
   int32_t* counters;            // [tiles][4], used when tiles are cut
   int32_t* err;
@@ -174,6 +177,9 @@ __device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map, int
       "{%2, %3}], [%4];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(smem_u32(bar))
       : "memory");
+}
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
 __device__ __forceinline__ bool elect_one() {
   uint32_t pred = 0;
@@ -421,6 +427,30 @@ __device__ __forceinline__ void store_y(const Fp8Params& p, uint8_t* box, const 
   __syncwarp();
 }
 
+// Bytes a step of tile t brings in, and the request for its weights (into sb, completing on fb).
+template <bool FUSED>
+__device__ __forceinline__ uint32_t load_bytes(const Fp8Params& p, const Tile& t) {
+  const bool two = FUSED || t.nt * 256 + 128 < p.N;
+  return (t.rows > 96 ? kABytes : ((t.rows + 31) >> 5) * 4096) + (two ? kBBytes : kFp8TileBytes);
+}
+template <bool FUSED, bool PLAIN>
+__device__ __forceinline__ void load_weights(const Fp8Params& p, const Tile& t, int kb, uint32_t sb,
+                                             uint64_t* fb) {
+  const int n0 = t.nt * (FUSED ? 128 : 256);
+  const bool two = FUSED || n0 + 128 < p.N;
+  if (PLAIN) {
+    tma_2d(sb, &p.tm_w, kb * 128, t.e * p.N + n0, fb);
+    if (two) tma_2d(sb + kFp8TileBytes, &p.tm_w, kb * 128, t.e * p.N + n0 + 128, fb);
+  } else {
+    const char* b = static_cast<const char*>(p.dev_tab ? p.dev_tab[t.e] : p.tab.p[t.e]) + p.w_off +
+                    ((size_t)(n0 >> 7) * p.KB + kb) * kFp8TileBytes;
+    bulk_g2s(sb, b, kFp8TileBytes, fb);
+    if (two)
+      bulk_g2s(sb + kFp8TileBytes, b + (size_t)(FUSED ? p.N >> 7 : 1) * p.KB * kFp8TileBytes,
+               kFp8TileBytes, fb);
+  }
+}
+
 // FUSED: N = columns of h (gate rows 0..N-1, up rows N..2N-1).  PLAIN: row-major weights by TMA.
 template <bool FUSED, bool PLAIN>
 __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_constant__ Fp8Params p) {
@@ -431,6 +461,11 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
   Ctl& c = *reinterpret_cast<Ctl*>(out + kOutBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_trigger();
+  if (threadIdx.x == 32) {
+    prefetch_map(&p.tm_x);
+    prefetch_map(&p.tm_x32);
+    if (PLAIN) prefetch_map(&p.tm_w);
+  }
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&c.full[s], 1);
@@ -450,7 +485,10 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
                  "r"(kTmemCols));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
-  pdl_wait();
+  // The second product of an FFN starts while the first one ends: of what that writes it reads
+  // the token rows and their scales only, and writes nothing itself, until pdl_wait (below, by
+  // the warps concerned); experts, offsets and weights are older.
+  if (!p.early) pdl_wait();
   const int n_act = p.host_n >= 0 ? p.host_n : p.active ? *p.n_active : p.E;
   // the experts' rows, a thread each (one memory latency), then the prefix of their tile counts
   if ((int)threadIdx.x < n_act) {
@@ -490,30 +528,33 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
     int stage = 0, issued = 0;
     uint32_t phase = 0;
     bool ok = true;
+    // early: the weights of the first stages are asked for before the token rows may be
+    int ahead = 0;
+    if (p.early && wk.next()) {
+      const Tile t = tile_of(c, n_act, wk.u);
+      for (; ahead < min(kStages, wk.hi - wk.lo); ++ahead) {
+        if (elect_one()) {
+          const uint32_t sb = smem_u32(smem + ahead * kStageBytes) + kABytes;
+          mbar_expect_tx(&c.full[ahead], load_bytes<FUSED>(p, t));
+          load_weights<FUSED, PLAIN>(p, t, wk.lo + ahead, sb, &c.full[ahead]);
+        }
+        __syncwarp();
+      }
+    }
+    if (p.early) pdl_wait();
+    wk = Walk(U, KB);
     while (ok && wk.next()) {
       const Tile t = tile_of(c, n_act, wk.u);
       const int nsub = t.rows > 96 ? 0 : (t.rows + 31) >> 5;
-      const int n0 = t.nt * (FUSED ? 128 : 256);
-      const bool two = FUSED || n0 + 128 < p.N;
-      const char *w0 = nullptr, *w1 = nullptr;
-      if (!PLAIN) {
-        const char* b = static_cast<const char*>(p.dev_tab ? p.dev_tab[t.e] : p.tab.p[t.e]);
-        w0 = b + p.w_off + (size_t)(n0 >> 7) * KB * kFp8TileBytes;
-        w1 = w0 + (size_t)(FUSED ? p.N >> 7 : 1) * KB * kFp8TileBytes;
-      }
+      const uint32_t bytes = load_bytes<FUSED>(p, t);
       for (int kb = wk.lo; kb < wk.hi; ++kb) {
         if (!(ok = warp_wait(&c.empty[stage], phase ^ 1, p.err, 1))) break;
         uint64_t* fb = &c.full[stage];
-        const uint32_t sa = smem_u32(smem + stage * kStageBytes), sb = sa + kABytes;
+        const uint32_t sa = smem_u32(smem + stage * kStageBytes);
         if (elect_one()) {
-          mbar_expect_tx(fb, (nsub ? nsub * 4096 : kABytes) + (two ? kBBytes : kFp8TileBytes));
-          if (PLAIN) {
-            tma_2d(sb, &p.tm_w, kb * 128, t.e * p.N + n0, fb);
-            if (two) tma_2d(sb + kFp8TileBytes, &p.tm_w, kb * 128, t.e * p.N + n0 + 128, fb);
-          } else {
-            bulk_g2s(sb, w0 + (size_t)kb * kFp8TileBytes, kFp8TileBytes, fb);
-            if (two)
-              bulk_g2s(sb + kFp8TileBytes, w1 + (size_t)kb * kFp8TileBytes, kFp8TileBytes, fb);
+          if (issued >= ahead) {
+            mbar_expect_tx(fb, bytes);
+            load_weights<FUSED, PLAIN>(p, t, kb, sa + kABytes, fb);
           }
           if (nsub) {
             // 32-row boxes stacked at 4 KB: the same swizzled layout as one box of all rows
@@ -577,6 +618,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
     }
   } else if (warp == 2) {
     // ------------------------------------------------------------ scale factors
+    if (p.early) pdl_wait();
     // per step: xs * ws of every token and weight tile into the TMEM buffer's slot; the loads
     // of a step are issued while its buffer is still in use
     int buf = 0;
@@ -613,6 +655,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
   } else if (warp >= 4) {
     // ------------------------------------------------------------ scaling and epilogue
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsHigh));
+    if (p.early) pdl_wait();
     const int q = warp & 3, half = (warp - 4) >> 2, r = q * 32 + lane;
     uint8_t* box = out + (warp - 4) * 2 * kBox;
     int buf = 0, flip = 0;
@@ -692,24 +735,61 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
         const long long W = (long long)U * KB, first = (long long)wk.u * KB;
         const int c_lo = (int)(((first + 1) * wk.G - 1) / W);
         const int c_hi = (int)(((first + KB) * wk.G - 1) / W);
-        __threadfence();
+        // both warps' pieces are written (meet), then published by one release at GPU scope
         if (!(ok = meet())) break;
         if (half == 0 && lane == 0) {
           int32_t* ctr = p.counters + (size_t)wk.u * 4 + q;
-          const int l = atomicAdd(ctr, 1) == c_hi - c_lo;
+          int before;
+          asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;"
+                       : "=r"(before)
+                       : "l"(ctr)
+                       : "memory");
+          const int l = before == c_hi - c_lo;
           if (l) *ctr = 0;
           c.last[q] = l;
-          __threadfence();
         }
         if (!(ok = meet())) break;
         if (!c.last[q]) continue;
-        __threadfence();
+        // only the first CTA's piece can begin at the tile's first step (slot 1)
+        const bool lo_inside = (long long)c_lo * W / wk.G > first;
+        const int have = t.rows - q * 32;
+        if (have <= kFewRows) {
+          // few rows: a lane sums 4 columns of a row over all pieces (their loads in flight
+          // together), the sums go to the row's lane through shared memory (the warp's boxes)
+          if (lane == 0) bulk_wait_read();
+          __syncwarp();
+          float4* sh = reinterpret_cast<float4*>(out + (warp - 4) * 2 * kBox);
+          for (int l = 0; l < have; ++l) {
+            const float4* op = part - lane + 32 * lane + l;
+            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+            for (int cc = c_lo; cc <= c_hi; ++cc) {
+              const float4 o =
+                  __ldcg(op + ((size_t)cc * 2 + (cc > c_lo || lo_inside ? 0 : 1)) * slot);
+              s.x += o.x;
+              s.y += o.y;
+              s.z += o.z;
+              s.w += o.w;
+            }
+            sh[32 * l + lane] = s;
+          }
+          __syncwarp();
+          if (mine) {
 #pragma unroll
-        for (int i = 0; i < 128; ++i) acc[i] = 0.f;
-        if (mine) {
-          for (int cc = c_lo; cc <= c_hi; ++cc) {
-            const bool inside = (long long)cc * W / wk.G > first;
-            const float4* op = part + ((size_t)cc * 2 + (inside ? 0 : 1)) * slot;
+            for (int i = 0; i < 32; ++i) {
+              const float4 o = sh[32 * lane + i];
+              acc[4 * i] = o.x;
+              acc[4 * i + 1] = o.y;
+              acc[4 * i + 2] = o.z;
+              acc[4 * i + 3] = o.w;
+            }
+          }
+          __syncwarp();
+        } else {
+#pragma unroll
+          for (int i = 0; i < 128; ++i) acc[i] = 0.f;
+          for (int cc = c_lo; mine && cc <= c_hi; ++cc) {
+            const float4* op = part + ((size_t)cc * 2 + (cc > c_lo || lo_inside ? 0 : 1)) * slot;
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
               const float4 o = __ldcg(op + 32 * i);
@@ -812,7 +892,22 @@ int launch_variant(const Fp8Params& p, cudaStream_t st) {
                                       cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem));
     attr = true;
   }
-  MOE_LAUNCH_PDL((fp8_gemm_kernel<FUSED, PLAIN>), dim3(sm_count()), dim3(kThreads), kSmem, st, p);
+  if (p.early) {
+    // scheduled as the CTAs of the kernel before it end (see pdl_wait in the kernel)
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(sm_count());
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    MOE_CUDA_TRY(cudaLaunchKernelEx(&cfg, fp8_gemm_kernel<FUSED, PLAIN>, p));
+  } else {
+    MOE_LAUNCH_PDL((fp8_gemm_kernel<FUSED, PLAIN>), dim3(sm_count()), dim3(kThreads), kSmem, st, p);
+  }
   MOE_COUNT_LAUNCH();
   MOE_LAUNCH_CHECK();
   return MOE_OK;
@@ -851,7 +946,7 @@ int launch_fp8(const Fp8Args& a, const Fp8Plan&, float* part, int32_t* counters,
   p.dev_tab = a.dev_tab; p.w_off = a.w_off; p.s_off = a.s_off; p.ws = a.ws;
   p.active = a.active; p.n_active = a.n_active; p.host_n = a.host_n;
   for (int i = 0; i < (a.host_n > 0 ? a.host_n : 0); ++i) p.host_ids[i] = (int16_t)a.host_ids[i];
-  p.hq = a.hq; p.hs = a.hs; p.y = a.y; p.y_f32 = a.y_f32;
+  p.hq = a.hq; p.hs = a.hs; p.y = a.y; p.y_f32 = a.y_f32; p.early = a.early;
   p.part = part; p.counters = counters; p.err = err;
   if (a.fused) return launch_variant<true, false>(p, st);
   return a.w ? launch_variant<false, true>(p, st) : launch_variant<false, false>(p, st);
