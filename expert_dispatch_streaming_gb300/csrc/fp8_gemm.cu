@@ -48,33 +48,19 @@ constexpr int kABytes = kFp8TileBytes, kBBytes = 2 * kFp8TileBytes;
 constexpr int kStageBytes = kABytes + kBBytes;
 constexpr int kThreads = 384;
 static_assert(kThreads >= kMaxExperts, "a thread looks up each expert's rows");
-// Registers per thread after the split: warps 0-3 and warps 4-11 (128 * 40 + 256 * 232 = the
+// Registers per thread after the split: warps 0-3 and warps 4-11 (128 * 56 + 256 * 224 = the
 // 384 * 168 the block is launched with).
-constexpr int kRegsLow = 40, kRegsHigh = 232;
+constexpr int kRegsLow = 56, kRegsHigh = 224;
 static_assert(128 * kRegsLow + 256 * kRegsHigh <= kThreads * 168, "within the launch's registers");
 constexpr int kAccCols = 256, kTmemCols = 512;
 // Tiles are cut into equal ranges of steps when there are fewer than kRangeTiles per CTA and the
 // busiest CTA is thereby spared kJoinSteps steps, about what writing and joining the pieces costs.
 constexpr int kRangeTiles = 4, kJoinSteps = 5;
 
-struct alignas(16) Ctl {
-  uint64_t full[kStages], empty[kStages], tfull[2], tempty[2], pair[4], drain[2];
-  uint32_t tmem;
-  int last[4];
-  int pref[kMaxExperts + 1];    // tiles before the a-th expert run
-  int row0[kMaxExperts], rows[kMaxExperts], id[kMaxExperts];   // its rows and id
-  float amax[2][2][128];
-  float2 f[2][128];             // per TMEM buffer and token: xs * ws of the two weight tiles
-};
 // Output rows on their way out: per epilogue warp two boxes of 32 rows x 128 bytes.
 constexpr int kBox = 4096, kOutBytes = 8 * 2 * kBox;
-// Up to this many rows of a quarter are joined a row at a time by the whole warp (their sums fit
-// the warp's boxes: 512 bytes a row).
-constexpr int kFewRows = 2 * kBox / 512;
-constexpr int kSmem = kStages * kStageBytes + kOutBytes + 1024 + (int)sizeof(Ctl);
-static_assert(kStages == 3, "the MMA issuers' order of waits covers a stage's use three steps back");
-static_assert(kSmem <= 232448, "over the 227 KB shared-memory limit of a CTA");
-
+// Up to this many rows of a quarter are joined and finished a row at a time by the whole warp.
+constexpr int kFewRows = 4;
 struct Fp8Params {
   CUtensorMap tm_x, tm_x32;     // token rows [max_rows][K], boxes of 128 / 32 rows x 128 bytes
   CUtensorMap tm_out;           // y (or hq): boxes of 32 rows x 128 (hq: 64) bytes
@@ -273,26 +259,43 @@ __device__ __forceinline__ bool expert_rows(const Fp8Params& p, int e, int& r0, 
   return r0 != a || r1 != b;
 }
 
-// The CTA's share of the steps: whole tiles CTA, CTA + G, ... or one range of all tiles' steps.
+// The CTA's share of the steps: whole tiles CTA, CTA + G, ... or one range of all tiles' steps,
+// in order: the first `more` CTAs take n + 1 steps, the others n.
+struct Cut {
+  int on, G, n, more;
+  __device__ __forceinline__ void set(int U, int KB) {
+    G = gridDim.x;
+    on = 0;
+    if (U >= kRangeTiles * G) return;
+    const int W = U * KB;
+    on = (U + G - 1) / G * KB - W / G >= kJoinSteps;
+    if (!on) return;
+    G = max(1, min(G, W));                      // no empty ranges
+    n = W / G;
+    more = W - n * G;
+  }
+  __device__ __forceinline__ int start(int cta) const { return cta * n + min(cta, more); }
+  __device__ __forceinline__ int owner(int step) const {
+    const int cta = step / (n + 1);
+    return cta < more ? cta : more + (step - more * (n + 1)) / n;
+  }
+};
 struct Walk {
   int KB, U, G, u, lo, hi, left;   // left: steps (cut) still to do
   bool cut;
-  __device__ __forceinline__ Walk(int U_, int KB_) : KB(KB_), U(U_), G(gridDim.x) {
-    const long long W = (long long)U * KB;
-    cut = U < kRangeTiles * G && (long long)((U + G - 1) / G) * KB - W / G >= kJoinSteps;
-    if (cut && W < G) G = (int)W;               // no empty ranges
+  __device__ __forceinline__ Walk(const Cut& c, int U_, int KB_) : KB(KB_), U(U_), G(c.G) {
+    cut = c.on;
     lo = hi = left = 0;
-    u = U;
-    if ((int)blockIdx.x >= G) return;
-    u = blockIdx.x;
+    u = (int)blockIdx.x;
     if (cut) {
-      const long long pos = blockIdx.x * W / G;
-      u = (int)(pos / KB);
-      lo = (int)(pos - (long long)u * KB);
-      left = (int)((blockIdx.x + 1) * W / G - pos);
+      const int pos = c.start(u);
+      left = u < G ? c.n + (u < c.more) : 0;
+      u = pos / KB;
+      lo = pos - u * KB;
     }
     u -= cut ? 1 : G;                           // next() steps on to the first
     hi = lo;
+    if (cut && lo == 0) hi = KB;
   }
   __device__ __forceinline__ bool next() {
     if (cut) {
@@ -309,6 +312,20 @@ struct Walk {
     return u < U;
   }
 };
+
+struct alignas(16) Ctl {
+  uint64_t full[kStages], empty[kStages], tfull[2], tempty[2], pair[4], drain[2];
+  uint32_t tmem;
+  int last[4];
+  Cut cut;
+  int pref[kMaxExperts + 1];    // tiles before the a-th expert run
+  int row0[kMaxExperts], rows[kMaxExperts], id[kMaxExperts];   // its rows and id
+  float amax[2][2][128];
+  float2 f[2][128];             // per TMEM buffer and token: xs * ws of the two weight tiles
+};
+constexpr int kSmem = kStages * kStageBytes + kOutBytes + 1024 + (int)sizeof(Ctl);
+static_assert(kStages == 3, "the MMA issuers' order of waits covers a stage's use three steps back");
+static_assert(kSmem <= 232448, "over the 227 KB shared-memory limit of a CTA");
 
 struct Tile {
   int e, nt, r0, rows;
@@ -513,14 +530,17 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
       if (a < n_act) c.pref[a] = carry + incl - cnt;
       carry += __shfl_sync(0xffffffffu, incl, 31);
     }
-    if (lane == 0) c.pref[n_act] = carry;
+    if (lane == 0) {
+      c.pref[n_act] = carry;
+      c.cut.set(carry, p.KB);
+    }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = c.tmem;
   const int U = c.pref[n_act], KB = p.KB;
-  Walk wk(U, KB);
+  Walk wk(c.cut, U, KB);
 
   if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLow));
   if (warp == 0) {
@@ -542,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
       }
     }
     if (p.early) pdl_wait();
-    wk = Walk(U, KB);
+    wk = Walk(c.cut, U, KB);
     while (ok && wk.next()) {
       const Tile t = tile_of(c, n_act, wk.u);
       const int nsub = t.rows > 96 ? 0 : (t.rows + 31) >> 5;
@@ -619,8 +639,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
   } else if (warp == 2) {
     // ------------------------------------------------------------ scale factors
     if (p.early) pdl_wait();
-    // per step: xs * ws of every token and weight tile into the TMEM buffer's slot; the loads
-    // of a step are issued while its buffer is still in use
+    // per step: xs * ws of every token and weight tile into the TMEM buffer's slot
     int buf = 0;
     uint32_t tphase = 0;
     bool ok = true;
@@ -638,24 +657,35 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
       const float* sw1 = two ? sw0 + (size_t)(FUSED ? NB : 1) * KB : sw0;
       const float* sx = p.xs + (size_t)(t.r0 + lane) * KB;
       const size_t step = (size_t)32 * KB;
-      for (int kb = wk.lo; kb < wk.hi; ++kb) {
-        const float a = __ldg(sw0 + kb), b = __ldg(sw1 + kb);
-        float x[4];
+      float x[2][4], a[2], b[2];      // two steps in turn: a step's loads go out a step ahead
+      auto load = [&](int j, int kb) {
+        a[j] = __ldg(sw0 + kb);
+        b[j] = __ldg(sw1 + kb);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = lane + 32 * i < t.rows ? __ldg(sx + i * step + kb) : 0.f;
-        if (!(ok = warp_wait(&c.tempty[buf], tphase ^ 1, p.err, 6))) break;
+        for (int i = 0; i < 4; ++i)
+          x[j][i] = lane + 32 * i < t.rows ? __ldg(sx + i * step + kb) : 0.f;
+      };
+      load(0, wk.lo);
+#pragma unroll 1
+      for (int kb = wk.lo; ok && kb < wk.hi; kb += 2) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) c.f[buf][lane + 32 * i] = make_float2(x[i] * a, x[i] * b);
-        __syncwarp();
-        warp_arrive(&c.tfull[buf], lane);
-        buf ^= 1;
-        if (buf == 0) tphase ^= 1;
+        for (int j = 0; j < 2; ++j) {
+          if (kb + j >= wk.hi) break;
+          load(j ^ 1, min(kb + j + 1, wk.hi - 1));
+          if (!(ok = warp_wait(&c.tempty[buf], tphase ^ 1, p.err, 6))) break;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            c.f[buf][lane + 32 * i] = make_float2(x[j][i] * a[j], x[j][i] * b[j]);
+          __syncwarp();
+          warp_arrive(&c.tfull[buf], lane);
+          buf ^= 1;
+          if (buf == 0) tphase ^= 1;
+        }
       }
     }
   } else if (warp >= 4) {
     // ------------------------------------------------------------ scaling and epilogue
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsHigh));
-    if (p.early) pdl_wait();
     const int q = warp & 3, half = (warp - 4) >> 2, r = q * 32 + lane;
     uint8_t* box = out + (warp - 4) * 2 * kBox;
     int buf = 0, flip = 0;
@@ -669,6 +699,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
       pphase ^= 1;
       return w;
     };
+    if (p.early) pdl_wait();
     while (ok && wk.next()) {
       const Tile t = tile_of(c, n_act, wk.u);
       const int n0 = t.nt * (FUSED ? 128 : 256);
@@ -732,9 +763,8 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
             __stcg(mp + 32 * i,
                    make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]));
         }
-        const long long W = (long long)U * KB, first = (long long)wk.u * KB;
-        const int c_lo = (int)(((first + 1) * wk.G - 1) / W);
-        const int c_hi = (int)(((first + KB) * wk.G - 1) / W);
+        const int first = wk.u * KB;
+        const int c_lo = c.cut.owner(first), c_hi = c.cut.owner(first + KB - 1);
         // both warps' pieces are written (meet), then published by one release at GPU scope
         if (!(ok = meet())) break;
         if (half == 0 && lane == 0) {
@@ -750,46 +780,67 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
         }
         if (!(ok = meet())) break;
         if (!c.last[q]) continue;
-        // only the first CTA's piece can begin at the tile's first step (slot 1)
-        const bool lo_inside = (long long)c_lo * W / wk.G > first;
+        // (the first CTA's piece begins at the tile's first step: its slot 1; the others' inside)
         const int have = t.rows - q * 32;
         if (have <= kFewRows) {
-          // few rows: a lane sums 4 columns of a row over all pieces (their loads in flight
-          // together), the sums go to the row's lane through shared memory (the warp's boxes)
-          if (lane == 0) bulk_wait_read();
-          __syncwarp();
-          float4* sh = reinterpret_cast<float4*>(out + (warp - 4) * 2 * kBox);
-          for (int l = 0; l < have; ++l) {
+          // few rows: row by row, a lane takes 4 of the warp's columns (lanes 0-15 of the first
+          // weight tile, 16-31 of the second), sums them over the pieces, whose loads are in flight
+          // together, and finishes them; a lane per row would leave the others idle for it
+          for (int l = 0; ok && l < have; ++l) {
             const float4* op = part - lane + 32 * lane + l;
             float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
             for (int cc = c_lo; cc <= c_hi; ++cc) {
-              const float4 o =
-                  __ldcg(op + ((size_t)cc * 2 + (cc > c_lo || lo_inside ? 0 : 1)) * slot);
+              const float4 o = __ldcg(op + ((size_t)cc * 2 + (cc > c_lo ? 0 : 1)) * slot);
               s.x += o.x;
               s.y += o.y;
               s.z += o.z;
               s.w += o.w;
             }
-            sh[32 * l + lane] = s;
-          }
-          __syncwarp();
-          if (mine) {
+            const size_t row = (size_t)t.r0 + q * 32 + l;
+            if (FUSED) {
+              const float4 u = make_float4(__shfl_down_sync(0xffffffffu, s.x, 16),
+                                           __shfl_down_sync(0xffffffffu, s.y, 16),
+                                           __shfl_down_sync(0xffffffffu, s.z, 16),
+                                           __shfl_down_sync(0xffffffffu, s.w, 16));
+              s = make_float4(silu_mul(s.x, u.x), silu_mul(s.y, u.y), silu_mul(s.z, u.z),
+                              silu_mul(s.w, u.w));
+              float m = lane < 16 ? fmaxf(fmaxf(fabsf(s.x), fabsf(s.y)),
+                                          fmaxf(fabsf(s.z), fabsf(s.w)))
+                                  : 0.f;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const float4 o = sh[32 * lane + i];
-              acc[4 * i] = o.x;
-              acc[4 * i + 1] = o.y;
-              acc[4 * i + 2] = o.z;
-              acc[4 * i + 3] = o.w;
+              for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+              if (lane == 0) c.amax[flip][half][q * 32] = m;
+              if (!(ok = meet())) break;
+              m = fmaxf(fmaxf(c.amax[flip][0][q * 32], c.amax[flip][1][q * 32]), kFp8MinAmax);
+              flip ^= 1;
+              if (lane < 16)
+                *reinterpret_cast<uint32_t*>(p.hq + row * p.N + n0 + 64 * half + 4 * lane) =
+                    fp8_pack4(s.x, s.y, s.z, s.w, __fdiv_rn(kFp8Max, m));
+              if (lane == 0 && half == 0) p.hs[row * NB + (n0 >> 7)] = __fdiv_rn(m, kFp8Max);
+            } else {
+              const int col = n0 + 128 * (lane >> 4) + 64 * half + 4 * (lane & 15);
+              const float v[4] = {s.x, s.y, s.z, s.w};
+              if (p.y_f32) {
+                float* y = static_cast<float*>(p.y) + row * p.N + col;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                  if (col + j < p.N) y[j] = v[j];
+              } else {
+                uint16_t* y = static_cast<uint16_t*>(p.y) + row * p.N + col;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                  if (col + j < p.N) y[j] = float_to_bf16_bits(v[j]);
+              }
             }
           }
-          __syncwarp();
+          if (!ok) break;
+          continue;
         } else {
 #pragma unroll
           for (int i = 0; i < 128; ++i) acc[i] = 0.f;
           for (int cc = c_lo; mine && cc <= c_hi; ++cc) {
-            const float4* op = part + ((size_t)cc * 2 + (cc > c_lo || lo_inside ? 0 : 1)) * slot;
+            const float4* op = part + ((size_t)cc * 2 + (cc > c_lo ? 0 : 1)) * slot;
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
               const float4 o = __ldcg(op + 32 * i);
