@@ -8,16 +8,17 @@
 //                      (softmax modes); a group of one expert has its score;
 //   taken        = the `take` groups of largest G_g, ties to the lower group;
 //   chosen       = the k largest c_e inside the taken groups, ties to the lower expert;
-//   weights      = those of the ungrouped gating at the chosen experts (gate_finish).
+//   weights      = those of the ungrouped gating at the chosen experts.
 // A NaN score counts as -infinity.
 //
 // Both selections are exact in the sense of gate.cuh: fp32 scores decide unless the k-th and
 // the next lie within the fp32 error margin; then the experts near the boundary (for a group:
-// the candidates for its two largest) are re-scored with exact_score and compared in fp64.
+// the candidates for its two largest) are re-scored and compared in fp64.
 //
-// One warp gates one token.  Expert e's score sits in slot e / 32 of lane e % 32; a copy in
-// shared memory lets the 32 / n_group lanes of a group (rounded down to a power of two) scan
-// its experts, each keeping the two largest it saw, merged by shuffles.
+// One warp gates one token, its scores in shared memory: expert e's is handled by lane e % 32;
+// 32 / n_group lanes (rounded down to a power of two) scan a group, each keeping the two largest
+// it saw.  What costs here is latency: a lane's loads go out together, and the few tokens that
+// need re-scoring are shared by their whole CTA.
 #include "gate.cuh"
 #include "route.cuh"
 
@@ -28,7 +29,24 @@ struct GroupSmem {
   float lrow[kMaxExperts];      // logits
   float srow[kMaxExperts];      // selection scores (NaN replaced)
   double exact_s[kMaxExperts];  // re-scored experts (NaN: not re-scored)
-  double gx[32];                // re-scored groups
+  int ids[kMaxK];               // the chosen, ascending
+};
+
+// The groups' layout over a warp's lanes.
+struct Groups {
+  int n, take, gs, P;           // groups, groups taken, experts per group, lanes per group
+  unsigned mul;                 // e / gs = e * mul >> 16 for e < 256
+  bool pairs;                   // a group's score is the sum of its two largest
+  __device__ __forceinline__ Groups(int n_, int take_, int E, bool sig) : n(n_), take(take_) {
+    gs = E / n;
+    P = 1;
+    while (2 * P * n <= 32) P *= 2;
+    mul = (65536u + gs - 1) / gs;
+    pairs = sig && gs > 1;
+  }
+  __device__ __forceinline__ int of(int e) const { return (int)(e * mul >> 16); }
+  // the lane that holds group g's score
+  __device__ __forceinline__ int lane_of(int g) const { return g * P; }
 };
 
 // Order-preserving map of a non-NaN float to an unsigned integer (0 is below every score).
@@ -40,143 +58,105 @@ __device__ __forceinline__ float key_score(uint32_t k) {
   return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xFFFFFFFFu));
 }
 
-// Re-scores expert b once (exact_s[b] keeps it); every lane returns the same value.
-__device__ __noinline__ double rescored(const GateParams& p, int t, int b, int lane,
-                                        GroupSmem& sm) {
-  double s = sm.exact_s[b];
-  __syncwarp();
-  if (s == s) return s;
-  s = exact_score(p, t, b, lane);
-  if (s != s) s = -CUDART_INF;
-  s = __shfl_sync(0xffffffffu, s, 0);
-  if (lane == 0) sm.exact_s[b] = s;
-  __syncwarp();
-  return s;
-}
-
-// Gating of token t by one warp (see the top of the file).  raw: the token's C summed router
-// outputs, or NULL: sum the S slices of p.part.
+// Logits and selection scores of token t into sm, all of a lane's loads in flight together.  raw:
+// the token's C summed router outputs, or NULL: sum the S slices of p.part.
 template <int NC>
-__device__ __forceinline__ void gate_token_grouped(const GateParams& p, int n_group, int take,
-                                                   int t, const float* raw, GroupSmem& sm) {
-  const int lane = threadIdx.x & 31, E = p.E, k = p.k, gs = E / n_group;
+__device__ __forceinline__ void score_token(const GateParams& p, int t, const float* raw,
+                                            GroupSmem& sm) {
+  const int lane = threadIdx.x & 31, E = p.E;
   const bool sig = p.mode == MOE_GATING_SIGMOID_BIAS_RENORM;
-  float l[NC], sc[NC];
+  const size_t stride = (size_t)p.T * p.ldp;
+  const float* part = raw ? raw : p.part + (size_t)t * p.ldp;
+  const int S = raw ? 1 : p.S;
+  float v[NC], lb[NC], sb[NC];
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    const int e = min(lane + 32 * c, E - 1);
+    v[c] = part[e];
+    lb[c] = p.logit_bias ? __ldg(p.logit_bias + e) : 0.f;
+    sb[c] = sig && p.sel_bias ? __ldg(p.sel_bias + e) : 0.f;
+  }
+  if (S > 1)
+#pragma unroll
+    for (int c = 0; c < NC; ++c) v[c] = sum_slices(part + min(lane + 32 * c, E - 1), S, stride);
+  if (lane == 0 && p.shared_gate && p.C > E)
+    p.shared_gate[t] = 1.f / (1.f + expf(-(S == 1 ? part[E] : sum_slices(part + E, S, stride))));
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
     const int e = lane + 32 * c;
-    float v = -CUDART_INF_F, s = -CUDART_INF_F;
+    const float l = v[c] + lb[c];
+    // (hardware exponential and reciprocal: off by less than 1e-6, far inside kTau)
+    const float s = sig ? __fdividef(1.f, 1.f + __expf(-l)) + sb[c] : l;
     if (e < E) {
-      v = raw ? raw[e] : sum_slices(p.part + (size_t)t * p.ldp + e, p.S, (size_t)p.T * p.ldp);
-      if (p.logit_bias) v += p.logit_bias[e];
-      s = v;
-      if (sig) {
-        s = 1.f / (1.f + expf(-v));
-        if (p.sel_bias) s += p.sel_bias[e];
-      }
-      if (s != s) s = -CUDART_INF_F;
-      sm.lrow[e] = v;
-      sm.srow[e] = s;
-      sm.exact_s[e] = CUDART_NAN;
-      if (p.logits) p.logits[(size_t)t * E + e] = v;
+      sm.lrow[e] = l;
+      sm.srow[e] = s != s ? -CUDART_INF_F : s;
+      if (p.logits) p.logits[(size_t)t * E + e] = l;
     }
-    l[c] = v;
-    sc[c] = s;
-  }
-  if (lane == 0 && p.shared_gate && p.C > E) {
-    const float z =
-        raw ? raw[E] : sum_slices(p.part + (size_t)t * p.ldp + E, p.S, (size_t)p.T * p.ldp);
-    p.shared_gate[t] = 1.f / (1.f + expf(-z));
   }
   __syncwarp();
+}
 
-  // ---- group scores: P lanes per group, lane (g, part) scans experts part, part + P, ...
-  int P = 1;
-  while (2 * P * n_group <= 32) P *= 2;
-  const int g = lane / P, part = lane % P;
+// Scores of the groups and the `take` best: of this lane's group (lane / P) its score, the score an
+// expert needs to be among its deciding ones, and its rank; kth / nxt: the take-th score and the
+// next (nxt = -infinity when every group is taken).
+struct GroupRank {
+  float score, least, kth, nxt;
+  int rank;
+};
+__device__ __noinline__ GroupRank rank_groups(const Groups& G, const GroupSmem& sm) {
+  const int lane = threadIdx.x & 31, g = lane / G.P, part = lane % G.P;
   float m1 = -CUDART_INF_F, m2 = -CUDART_INF_F;
-  if (g < n_group)
-    for (int i = part; i < gs; i += P) {
-      const float s = sm.srow[g * gs + i];
+  if (g < G.n)
+#pragma unroll 1
+    for (int i = part; i < G.gs; i += G.P) {
+      const float s = sm.srow[g * G.gs + i];
       m2 = fmaxf(m2, fminf(m1, s));
       m1 = fmaxf(m1, s);
     }
-  for (int o = 1; o < P; o <<= 1) {
+#pragma unroll 1
+  for (int o = 1; o < G.P; o <<= 1) {
     const float a1 = __shfl_xor_sync(0xffffffffu, m1, o), a2 = __shfl_xor_sync(0xffffffffu, m2, o);
     m2 = fmaxf(fmaxf(m2, a2), fminf(m1, a1));
     m1 = fmaxf(m1, a1);
   }
-  float gsc = sig && gs > 1 ? m1 + m2 : m1;
-  if (gsc != gsc) gsc = -CUDART_INF_F;
-  // ---- the `take` best groups
-  int rank = 0;
-  for (int q = 0; q < n_group; ++q) {
-    const float so = __shfl_sync(0xffffffffu, gsc, q * P);
-    rank += better(so, q, gsc, g);
-  }
-  const bool lead = part == 0 && g < n_group;
-  bool kept = lead && rank < take;
-  int flag = 0;
-  if (take < n_group) {
-    const unsigned bk = __ballot_sync(0xffffffffu, lead && rank == take - 1);
-    const unsigned bn = __ballot_sync(0xffffffffu, lead && rank == take);
-    const float kth = __shfl_sync(0xffffffffu, gsc, __ffs(bk) - 1);
-    const float nxt = __shfl_sync(0xffffffffu, gsc, __ffs(bn) - 1);
-    const float tau = sig && gs > 1 ? 2.f * kTau : kTau;
-    if (kth - nxt <= tau) {
-      flag = 1;
-      const bool def = kept && gsc - nxt > tau;
-      const bool band = lead && !def && gsc >= kth - tau;
-      unsigned bm = __ballot_sync(0xffffffffu, band);
-      const int need = take - __popc(__ballot_sync(0xffffffffu, def));
-      for (unsigned m = bm; m; m &= m - 1) {
-        const int ll = __ffs(m) - 1, q = ll / P;
-        // the experts that can be among the group's two largest (its largest, one-expert sums)
-        const float lo = __shfl_sync(0xffffffffu, sig && gs > 1 ? m2 : m1, ll) - kTau;
-        double x1 = -CUDART_INF, x2 = -CUDART_INF;
-        for (int i = 0; i < gs; ++i) {
-          if (!(sm.srow[q * gs + i] >= lo)) continue;
-          const double s = rescored(p, t, q * gs + i, lane, sm);
-          x2 = fmax(x2, fmin(x1, s));
-          x1 = fmax(x1, s);
-        }
-        if (lane == 0) sm.gx[q] = sig && gs > 1 ? x1 + x2 : x1;
-      }
-      __syncwarp();
-      const double mine = band ? sm.gx[g] : -CUDART_INF;
-      int r = 0;
-      double last = CUDART_INF, first = -CUDART_INF;   // worst taken, best left
-      for (unsigned m = bm; m; m &= m - 1) {
-        const int q = (__ffs(m) - 1) / P;
-        r += better_d(sm.gx[q], q, mine, g);
-      }
-      kept = def || (band && r < need);
-      const unsigned tk = __ballot_sync(0xffffffffu, band && r < need);
-      for (unsigned m = bm; m; m &= m - 1) {
-        const int ll = __ffs(m) - 1;
-        const double s = sm.gx[ll / P];
-        if ((tk >> ll) & 1) last = fmin(last, s);
-        else first = fmax(first, s);
-      }
-      if (last - first < kNearTie) flag = 2;
-    }
-  }
-  const unsigned gm = __ballot_sync(0xffffffffu, kept);   // leader lane of group q: q * P
+  GroupRank r;
+  r.score = G.pairs ? m1 + m2 : m1;
+  if (r.score != r.score) r.score = -CUDART_INF_F;
+  r.least = (G.pairs ? m2 : m1) - kTau;
+  r.rank = 0;
+  r.kth = 0.f;
+  r.nxt = -CUDART_INF_F;
+#pragma unroll 1
+  for (int q = 0; q < G.n; ++q)
+    r.rank += better(__shfl_sync(0xffffffffu, r.score, G.lane_of(q)), q, r.score, g);
+  if (g >= G.n) r.rank = 32;
+  const unsigned bk = __ballot_sync(0xffffffffu, r.rank == G.take - 1);
+  const unsigned bn = __ballot_sync(0xffffffffu, r.rank == G.take);
+  r.kth = __shfl_sync(0xffffffffu, r.score, __ffs(bk) - 1);
+  if (bn) r.nxt = __shfl_sync(0xffffffffu, r.score, __ffs(bn) - 1);
+  return r;
+}
 
-  // ---- the k + 1 best experts inside the taken groups
+// The k + 1 best experts of the groups in gm (bit lane_of(g)): chosen: bit c = the lane's expert
+// lane + 32 c is among the k; kth / nxt the k-th score and the next.
+struct Top {
+  unsigned chosen;
+  float kth, nxt;
+};
+template <int NC>
+__device__ __noinline__ Top top_experts(const Groups& G, const GroupSmem& sm, unsigned gm, int E,
+                                        int k) {
+  const int lane = threadIdx.x & 31;
   uint32_t key[NC];
-  bool open[NC], chosen[NC];
 #pragma unroll
   for (int c = 0; c < NC; ++c) {
     const int e = lane + 32 * c;
-    open[c] = e < E && ((gm >> ((e / gs) * P)) & 1);
-    key[c] = open[c] ? score_key(sc[c]) : 0u;
-    chosen[c] = false;
+    const bool open = e < E && ((gm >> G.lane_of(G.of(e))) & 1);
+    key[c] = open ? score_key(sm.srow[e]) : 0u;
   }
-  const int pool = take * gs;
-  float kth = 0.f, nxt = -CUDART_INF_F;
+  Top r{0u, 0.f, -CUDART_INF_F};
 #pragma unroll 1
-  for (int r = 0; r < min(k + 1, pool); ++r) {
+  for (int i = 0; i < min(k + 1, G.take * G.gs); ++i) {
     uint32_t best = 0;
     int id = 0x7fffffff;
 #pragma unroll
@@ -184,86 +164,342 @@ __device__ __forceinline__ void gate_token_grouped(const GateParams& p, int n_gr
       if (key[c] >= best) { best = key[c]; id = lane + 32 * c; }
     const uint32_t top = __reduce_max_sync(0xffffffffu, best);
     id = (int)__reduce_min_sync(0xffffffffu, best == top ? (unsigned)id : 0x7fffffffu);
-    if (r == k - 1) kth = key_score(top);
-    if (r == k) nxt = key_score(top);
+    if (i == k - 1) r.kth = key_score(top);
+    if (i == k) r.nxt = key_score(top);
+    const bool won = (id & 31) == lane;
+    if (won && i < k) r.chosen |= 1u << (id >> 5);
 #pragma unroll
     for (int c = 0; c < NC; ++c)
-      if (lane + 32 * c == id) {
-        key[c] = 0u;
-        if (r < k) chosen[c] = true;
-      }
+      if (won && (id >> 5) == c) key[c] = 0u;
   }
-  if (k < pool && kth - nxt <= kTau) {
-    // experts within the margin of the boundary are re-scored; the ones clear of it stay
-    if (flag == 0) flag = 1;
-    bool band[NC];
-    int n_def = 0;
-#pragma unroll
-    for (int c = 0; c < NC; ++c) {
-      const bool d = chosen[c] && sc[c] - nxt > kTau;
-      band[c] = open[c] && !d && sc[c] >= kth - kTau;
-      chosen[c] = d;
-      n_def += __popc(__ballot_sync(0xffffffffu, d));
-    }
+  return r;
+}
+
+// The chosen in ascending id order, lane j the j-th, and their weights (those of gate_finish,
+// which has one lane do it, summed in the same order).
+__device__ __noinline__ void finish_token(const GateParams& p, int t, GroupSmem& sm,
+                                          unsigned chosen, int flag) {
+  const int lane = threadIdx.x & 31, E = p.E, k = p.k;
+  const bool sig = p.mode == MOE_GATING_SIGMOID_BIAS_RENORM;
+  int base = 0;
 #pragma unroll 1
-    for (int c = 0; c < NC; ++c) {
-      unsigned m = 0;
+  for (int c = 0; 32 * c < E; ++c) {
+    const unsigned m = __ballot_sync(0xffffffffu, (chosen >> c) & 1);
+    if ((chosen >> c) & 1) sm.ids[base + __popc(m & ((1u << lane) - 1u))] = lane + 32 * c;
+    base += __popc(m);
+  }
+  __syncwarp();
+  const int id = lane < k ? sm.ids[lane] : 0;
+  const float lj = lane < k ? sm.lrow[id] : -CUDART_INF_F;
+  const bool all = p.mode == MOE_GATING_SOFTMAX;
+  float v, denom = 0.f;
+  if (sig) {
+    v = 1.f / (1.f + expf(-lj));
+  } else {
+    float top = lj;
+    if (all)
+#pragma unroll 1
+      for (int e = lane; e < E; e += 32) top = fmaxf(top, sm.lrow[e]);
+    top = warp_max(top);
+    v = expf(lj - top);
+    if (all) {
+#pragma unroll 1
+      for (int e = lane; e < E; e += 32) denom += expf(sm.lrow[e] - top);
+      denom = warp_sum(denom);
+    }
+  }
+  if (!all)
+#pragma unroll 1
+    for (int j = 0; j < k; ++j) denom += __shfl_sync(0xffffffffu, v, j);
+  // a token whose chosen scores are all zero (every expert left to it is masked) would get
+  // 0 / 0: its weights are zero instead
+  const float has = lane >= k ? 0.f : sig ? v : (lj == -CUDART_INF_F ? 0.f : 1.f);
+  const bool none = __all_sync(0xffffffffu, has == 0.f);
+  if (lane < k) {
+    p.ids[(size_t)t * k + lane] = id;
+    if (p.ids_local) p.ids_local[lane] = id;
+    p.w[(size_t)t * k + lane] = none ? 0.f : v * (p.scale / denom);
+    atomicAdd(&p.hist[(t / kTileT) * E + id], 1);
+  }
+  if (lane == 0 && p.tie_flags) p.tie_flags[t] = flag;
+  __syncwarp();
+}
+
+// Gating of token t by one warp when no boundary is near; returns false, with the scores in sm
+// and nothing chosen, when one is.
+template <int NC>
+__device__ __forceinline__ bool gate_quick(const GateParams& p, const Groups& G, int t,
+                                           const float* raw, GroupSmem& sm) {
+  score_token<NC>(p, t, raw, sm);
+  const GroupRank r = rank_groups(G, sm);
+  if (r.kth - r.nxt <= (G.pairs ? 2.f * kTau : kTau)) return false;
+  const unsigned lead = __ballot_sync(0xffffffffu, r.rank < G.take);
+  const Top top = top_experts<NC>(G, sm, lead, p.E, p.k);
+  if (top.kth - top.nxt <= kTau) return false;
+  finish_token(p, t, sm, top.chosen, 0);
+  return true;
+}
+
+// Re-scoring of near-boundary experts by the whole CTA.  The token's warp lists the experts it
+// needs; all threads share each dot product (their loads in flight together: one memory latency
+// an expert where a warp by itself would wait for dozens); then the token's warp turns them into
+// fp64 scores, an expert per lane (fp64 functions are slow here, once for all lanes).  One token
+// in a hundred needs it, and one that is slow sets the time of the kernel.
+constexpr int kBatch = 16;
+struct Service {
+  int n, token;                // n = 0: nothing more
+  int list[kMaxExperts];
+  float2 part[kBatch][32];     // per expert of a batch and warp: (hi, lo) of its share
+};
+
+// All the CTA's threads: their shares of x[token] . W_r[:, list[i0 + i]] in compensated fp32 (as
+// exact_score's), thread i the 8-element chunks i, i + threads, ...
+__device__ __noinline__ void dots(const GateParams& p, Service& sv, int i0) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x;
+  const uint16_t* xr = p.x + (size_t)sv.token * p.H;
+  const int n = min(sv.n - i0, kBatch), nch = p.H / 8;
+#pragma unroll 1
+  for (int i = 0; i < n; ++i) {
+    const int b = sv.list[i0 + i];
+    float hi = 0.f, lo = 0.f;
+#pragma unroll 1
+    for (int c0 = tid; c0 < nch; c0 += 4 * nt) {
+      uint4 xq[4];
+      float4 wa[4], wb[4];
 #pragma unroll
-      for (int c2 = 0; c2 < NC; ++c2) {
-        const unsigned b = __ballot_sync(0xffffffffu, band[c2]);
-        m = c2 == c ? b : m;
+      for (int j = 0; j < 4; ++j) {
+        const int c = c0 + j * nt;
+        xq[j] = make_uint4(0u, 0u, 0u, 0u);
+        wa[j] = wb[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (c >= nch) continue;
+        xq[j] = __ldg(reinterpret_cast<const uint4*>(xr + 8 * c));
+        if (p.w_rT) {
+          const float4* w = reinterpret_cast<const float4*>(p.w_rT + (size_t)b * p.H + 8 * c);
+          wa[j] = w[0];
+          wb[j] = w[1];
+        } else {
+          const float* w = p.w_r + (size_t)8 * c * p.E + b;
+          const size_t E = p.E;
+          wa[j] = make_float4(w[0], w[E], w[2 * E], w[3 * E]);
+          wb[j] = make_float4(w[4 * E], w[5 * E], w[6 * E], w[7 * E]);
+        }
       }
-      for (; m; m &= m - 1) rescored(p, t, 32 * c + __ffs(m) - 1, lane, sm);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 x01 = bf16x2_to_float2(xq[j].x), x23 = bf16x2_to_float2(xq[j].y);
+        const float2 x45 = bf16x2_to_float2(xq[j].z), x67 = bf16x2_to_float2(xq[j].w);
+        dot_term(hi, lo, x01.x, wa[j].x);
+        dot_term(hi, lo, x01.y, wa[j].y);
+        dot_term(hi, lo, x23.x, wa[j].z);
+        dot_term(hi, lo, x23.y, wa[j].w);
+        dot_term(hi, lo, x45.x, wb[j].x);
+        dot_term(hi, lo, x45.y, wb[j].y);
+        dot_term(hi, lo, x67.x, wb[j].z);
+        dot_term(hi, lo, x67.y, wb[j].w);
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const float h2 = __shfl_xor_sync(0xffffffffu, hi, o);
+      const float l2 = __shfl_xor_sync(0xffffffffu, lo, o);
+      df_add(hi, lo, h2, l2);
+    }
+    if (lane == 0) sv.part[i][warp] = make_float2(hi, lo);
+  }
+  __syncthreads();
+}
+// The asking warp: exact scores of the experts e of token t with srow[e] >= lo(e) that are
+// open(e) and have none yet.
+template <class Want>
+__device__ __forceinline__ void rescore(const GateParams& p, int t, GroupSmem& sm, Service& sv,
+                                        Want want) {
+  const int lane = threadIdx.x & 31;
+  int n = 0;
+#pragma unroll 1
+  for (int c = 0; 32 * c < p.E; ++c) {
+    const int e = lane + 32 * c;
+    const bool asked = want(min(e, p.E - 1));       // (all lanes call it: it may shuffle)
+    const bool w = e < p.E && asked && sm.exact_s[e] != sm.exact_s[e];
+    const unsigned m = __ballot_sync(0xffffffffu, w);
+    if (w) sv.list[n + __popc(m & ((1u << lane) - 1u))] = e;
+    n += __popc(m);
+  }
+  if (n == 0) return;
+  if (lane == 0) {
+    sv.n = n;
+    sv.token = t;
+  }
+#pragma unroll 1
+  for (int i0 = 0; i0 < n; i0 += kBatch) {
+    __syncthreads();
+    dots(p, sv, i0);
+    if (lane < min(n - i0, kBatch)) {
+      const int e = sv.list[i0 + lane];
+      float hi = 0.f, lo = 0.f;
+#pragma unroll 1
+      for (int w = 0; w < (int)(blockDim.x >> 5); ++w)
+        df_add(hi, lo, sv.part[lane][w].x, sv.part[lane][w].y);
+      double d = (double)hi + (double)lo;
+      if (p.logit_bias) d += (double)p.logit_bias[e];
+      if (p.mode == MOE_GATING_SIGMOID_BIAS_RENORM) {
+        d = 1.0 / (1.0 + exp(-d));
+        if (p.sel_bias) d += (double)p.sel_bias[e];
+      }
+      sm.exact_s[e] = d != d ? -CUDART_INF : d;
+    }
+    __syncwarp();
+  }
+}
+
+// Gating of token t (scores in sm) with the boundaries that are near decided by exact scores.
+template <int NC>
+__device__ __noinline__ void gate_slow(const GateParams& p, const Groups& G, int t, GroupSmem& sm,
+                                       Service& sv) {
+  const int lane = threadIdx.x & 31, E = p.E, k = p.k, g = lane / G.P;
+#pragma unroll 1
+  for (int e = lane; e < E; e += 32) sm.exact_s[e] = CUDART_NAN;
+  __syncwarp();
+  int flag = 0;
+  const GroupRank r = rank_groups(G, sm);
+  bool kept = r.rank < G.take;
+  const float tau = G.pairs ? 2.f * kTau : kTau;
+  if (r.kth - r.nxt <= tau) {
+    flag = 1;
+    // groups clear of the boundary stay; the band is decided by its exact scores
+    const bool in = g < G.n, def = kept && r.score - r.nxt > tau;
+    const bool band = in && !def && r.score >= r.kth - tau;
+    const unsigned bm = __ballot_sync(0xffffffffu, band);
+    rescore(p, t, sm, sv, [&](int e) {
+      const int ll = G.lane_of(G.of(e));
+      const float lo = __shfl_sync(0xffffffffu, r.least, ll);
+      return ((bm >> ll) & 1) && sm.srow[e] >= lo;
+    });
+    double x1 = -CUDART_INF, x2 = -CUDART_INF;
+    if (band)
+#pragma unroll 1
+      for (int i = 0; i < G.gs; ++i) {
+        const int e = g * G.gs + i;
+        if (!(sm.srow[e] >= r.least)) continue;
+        const double s = sm.exact_s[e];
+        if (s > x1) { x2 = x1; x1 = s; }
+        else if (s > x2) x2 = s;
+      }
+    const double gx = G.pairs ? x1 + x2 : x1;
+    int clear = 0, rank = 0;
+    double last = CUDART_INF, first = -CUDART_INF;   // the band's worst taken, best left
+#pragma unroll 1
+    for (int q = 0; q < G.n; ++q) {
+      clear += (int)__shfl_sync(0xffffffffu, (int)def, G.lane_of(q));
+      const double o = __shfl_sync(0xffffffffu, gx, G.lane_of(q));
+      rank += ((bm >> G.lane_of(q)) & 1) && better_d(o, q, gx, g);
+    }
+    kept = def || (band && rank < G.take - clear);
+#pragma unroll 1
+    for (int q = 0; q < G.n; ++q) {
+      const double o = __shfl_sync(0xffffffffu, gx, G.lane_of(q));
+      const int tk = __shfl_sync(0xffffffffu, (int)kept, G.lane_of(q));
+      if (!((bm >> G.lane_of(q)) & 1)) continue;
+      if (tk) last = o < last ? o : last;
+      else first = o > first ? o : first;
+    }
+    if (last - first < kNearTie) flag = 2;
+  }
+  const unsigned gm = __ballot_sync(0xffffffffu, kept);
+  Top top = top_experts<NC>(G, sm, gm, E, k);
+  if (top.kth - top.nxt <= kTau) {
+    if (flag == 0) flag = 1;
+    // experts clear of the boundary stay; the band is decided by its exact scores
+    const float lo = top.kth - kTau;
+    auto in_band = [&](int e) {
+      const float s = sm.srow[e];
+      return ((gm >> G.lane_of(G.of(e))) & 1) && !(s - top.nxt > kTau) && s >= lo;
+    };
+    rescore(p, t, sm, sv, in_band);
+    unsigned chosen = 0, band = 0;
+    int clear = 0;
+#pragma unroll 1
+    for (int c = 0; 32 * c < E; ++c) {
+      const int e = lane + 32 * c;
+      const bool b = e < E && in_band(e), d = ((top.chosen >> c) & 1) && !b;
+      band |= (unsigned)b << c;
+      chosen |= (unsigned)d << c;
+      clear += __popc(__ballot_sync(0xffffffffu, d));
     }
     double last = CUDART_INF;
-    for (int r = n_def; r <= k; ++r) {   // the last round finds the best one left out
+#pragma unroll 1
+    for (int i = clear; i <= k; ++i) {   // the last round finds the best one left out
       double bs = -CUDART_INF;
       int bi = 0x7fffffff;
-#pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        const int e = lane + 32 * c;
-        if (band[c] && !chosen[c] && better_d(sm.exact_s[e], e, bs, bi)) {
+#pragma unroll 1
+      for (unsigned m = band & ~chosen; m; m &= m - 1) {
+        const int e = lane + 32 * (__ffs(m) - 1);
+        if (better_d(sm.exact_s[e], e, bs, bi)) {
           bs = sm.exact_s[e];
           bi = e;
         }
       }
-      warp_argmax_d(bs, bi);
-      if (r == k) {
+#pragma unroll 1
+      for (int o = 16; o > 0; o >>= 1) {
+        const double so = __shfl_xor_sync(0xffffffffu, bs, o);
+        const int io = __shfl_xor_sync(0xffffffffu, bi, o);
+        if (better_d(so, io, bs, bi)) {
+          bs = so;
+          bi = io;
+        }
+      }
+      if (i == k) {
         if (bi != 0x7fffffff && last - bs < kNearTie) flag = 2;
         break;
       }
       last = bs;
-#pragma unroll
-      for (int c = 0; c < NC; ++c)
-        if (lane + 32 * c == bi) chosen[c] = true;
+      if ((bi & 31) == lane && bi != 0x7fffffff) chosen |= 1u << (bi >> 5);
     }
+    top.chosen = chosen;
   }
-  __syncwarp();
-  gate_finish<NC>(p, t, l, chosen, sm.lrow, flag);
-  // a token whose chosen scores are all zero (every expert left to it is masked) would get
-  // 0 / 0: its weights are zero instead
-  __syncwarp();
-  float left = 0.f;
-  if (lane < k) {
-    const float lj = sm.lrow[p.ids[(size_t)t * k + lane]];
-    left = sig ? 1.f / (1.f + expf(-lj)) : (lj == -CUDART_INF_F ? 0.f : 1.f);
+  finish_token(p, t, sm, top.chosen, flag);
+}
+
+// The tokens of the CTA's warps that need re-scoring (bit w of `slow`: warp w's, t0 + w), one after
+// another, each by its own warp with the others serving.  All threads call it.
+template <int NC>
+__device__ __forceinline__ void gate_slow_all(const GateParams& p, const Groups& G, int t0,
+                                              unsigned slow, GroupSmem* sm, Service& sv) {
+  const int warp = threadIdx.x >> 5;
+#pragma unroll 1
+  for (; slow; slow &= slow - 1) {
+    const int w = __ffs(slow) - 1;
+    if (warp == w) {
+      gate_slow<NC>(p, G, t0 + w, sm[w], sv);
+      if ((threadIdx.x & 31) == 0) sv.n = 0;
+      __syncthreads();
+    } else {
+      for (int i0 = 0;;) {
+        __syncthreads();
+        if (sv.n == 0) break;
+        dots(p, sv, i0);
+        i0 = i0 + kBatch < sv.n ? i0 + kBatch : 0;
+      }
+    }
+    __syncthreads();
   }
-  if (__all_sync(0xffffffffu, left == 0.f) && lane < k) p.w[(size_t)t * k + lane] = 0.f;
 }
 
 template <int NC>
 __global__ void __launch_bounds__(G_WARPS * 32)
-gate_group_kernel(GateParams p, int n_group, int take) {
+gate_group_kernel(const __grid_constant__ GateParams p, int n_group, int take) {
   pdl_trigger();
   pdl_wait();
   __shared__ GroupSmem sm[G_WARPS];
-  const int warp = threadIdx.x >> 5;
-  for (int it = 0; it < p.tok_per_warp; ++it) {
-    const int t = (blockIdx.x * G_WARPS + warp) * p.tok_per_warp + it;
-    if (t >= p.T) break;
-    gate_token_grouped<NC>(p, n_group, take, t, nullptr, sm[warp]);
-    __syncwarp();
-  }
+  __shared__ Service sv;
+  __shared__ unsigned slow;
+  const int warp = threadIdx.x >> 5, t0 = blockIdx.x * G_WARPS, t = t0 + warp;
+  const Groups G(n_group, take, p.E, p.mode == MOE_GATING_SIGMOID_BIAS_RENORM);
+  if (threadIdx.x == 0) slow = 0;
+  __syncthreads();
+  if (t < p.T && !gate_quick<NC>(p, G, t, nullptr, sm[warp]) && (threadIdx.x & 31) == 0)
+    atomicOr(&slow, 1u << warp);
+  __syncthreads();
+  gate_slow_all<NC>(p, G, t0, slow, sm, sv);
 }
 
 // Everything after the router product for a batch of at most kSmallT tokens in one CTA, as
@@ -273,6 +509,8 @@ constexpr int kTailWarps = 32;
 struct GroupTailSmem {
   TailSmem tail;                 // (lrow / exact_s unused)
   GroupSmem g[kSmallT];
+  Service sv;
+  unsigned slow;
 };
 __global__ void __launch_bounds__(kTailWarps * 32)
 route_group_tail_kernel(GateParams p, int n_group, int take, int32_t* __restrict__ counts,
@@ -302,14 +540,16 @@ route_group_tail_kernel(GateParams p, int n_group, int take, int32_t* __restrict
     if (g == 0 && li < n) sm.tail.lg[li] = v;
   }
   for (int e = tid; e < kMaxExperts; e += NT) sm.tail.hist[e] = 0;
+  if (tid == 0) sm.slow = 0;
   __syncthreads();
-  if (warp < T) {
-    GateParams q = p;
-    q.hist = sm.tail.hist;
-    const float* raw = sm.tail.lg + (size_t)warp * C;
-    if (E <= 64) gate_token_grouped<2>(q, n_group, take, warp, raw, sm.g[warp]);
-    else gate_token_grouped<EC>(q, n_group, take, warp, raw, sm.g[warp]);
-  }
+  GateParams q = p;
+  q.hist = sm.tail.hist;
+  const Groups grp(n_group, take, E, p.mode == MOE_GATING_SIGMOID_BIAS_RENORM);
+  if (warp < T && !gate_quick<EC>(q, grp, warp, sm.tail.lg + (size_t)warp * C, sm.g[warp]) &&
+      (tid & 31) == 0)
+    atomicOr(&sm.slow, 1u << warp);
+  __syncthreads();
+  gate_slow_all<EC>(q, grp, 0, sm.slow, sm.g, sm.sv);
   __syncthreads();
   route_dispatch_block<NT>(p.ids, T, p.k, E, counts, offsets, pos, src, active, n_active,
                            shared_meta, x_perm, p.x, p.H, sm.tail);
@@ -337,9 +577,8 @@ int launch_route_group_tail(const GateParams& p, int n_group, int take, int32_t*
 }
 
 int launch_gate_group(const GateParams& p, int n_group, int take, cudaStream_t st) {
-  GateParams q = p;
-  q.tok_per_warp = 1;
-  const dim3 grid(ceil_div(q.T, G_WARPS * q.tok_per_warp)), block(G_WARPS * 32);
+  const GateParams& q = p;
+  const dim3 grid(ceil_div(q.T, G_WARPS)), block(G_WARPS * 32);
   if (q.E <= 32) MOE_LAUNCH_PDL(gate_group_kernel<1>, grid, block, 0, st, q, n_group, take);
   else if (q.E <= 64) MOE_LAUNCH_PDL(gate_group_kernel<2>, grid, block, 0, st, q, n_group, take);
   else if (q.E <= 128) MOE_LAUNCH_PDL(gate_group_kernel<4>, grid, block, 0, st, q, n_group, take);
