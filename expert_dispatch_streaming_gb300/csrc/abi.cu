@@ -76,8 +76,11 @@ static int route_topk(const uint16_t* x, const float* w_r, const float* logit_bi
   MOE_REQUIRE(c.ok());
   // the error word (first 4 bytes of ws) starts every call at zero; only the tensor-core
   // router's bounded waits (T >= 256) can set it
-  MOE_CUDA_TRY(cudaMemsetAsync(err, 0, sizeof(int32_t), (cudaStream_t)stream));
+  // (a small group-limited batch's last kernel clears it: a launch less)
+  const bool clear = n_group && rp.small;
+  if (!clear) MOE_CUDA_TRY(cudaMemsetAsync(err, 0, sizeof(int32_t), (cudaStream_t)stream));
   RouteArgs a{};
+  a.clear_err = clear;
   a.x = x; a.w_r = w_r; a.logit_bias = logit_bias; a.sel_bias = sel_bias; a.w_gate = w_gate;
   a.forced = forced_ids; a.T = T; a.H = H; a.E = E; a.k = k; a.gating = gating;
   a.scale = scale; a.ids = ids; a.counts = counts; a.offsets = offsets; a.pos = pos;

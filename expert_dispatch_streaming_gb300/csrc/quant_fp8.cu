@@ -28,7 +28,9 @@ quantize_fp8_kernel(const uint16_t* __restrict__ x, const int32_t* __restrict__ 
   const long long item = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
   const int lane = threadIdx.x & 31;
   if (item >= (long long)rows * parts) return;
-  const int row = (int)(item / parts), c0 = (int)(item % parts) * kCols + 16 * lane;
+  // all rows' first columns, then the next: a gathered x row is read k times, and 2 KB of every
+  // row at a time stay in L2 where whole rows (117 MB at 8192 x 7168) would not
+  const int row = (int)(item % rows), c0 = (int)(item / rows) * kCols + 16 * lane;
   int from = row;
   if (src) {
     const int s = __ldg(src + row);

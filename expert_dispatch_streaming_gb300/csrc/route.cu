@@ -504,7 +504,8 @@ int launch_route(const RouteArgs& a, const RoutePlan& r, const RouteScratch& s,
       p.shared_gate = a.shared_gate; p.tie_flags = a.tie_flags; p.hist = nullptr;
       if (a.n_group)
         return launch_route_group_tail(p, a.n_group, a.take, a.counts, a.offsets, a.pos, a.src,
-                                       s.active, s.n_active, s.shared_meta, a.x_perm, st);
+                                       s.active, s.n_active, s.shared_meta, a.x_perm,
+                                       a.clear_err ? a.err : nullptr, st);
       MOE_LAUNCH_PDL(route_tail_kernel, dim3(1), dim3(kTailThreads), 0, st, p, a.counts,
                      a.offsets, a.pos, a.src, s.active, s.n_active, s.shared_meta, a.x_perm);
       MOE_COUNT_LAUNCH();

@@ -77,6 +77,7 @@ struct RouteArgs {
   uint16_t* x_perm;  // nullable: fused gather into expert order
   int32_t* err;      // device error word (bounded waits of the tensor-core router)
   int n_group, take; // group-limited selection: `take` of n_group groups; 0 = no groups
+  int clear_err;     // group-limited, small batch: the kernels clear *err themselves
 };
 
 RoutePlan plan_route(int T, int H, int E, int k, bool has_gate);
@@ -89,7 +90,7 @@ int launch_gate_group(const GateParams& p, int n_group, int take, cudaStream_t s
 int launch_route_group_tail(const GateParams& p, int n_group, int take, int32_t* counts,
                             int32_t* offsets, int32_t* pos, int32_t* src, int32_t* active,
                             int32_t* n_active, int32_t* shared_meta, uint16_t* x_perm,
-                            cudaStream_t st);
+                            int32_t* err, cudaStream_t st);
 int launch_gather(const uint16_t* x, const int32_t* src, int rows, int k, int H,
                   uint16_t* x_perm, cudaStream_t st);
 

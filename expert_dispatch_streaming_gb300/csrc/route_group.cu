@@ -503,21 +503,23 @@ gate_group_kernel(const __grid_constant__ GateParams p, int n_group, int take) {
 }
 
 // Everything after the router product for a batch of at most kSmallT tokens in one CTA, as
-// route_tail_kernel: the slices of every logit summed (G lanes a logit, fixed order), one warp a
-// token gating, then the histogram, scan, ranks and tables (route_dispatch_block).
+// route_tail_kernel: the slices of every logit summed in a fixed order, one warp a token gating,
+// then the counts, scan, ranks and tables.  err: an error word to clear (NULL: none).
 constexpr int kTailWarps = 32;
 struct GroupTailSmem {
   TailSmem tail;                 // (lrow / exact_s unused)
   GroupSmem g[kSmallT];
   Service sv;
   unsigned slow;
+  float sum[kTailWarps * 32];
+  int wcnt[kMaxExperts / 32], wact[kMaxExperts / 32];
 };
 __global__ void __launch_bounds__(kTailWarps * 32)
 route_group_tail_kernel(GateParams p, int n_group, int take, int32_t* __restrict__ counts,
                         int32_t* __restrict__ offsets, int32_t* __restrict__ pos,
                         int32_t* __restrict__ src, int32_t* __restrict__ active,
                         int32_t* __restrict__ n_active, int32_t* __restrict__ shared_meta,
-                        uint16_t* __restrict__ x_perm) {
+                        uint16_t* __restrict__ x_perm, int32_t* __restrict__ err) {
   pdl_trigger();
   pdl_wait();
   extern __shared__ __align__(16) uint8_t raw_smem[];
@@ -525,19 +527,34 @@ route_group_tail_kernel(GateParams p, int n_group, int take, int32_t* __restrict
   constexpr int NT = kTailWarps * 32;
   const int tid = threadIdx.x, warp = tid >> 5, T = p.T, C = p.C, E = p.E, S = p.S, n = T * C;
   const size_t stride = (size_t)T * C;
-  int G = 32;
-  while (G > 1 && n * G > NT) G >>= 1;
-  const int per = NT / G, g = tid % G;
-  for (int li = tid / G; li < ((n + per - 1) / per) * per; li += per) {
+  if (tid == 0 && err) *err = 0;
+  // the logits: thread (g, li) sums slices g, g + G, ... of logit li (their loads in flight
+  // together, neighbouring logits side by side), then the G sums in order
+  const int G = max(1, NT / n);
+  for (int i = tid; i < n * G; i += NT) {
+    const int li = i % n, g = i / n;
     float a[4] = {0.f, 0.f, 0.f, 0.f};
-    if (li < n) {
-      int sp = g, i = 0;
-#pragma unroll 4
-      for (; sp < S; sp += G, ++i) a[i & 3] += __ldcg(p.part + (size_t)sp * stride + li);
+    const float* q = p.part + li;
+    int sp = g;
+    for (; sp + 7 * G < S; sp += 8 * G) {
+      float v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = __ldcg(q + (size_t)(sp + j * G) * stride);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) a[j & 3] += v[j];
     }
-    float v = (a[0] + a[1]) + (a[2] + a[3]);
-    for (int o = G >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    if (g == 0 && li < n) sm.tail.lg[li] = v;
+    for (int j = 0; sp < S; sp += G, ++j) a[j & 3] += __ldcg(q + (size_t)sp * stride);
+    const float v = (a[0] + a[1]) + (a[2] + a[3]);
+    if (G == 1) sm.tail.lg[li] = v;
+    else sm.sum[i] = v;
+  }
+  if (G > 1) {
+    __syncthreads();
+    for (int li = tid; li < n; li += NT) {
+      float v = 0.f;
+      for (int g = 0; g < G; ++g) v += sm.sum[g * n + li];
+      sm.tail.lg[li] = v;
+    }
   }
   for (int e = tid; e < kMaxExperts; e += NT) sm.tail.hist[e] = 0;
   if (tid == 0) sm.slow = 0;
@@ -551,8 +568,65 @@ route_group_tail_kernel(GateParams p, int n_group, int take, int32_t* __restrict
   __syncthreads();
   gate_slow_all<EC>(q, grp, 0, sm.slow, sm.g, sm.sv);
   __syncthreads();
-  route_dispatch_block<NT>(p.ids, T, p.k, E, counts, offsets, pos, src, active, n_active,
-                           shared_meta, x_perm, p.x, p.H, sm.tail);
+  // ---- counts, offsets, the experts with rows: a thread an expert, scans by warp and over the
+  // eight warps
+  const int lane = tid & 31, k = p.k;
+  int cnt = 0, incl = 0;
+  unsigned act = 0;
+  if (warp < kMaxExperts / 32) {
+    cnt = tid < E ? sm.tail.hist[tid] : 0;
+    incl = cnt;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    act = __ballot_sync(0xffffffffu, cnt > 0);
+    if (lane == 31) {
+      sm.wcnt[warp] = incl;
+      sm.wact[warp] = __popc(act);
+    }
+  }
+  __syncthreads();
+  if (warp < kMaxExperts / 32) {
+    int before = 0, seen = 0;
+    for (int w = 0; w < warp; ++w) {
+      before += sm.wcnt[w];
+      seen += sm.wact[w];
+    }
+    const int at = before + incl - cnt;
+    seen += __popc(act & ((1u << lane) - 1u));
+    sm.tail.excl[tid] = at;
+    if (tid < E) {
+      counts[tid] = cnt;
+      offsets[tid] = at;
+      if (cnt) active[seen] = tid;
+      if (tid == E - 1) {
+        offsets[E] = at + cnt;
+        *n_active = seen + (cnt > 0);
+      }
+    }
+  }
+  if (tid < 4) shared_meta[tid] = tid == 1 ? T : tid == 3 ? 1 : 0;
+  __syncthreads();
+  // ---- stable ranks: pair i goes after every earlier pair of its expert
+  if (tid < T * k) {
+    const int e = __ldcg(p.ids + tid);
+    int rank = 0;
+    for (int i = 0; i < tid; ++i) rank += __ldcg(p.ids + i) == e;
+    const int pp = sm.tail.excl[e] + rank;
+    pos[tid] = pp;
+    src[pp] = tid;
+    sm.tail.srow[pp] = tid / k;
+  }
+  if (!x_perm) return;
+  __syncthreads();
+  const int nvec = p.H / 8;
+  for (int i = tid; i < T * k * nvec; i += NT) {
+    const int r = i / nvec, v = i % nvec;
+    reinterpret_cast<uint4*>(x_perm + (size_t)r * p.H)[v] =
+        __ldg(reinterpret_cast<const uint4*>(p.x + (size_t)sm.tail.srow[r] * p.H) + v);
+  }
 }
 
 }  // namespace
@@ -560,7 +634,7 @@ route_group_tail_kernel(GateParams p, int n_group, int take, int32_t* __restrict
 int launch_route_group_tail(const GateParams& p, int n_group, int take, int32_t* counts,
                             int32_t* offsets, int32_t* pos, int32_t* src, int32_t* active,
                             int32_t* n_active, int32_t* shared_meta, uint16_t* x_perm,
-                            cudaStream_t st) {
+                            int32_t* err, cudaStream_t st) {
   static bool attr = false;
   if (!attr) {
     MOE_CUDA_TRY(cudaFuncSetAttribute(route_group_tail_kernel,
@@ -570,7 +644,7 @@ int launch_route_group_tail(const GateParams& p, int n_group, int take, int32_t*
   }
   MOE_LAUNCH_PDL(route_group_tail_kernel, dim3(1), dim3(kTailWarps * 32), sizeof(GroupTailSmem),
                  st, p, n_group, take, counts, offsets, pos, src, active, n_active, shared_meta,
-                 x_perm);
+                 x_perm, err);
   MOE_COUNT_LAUNCH();
   MOE_LAUNCH_CHECK();
   return MOE_OK;
