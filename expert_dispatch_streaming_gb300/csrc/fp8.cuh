@@ -6,8 +6,6 @@
 // zeros has zero codes).  A NaN stays a NaN code and does not move its block's scale; an
 // infinity makes s infinite, so its block reads NaN.
 #pragma once
-#include <cuda_fp8.h>
-
 #include "expert_ffn.cuh"
 
 namespace moe {
@@ -17,13 +15,16 @@ constexpr float kFp8Max = 448.f;
 constexpr float kFp8MinAmax = 0x1p-96f;
 constexpr int kFp8TileBytes = 16384;    // 128 rows x 128 k
 
-// Four floats times inv -> four E4M3 codes (round to nearest even, saturating).
+// Four floats times inv -> four E4M3 codes (round to nearest even, saturating), the first in the
+// low byte.  (The instruction takes its second operand as the low half; written out, the two
+// conversions merge into one register without extracting and shifting 16-bit values.)
 __device__ __forceinline__ uint32_t fp8_pack4(float a, float b, float c, float d, float inv) {
-  const uint32_t lo =
-      __nv_cvt_float2_to_fp8x2(make_float2(a * inv, b * inv), __NV_SATFINITE, __NV_E4M3);
-  const uint32_t hi =
-      __nv_cvt_float2_to_fp8x2(make_float2(c * inv, d * inv), __NV_SATFINITE, __NV_E4M3);
-  return lo | (hi << 16);
+  uint32_t r;
+  asm("{\n.reg .b16 l, h;\ncvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n"
+      "cvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\nmov.b32 %0, {l, h};\n}\n"
+      : "=r"(r)
+      : "f"(a * inv), "f"(b * inv), "f"(c * inv), "f"(d * inv));
+  return r;
 }
 
 inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }

@@ -14,7 +14,9 @@ constexpr int kCols = 1024;
 
 __device__ __forceinline__ uint32_t abs_max2(uint32_t a, uint32_t b) {
   uint32_t d;
-  asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a & 0x7FFF7FFFu), "r"(b & 0x7FFF7FFFu));
+  asm("{\n.reg .b32 s, t;\nabs.bf16x2 s, %1;\nabs.bf16x2 t, %2;\nmax.bf16x2 %0, s, t;\n}\n"
+      : "=r"(d)
+      : "r"(a), "r"(b));
   return d;
 }
 
@@ -24,13 +26,11 @@ quantize_fp8_kernel(const uint16_t* __restrict__ x, const int32_t* __restrict__ 
                     float* __restrict__ scale) {
   pdl_trigger();
   pdl_wait();
-  const int parts = (H + kCols - 1) / kCols;
-  const long long item = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-  const int lane = threadIdx.x & 31;
-  if (item >= (long long)rows * parts) return;
-  // all rows' first columns, then the next: a gathered x row is read k times, and 2 KB of every
-  // row at a time stay in L2 where whole rows (117 MB at 8192 x 7168) would not
-  const int row = (int)(item % rows), c0 = (int)(item / rows) * kCols + 16 * lane;
+  const int lane = threadIdx.x & 31, row = blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (row >= rows) return;
+  // (grid x first: all rows' first columns, then the next.  A gathered x row is read k times, and
+  // 2 KB of every row at a time stay in L2 where whole rows, 117 MB at 8192 x 7168, would not)
+  const int c0 = blockIdx.y * kCols + 16 * lane;
   int from = row;
   if (src) {
     const int s = __ldg(src + row);
@@ -47,30 +47,42 @@ quantize_fp8_kernel(const uint16_t* __restrict__ x, const int32_t* __restrict__ 
       v[h][1] = __ldg(p + 1);
     }
   }
+  // the blocks' largest magnitudes, both halves' pairs reduced side by side
+  uint32_t m2[2] = {0u, 0u};
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t w[8] = {v[h][0].x, v[h][0].y, v[h][0].z, v[h][0].w,
+                           v[h][1].x, v[h][1].y, v[h][1].z, v[h][1].w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m2[h] = abs_max2(m2[h], w[i]);
+  }
+  // each as one bf16: this half's in the low half-word, the other's in the high one
+  uint32_t mm = abs_max2(__byte_perm(m2[0], m2[1], 0x5410), __byte_perm(m2[0], m2[1], 0x7632));
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) mm = abs_max2(mm, __shfl_xor_sync(0xffffffffu, mm, o));
+  const float2 mf = bf16x2_to_float2(mm);
+  // one division a lane: of a block's eight lanes, the first four take 448 / amax and amax / 448
+  // of the two halves
+  const int kind = lane & 3;
+  const float m = fmaxf(kind < 2 ? mf.x : mf.y, kFp8MinAmax);
+  const float d = __fdiv_rn(kind & 1 ? m : kFp8Max, kind & 1 ? kFp8Max : m);
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const int col = c0 + 512 * h;
+    const float inv = __shfl_sync(0xffffffffu, d, (lane & 24) + 2 * h);
     const uint32_t w[8] = {v[h][0].x, v[h][0].y, v[h][0].z, v[h][0].w,
                            v[h][1].x, v[h][1].y, v[h][1].z, v[h][1].w};
-    uint32_t m2 = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) m2 = abs_max2(m2, w[i]);
-#pragma unroll
-    for (int o = 1; o < 8; o <<= 1) m2 = abs_max2(m2, __shfl_xor_sync(0xffffffffu, m2, o));
-    const float2 mf = bf16x2_to_float2(m2);
-    const float m = fmaxf(fmaxf(mf.x, mf.y), kFp8MinAmax);
-    const float inv = __fdiv_rn(kFp8Max, m);
     uint32_t o[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float2 a = bf16x2_to_float2(w[2 * i]), b = bf16x2_to_float2(w[2 * i + 1]);
       o[i] = fp8_pack4(a.x, a.y, b.x, b.y, inv);
     }
-    if (col < H) {
+    if (col < H)
       __stcs(reinterpret_cast<uint4*>(q + (size_t)row * H + col),
              make_uint4(o[0], o[1], o[2], o[3]));
-      if ((lane & 7) == 0) scale[(size_t)row * nb + (col >> 7)] = __fdiv_rn(m, kFp8Max);
-    }
+    if ((lane & 7) == 2 * h + 1 && col - 16 * (lane & 7) < H)
+      scale[(size_t)row * nb + (col >> 7)] = d;
   }
 }
 
@@ -92,10 +104,8 @@ pack_fp8_kernel(const uint8_t* __restrict__ w, int rows, int K, uint8_t* __restr
 int launch_quantize_fp8(const uint16_t* x, const int32_t* src, int rows, int k, int T, int H,
                         uint8_t* q, float* scale, cudaStream_t st) {
   if (rows <= 0) return MOE_OK;
-  const int nb = ceil_div(H, kFp8Block);
-  const long long items = (long long)rows * ceil_div(H, kCols);
-  MOE_LAUNCH_PDL(quantize_fp8_kernel, dim3((unsigned)((items + 7) / 8)), dim3(256), 0, st, x, src,
-                 rows, k, T, H, nb, q, scale);
+  MOE_LAUNCH_PDL(quantize_fp8_kernel, dim3(ceil_div(rows, 8), ceil_div(H, kCols)), dim3(256), 0,
+                 st, x, src, rows, k, T, H, ceil_div(H, kFp8Block), q, scale);
   MOE_COUNT_LAUNCH();
   MOE_LAUNCH_CHECK();
   return MOE_OK;
@@ -109,7 +119,7 @@ extern "C" {
 
 int moe_quantize_fp8(const uint16_t* x, const int32_t* src, int T, int k, int H, uint8_t* q,
                      float* scale, void* stream) {
-  MOE_REQUIRE(T >= 0 && H > 0 && H % 16 == 0);
+  MOE_REQUIRE(T >= 0 && H > 0 && H % 16 == 0 && H <= (1 << 24));
   MOE_REQUIRE(!src || (k >= 1 && (long long)T * k <= 0x7fffffffLL));
   if (T == 0) return MOE_OK;
   MOE_REQUIRE(x && q && scale && aligned16(x) && aligned16(q) && aligned4(scale) &&
