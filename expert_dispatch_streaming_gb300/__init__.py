@@ -26,6 +26,7 @@ MOE_ERR_NO_MEMORY = -7
 MOE_GATING_SOFTMAX_RENORM = 0
 MOE_GATING_SOFTMAX = 1
 MOE_GATING_SIGMOID_BIAS_RENORM = 2
+MOE_GATING_GROUPED = 16
 GATING = {"softmax_renorm": 0, "softmax": 1, "sigmoid_bias_renorm": 2}
 
 MOE_W_BF16 = 0
@@ -82,7 +83,8 @@ class moe_layer(C.Structure):
                 ("layer_index", C.c_int), ("shared_gate_sigmoid", C.c_int),
                 ("w_r", C.c_void_p), ("logit_bias", C.c_void_p), ("sel_bias", C.c_void_p),
                 ("w_gate", C.c_void_p), ("shared_bundle", C.c_void_p),
-                ("bundles", C.POINTER(C.c_void_p)), ("norm_eps", C.c_float)]
+                ("bundles", C.POINTER(C.c_void_p)), ("norm_eps", C.c_float),
+                ("n_group", C.c_int), ("topk_group", C.c_int)]
 
 
 MOE_N_PHASE_EVENTS = 6

@@ -10,6 +10,7 @@
 #include "common.cuh"
 #include "decode.cuh"
 #include "expert_ffn.cuh"
+#include "fp8.cuh"
 #include "route.cuh"
 #include "tc_gemm.cuh"
 
@@ -96,6 +97,8 @@ struct LayerScratch {
   int32_t *ids, *counts, *offsets, *pos, *src, *tie;
   float *w, *shared_gate;
   uint16_t *x_perm, *h, *y_perm, *h_s, *s;
+  uint8_t *xq, *hq, *xq_s, *hq_s;   // FP8 weights: quantised rows instead of x_perm, h, x, h_s,
+  float *xs, *hs, *xs_s, *hs_s;     // and their scales
   float* part;
   float* part_s;    // split-K partials of the shared expert when it shares a launch
   float *dec_rpart, *dec_gpart, *dec_dpart, *dec_ss;   // fused decode kernel scratch
@@ -107,6 +110,8 @@ struct LayerScratch {
 struct LayerPlan {
   RoutePlan rp;
   GemmPlan gu, dn, sgu, sdn;
+  int fp8;           // MOE_W_FP8_B128: the FP8 products and their plans, routed and shared
+  Fp8Plan qgu, qdn, qsgu, qsdn;
   moe_bundle_layout lay, slay;
   int merged;        // routed and shared expert share one tcgen05 launch per GEMM
   TcPair mgu, mdn;
@@ -132,15 +137,39 @@ static GemmArgs gemm_args(const moe_bundle_layout& lay, int wdtype, bool fused, 
   return a;
 }
 
+// FP8 product over a bundle section: K reduction elements, N outputs (fused: N gate + N up rows)
+static Fp8Args fp8_args(const moe_bundle_layout& lay, bool fused, int K, int N, int E,
+                        int max_rows) {
+  Fp8Args a{};
+  a.K = K; a.N = N; a.E = E; a.max_rows = max_rows; a.fused = fused; a.host_n = -1;
+  a.w_off = fused ? lay.gate_up_offset : lay.down_offset;
+  a.s_off = fused ? lay.gate_up_scale_offset : lay.down_scale_offset;
+  return a;
+}
+
+static bool grouped(const moe_layer* L) { return (L->gating & MOE_GATING_GROUPED) != 0; }
+
 static int make_plan(const moe_layer* L, int T, LayerPlan* P) {
-  if (!L || L->wdtype == MOE_W_FP8_B128 || !valid_route_shape(T, L->H, L->E, L->k) || L->I <= 0 || L->I % 128 ||
+  if (!L || !valid_route_shape(T, L->H, L->E, L->k) || L->I <= 0 || L->I % 128 ||
       L->H % 128 || L->Is < 0 || L->Is % 128)
+    return MOE_ERR_INVALID_ARG;
+  if (grouped(L) && !valid_groups(L->E, L->k, L->n_group, L->topk_group))
     return MOE_ERR_INVALID_ARG;
   if (moe_bundle_layout_of(L->H, L->I, L->wdtype, &P->lay) != MOE_OK) return MOE_ERR_INVALID_ARG;
   if (L->Is && moe_bundle_layout_of(L->H, L->Is, L->wdtype, &P->slay) != MOE_OK)
     return MOE_ERR_INVALID_ARG;
   const int rows = T * L->k;
   P->rp = plan_route(T, L->H, L->E, L->k, L->Is > 0 && L->shared_gate_sigmoid);
+  if (L->wdtype == MOE_W_FP8_B128) {
+    P->fp8 = 1;
+    P->qgu = plan_fp8(fp8_args(P->lay, true, L->H, L->I, L->E, rows));
+    P->qdn = plan_fp8(fp8_args(P->lay, false, L->I, L->H, L->E, rows));
+    if (L->Is) {
+      P->qsgu = plan_fp8(fp8_args(P->slay, true, L->H, L->Is, 1, T));
+      P->qsdn = plan_fp8(fp8_args(P->slay, false, L->Is, L->H, 1, T));
+    }
+    return MOE_OK;
+  }
   P->gu = plan_gemm(gemm_args(P->lay, L->wdtype, true, L->H, L->I, L->E, rows, T));
   P->dn = plan_gemm(gemm_args(P->lay, L->wdtype, false, L->I, L->H, L->E, rows, T));
   if (L->Is) {
@@ -159,8 +188,10 @@ static int make_plan(const moe_layer* L, int T, LayerPlan* P) {
       P->mdn = plan_tc_pair(gemm_args(P->lay, L->wdtype, false, L->I, L->H, L->E, rows, T), sdn);
     }
   }
-  P->dec = plan_decode(T, L->H, L->E, L->k, L->I, L->Is, L->wdtype,
-                       L->Is > 0 && L->shared_gate_sigmoid);
+  // (the fused decode kernel selects without groups)
+  if (!grouped(L))
+    P->dec = plan_decode(T, L->H, L->E, L->k, L->I, L->Is, L->wdtype,
+                         L->Is > 0 && L->shared_gate_sigmoid);
   return MOE_OK;
 }
 
@@ -172,7 +203,8 @@ static size_t carve(WsCursor& c, const moe_layer* L, int T, const LayerPlan& P, 
   z.err = c.take<int32_t>(64);
   size_t ce = std::max({P.gu.counter_elems, P.dn.counter_elems, P.sgu.counter_elems,
                         P.sdn.counter_elems, P.mgu.t1.counter_elems, P.mdn.t1.counter_elems,
-                        P.dec.ok ? P.dec.ctl_words : (size_t)1, (size_t)1});
+                        P.qgu.counter_elems, P.qdn.counter_elems, P.qsgu.counter_elems,
+                        P.qsdn.counter_elems, P.dec.ok ? P.dec.ctl_words : (size_t)1, (size_t)1});
   z.counters = c.take<int32_t>(ce);
   z.ctl_bytes = c.used;
   route_scratch(c, P.rp, T, L->E, &z.rs);
@@ -184,15 +216,29 @@ static size_t carve(WsCursor& c, const moe_layer* L, int T, const LayerPlan& P, 
   z.src = c.take<int32_t>(tk + 1);
   z.tie = c.take<int32_t>(T + 1);
   z.shared_gate = c.take<float>(T + 1);
-  z.x_perm = c.take<uint16_t>(tk * L->H + 8);
-  z.h = c.take<uint16_t>(tk * L->I + 8);
+  if (P.fp8) {
+    z.xq = c.take<uint8_t>(tk * L->H + 16);
+    z.xs = c.take<float>(tk * (L->H / kFp8Block) + 1);
+    z.hq = c.take<uint8_t>(tk * L->I + 16);
+    z.hs = c.take<float>(tk * (L->I / kFp8Block) + 1);
+    if (L->Is) {
+      z.xq_s = c.take<uint8_t>((size_t)T * L->H + 16);
+      z.xs_s = c.take<float>((size_t)T * (L->H / kFp8Block) + 1);
+      z.hq_s = c.take<uint8_t>((size_t)T * L->Is + 16);
+      z.hs_s = c.take<float>((size_t)T * (L->Is / kFp8Block) + 1);
+    }
+  } else {
+    z.x_perm = c.take<uint16_t>(tk * L->H + 8);
+    z.h = c.take<uint16_t>(tk * L->I + 8);
+  }
   z.y_perm = c.take<uint16_t>(tk * L->H + 8);
   if (L->Is) {
-    z.h_s = c.take<uint16_t>((size_t)T * L->Is + 8);
+    if (!P.fp8) z.h_s = c.take<uint16_t>((size_t)T * L->Is + 8);
     z.s = c.take<uint16_t>((size_t)T * L->H + 8);
   }
   size_t pe = std::max({P.gu.part_elems, P.dn.part_elems, P.sgu.part_elems, P.sdn.part_elems,
-                        P.mgu.t1.part_elems, P.mdn.t1.part_elems, (size_t)1});
+                        P.mgu.t1.part_elems, P.mdn.t1.part_elems, P.qgu.part_elems, P.qdn.part_elems,
+                        P.qsgu.part_elems, P.qsdn.part_elems, (size_t)1});
   z.part = c.take<float>(pe);
   z.part_s = c.take<float>(std::max({P.mgu.t2.part_elems, P.mdn.t2.part_elems, (size_t)1}));
   if (P.dec.ok) {
@@ -216,6 +262,24 @@ struct DevExperts {
   const void* const* tab = nullptr;
 };
 
+// The two FP8 products of an expert FFN (`gu` holds the caller's rows, tables and expert list).
+// Without work between the two, the down product may start while gate/up ends (see Fp8Args).
+static int run_fp8(const moe_bundle_layout& lay, Fp8Args gu, const Fp8Plan& pg, const Fp8Plan& pd,
+                   uint8_t* hq, float* hs, uint16_t* y, const LayerScratch& s, cudaStream_t st,
+                   const std::function<int()>& between) {
+  Fp8Args dn = fp8_args(lay, false, gu.N, gu.K, gu.E, gu.max_rows);
+  dn.offsets = gu.offsets; dn.tab = gu.tab; dn.dev_tab = gu.dev_tab;
+  dn.active = gu.active; dn.n_active = gu.n_active; dn.host_n = gu.host_n;
+  dn.host_ids = gu.host_ids;
+  gu.hq = hq; gu.hs = hs;
+  dn.xq = hq; dn.xs = hs; dn.y = y;
+  int r = launch_fp8(gu, pg, s.part, s.counters, s.err, st);
+  if (r != MOE_OK) return r;
+  if (between && (r = between()) != MOE_OK) return r;
+  dn.early = !between;
+  return launch_fp8(dn, pd, s.part, s.counters, s.err, st);
+}
+
 static int run_experts(const moe_layer* L, const LayerPlan& P, const LayerScratch& s,
                        const BundleTable& tab, int T, int host_n, const int32_t* host_ids,
                        cudaStream_t st, std::function<int()> between,
@@ -223,6 +287,12 @@ static int run_experts(const moe_layer* L, const LayerPlan& P, const LayerScratc
   const int rows = T * L->k;
   const int32_t* act = dx.active ? dx.active : s.rs.active;
   const int32_t* nact = dx.active ? dx.n_active : s.rs.n_active;
+  if (P.fp8) {
+    Fp8Args q = fp8_args(P.lay, true, L->H, L->I, L->E, rows);
+    q.xq = s.xq; q.xs = s.xs; q.offsets = s.offsets; q.active = act; q.n_active = nact;
+    q.tab = &tab; q.dev_tab = dx.tab; q.host_n = host_n; q.host_ids = host_ids;
+    return run_fp8(P.lay, q, P.qgu, P.qdn, s.hq, s.hs, s.y_perm, s, st, between);
+  }
   GemmArgs gu = gemm_args(P.lay, L->wdtype, true, L->H, L->I, L->E, rows, T);
   gu.xin = s.x_perm; gu.offsets = s.offsets; gu.active = act;
   gu.n_active = nact; gu.tab = &tab; gu.out = s.h; gu.dev_tab = dx.tab;
@@ -274,6 +344,13 @@ static int run_shared(const moe_layer* L, const LayerPlan& P, const LayerScratch
   BundleTable tab{};
   tab.p[0] = L->shared_bundle;
   const int32_t* meta = s.rs.shared_meta;
+  if (P.fp8) {
+    const int q = launch_quantize_fp8(x, nullptr, T, 0, T, L->H, s.xq_s, s.xs_s, st);
+    if (q != MOE_OK) return q;
+    Fp8Args a = fp8_args(P.slay, true, L->H, L->Is, 1, T);   // one group: every token's row
+    a.xq = s.xq_s; a.xs = s.xs_s; a.tab = &tab;
+    return run_fp8(P.slay, a, P.qsgu, P.qsdn, s.hq_s, s.hs_s, s.s, s, st, nullptr);
+  }
   GemmArgs gu = gemm_args(P.slay, L->wdtype, true, L->H, L->Is, 1, T);
   gu.xin = x; gu.offsets = meta; gu.active = meta + 2; gu.n_active = meta + 3;
   gu.tab = &tab; gu.out = s.h_s;
@@ -469,7 +546,9 @@ int moe_layer_forward(const moe_layer* L, const uint16_t* x, int T, const int32_
   LayerPlan P{};
   int r = make_plan(L, T, &P);
   if (r != MOE_OK) return r;
-  MOE_REQUIRE(L->gating >= 0 && L->gating <= 2 && L->w_r && ws);
+  const int gating = L->gating & ~(int)MOE_GATING_GROUPED;
+  MOE_REQUIRE(gating >= 0 && gating <= 2 && L->w_r && ws);
+  MOE_REQUIRE(!grouped(L) || !forced_ids);
   MOE_REQUIRE(!L->Is || L->shared_bundle);
   MOE_REQUIRE(!(L->Is && L->shared_gate_sigmoid) || L->w_gate);
   MOE_REQUIRE(cache || L->bundles);
@@ -523,7 +602,7 @@ int moe_layer_forward(const moe_layer* L, const uint16_t* x, int T, const int32_
     da.logit_bias = L->logit_bias; da.sel_bias = L->sel_bias;
     da.w_gate = (L->Is && L->shared_gate_sigmoid) ? L->w_gate : nullptr;
     da.T = T; da.H = L->H; da.E = L->E; da.k = L->k; da.I = L->I; da.Is = L->Is;
-    da.gating = L->gating; da.wdtype = L->wdtype;
+    da.gating = gating; da.wdtype = L->wdtype;
     da.shared_sigmoid = (L->Is && L->shared_gate_sigmoid) ? 1 : 0;
     da.scale = L->scale; da.eps = L->norm_eps;
     for (int e = 0; e < L->E; ++e) da.tab.p[e] = L->bundles[e];
@@ -555,11 +634,16 @@ int moe_layer_forward(const moe_layer* L, const uint16_t* x, int T, const int32_
   ra.x = x; ra.w_r = L->w_r; ra.logit_bias = L->logit_bias; ra.sel_bias = L->sel_bias;
   ra.w_gate = (L->Is && L->shared_gate_sigmoid) ? L->w_gate : nullptr;
   ra.forced = forced_ids; ra.T = T; ra.H = L->H; ra.E = L->E; ra.k = L->k;
-  ra.gating = L->gating; ra.scale = L->scale; ra.ids = s.ids; ra.counts = s.counts;
+  ra.gating = gating; ra.scale = L->scale; ra.ids = s.ids; ra.counts = s.counts;
   ra.offsets = s.offsets; ra.pos = s.pos; ra.src = s.src; ra.tie_flags = s.tie; ra.w = s.w;
   ra.logits = nullptr; ra.shared_gate = s.shared_gate; ra.x_perm = s.x_perm; ra.err = s.err;
+  if (grouped(L)) { ra.n_group = L->n_group; ra.take = L->topk_group; }
   r = launch_route(ra, P.rp, s.rs, s0);
   if (r != MOE_OK) return r;
+  if (P.fp8) {
+    r = launch_quantize_fp8(x, s.src, T * L->k, L->k, T, L->H, s.xq, s.xs, s0);
+    if (r != MOE_OK) return r;
+  }
   if ((r = phase(1)) != MOE_OK) return r;
   const float* sgate = (L->Is && L->shared_gate_sigmoid) ? s.shared_gate : nullptr;
 

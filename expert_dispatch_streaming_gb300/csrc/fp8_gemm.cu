@@ -478,7 +478,6 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
   uint8_t* out = smem + kStages * kStageBytes;
   Ctl& c = *reinterpret_cast<Ctl*>(out + kOutBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  pdl_trigger();
   if (threadIdx.x == 32) {
     prefetch_map(&p.tm_x);
     prefetch_map(&p.tm_x32);
@@ -505,8 +504,10 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
   }
   // The second product of an FFN starts while the first one ends: of what that writes it reads
   // the token rows and their scales only, and writes nothing itself, until pdl_wait (below, by
-  // the warps concerned); experts, offsets and weights are older.
+  // the warps concerned); experts, offsets and weights are older: it is let go only after this
+  // first wait, when whatever wrote them has completed.
   if (!p.early) pdl_wait();
+  pdl_trigger();
   const int n_act = p.host_n >= 0 ? p.host_n : p.active ? *p.n_active : p.E;
   // the experts' rows, a thread each (one memory latency), then the prefix of their tile counts
   if ((int)threadIdx.x < n_act) {

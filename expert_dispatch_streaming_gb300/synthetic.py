@@ -16,9 +16,9 @@ import torch
 
 import workloads as wl
 
-from . import (GATING, WDTYPE, moe_bundle_bytes, moe_checksum64, moe_host_bundle, moe_layer,
+from . import (GATING, MOE_GATING_GROUPED, WDTYPE, moe_bundle_bytes, moe_checksum64, moe_host_bundle, moe_layer,
                moe_layer_forward, moe_layer_workspace_size, moe_pack_bundle,
-               moe_pack_bundle_nvfp4)
+               moe_pack_bundle_fp8, moe_pack_bundle_nvfp4)
 
 _POOL = ThreadPoolExecutor(max_workers=max(1, min(16, len(os.sched_getaffinity(0)))))
 
@@ -29,6 +29,11 @@ def pack_expert(cfg: wl.MoEConfig, layer: int, e: int, dst: np.ndarray, shared=F
     I = cfg.Is if shared else cfg.I
     if cfg.wdtype == "nvfp4":
         moe_pack_bundle_nvfp4(cfg.H, I, w.wg, w.wu, w.wd, w.sg, w.su, w.sd, w.gs, dst)
+    elif cfg.wdtype == "fp8_b128":      # weight rows: the transposed matrices, gate above up
+        rows = [np.ascontiguousarray(m) for m in (np.concatenate([w.wg.T, w.wu.T]),
+                                                  np.concatenate([w.sg.T, w.su.T]), w.wd.T,
+                                                  w.sd.T)]
+        moe_pack_bundle_fp8(cfg.H, I, *rows, dst)
     else:
         moe_pack_bundle(cfg.H, I, cfg.wdtype, w.wg, w.wu, w.wd, w.sg, w.su, w.sd, dst)
 
@@ -72,6 +77,9 @@ class DeviceLayer:
         d = moe_layer()
         d.H, d.E, d.k, d.I, d.Is = cfg.H, cfg.E, cfg.k, cfg.I, cfg.Is
         d.gating, d.scale, d.wdtype = GATING[cfg.gating], cfg.scale, WDTYPE[cfg.wdtype]
+        if cfg.n_group:
+            d.gating |= MOE_GATING_GROUPED
+            d.n_group, d.topk_group = cfg.n_group, cfg.topk_group
         d.layer_index = layer
         d.shared_gate_sigmoid = 1 if cfg.shared_gate == "sigmoid" else 0
         d.w_r = self.w_r.data_ptr()

@@ -101,7 +101,10 @@ int moe_workspace_error(const void* ws, int32_t* code, void* stream);
 enum moe_gating {
   MOE_GATING_SOFTMAX_RENORM = 0,
   MOE_GATING_SOFTMAX = 1,
-  MOE_GATING_SIGMOID_BIAS_RENORM = 2
+  MOE_GATING_SIGMOID_BIAS_RENORM = 2,
+  /* moe_layer.gating only, added to one of the above: group-limited selection
+   * (moe_route_topk_grouped) with moe_layer.n_group and moe_layer.topk_group */
+  MOE_GATING_GROUPED = 16
 };
 
 /* Expert weight storage inside a bundle. */
@@ -565,7 +568,7 @@ int moe_expert_cache_copy_time(moe_expert_cache* cache, double* ms, int64_t* n);
 /* ------------------------------------------------------------------ whole layer */
 typedef struct moe_layer {
   int H, E, k, I, Is;        /* Is = shared-expert intermediate size, 0 = none          */
-  int gating;                /* enum moe_gating                                          */
+  int gating;                /* enum moe_gating, or one of its modes + MOE_GATING_GROUPED */
   float scale;               /* routed weight multiplier                                 */
   int wdtype;                /* enum moe_wdtype of routed and shared bundles            */
   int layer_index;           /* cache key                                                */
@@ -578,6 +581,7 @@ typedef struct moe_layer {
   const void* const* bundles;/* HOST array [E] of device bundles (all resident), or NULL
                                 when a cache is attached                                 */
   float norm_eps;            /* epsilon of the optional RMS-normalised output (out_normed) */
+  int n_group, topk_group;   /* read only with MOE_GATING_GROUPED: see moe_route_topk_grouped */
 } moe_layer;
 
 /* Number of phase events moe_layer_forward can record (see moe_layer_stats). */
@@ -618,6 +622,11 @@ size_t moe_layer_workspace_size(const moe_layer* L, int T);
  *  ids_out, w_out  device [T][k] or NULL: copies of the routing decision.
  *  ws, ws_bytes    device scratch of moe_layer_workspace_size(L, T) bytes, 256-byte aligned
  *             (MOE_ERR_INVALID_ARG otherwise).
+ * With MOE_GATING_GROUPED the routing is moe_route_topk_grouped's (forced_ids must be NULL, else
+ * MOE_ERR_INVALID_ARG).  With MOE_W_FP8_B128 bundles the token rows are quantised on their way
+ * into expert order (moe_quantize_fp8) and the routed and shared experts run as in
+ * moe_grouped_swiglu_fp8.  Both take the step-by-step kernels at every batch size, and an FP8
+ * layer's shared expert has launches of its own.
  * With cache == NULL the call is fully asynchronous.
  * Defined by: "NovaLLM ...", "2. Why MoE Is a Natural Breakthrough Point" and "3. Optimization
  * #1 -- Expert-Level Streaming" (route, then run only the selected experts, whose weights are

@@ -83,6 +83,21 @@ def topk_select(score: np.ndarray, k: int):
     return chosen, gap
 
 
+def limit_to_groups(score: np.ndarray, mode: str, n_group: int, take: int):
+    """Selection scores with every expert outside the token's `take` best groups at -inf, and the
+    gap between the last group taken and the first one left.  A group's score is the sum of its
+    two largest scores (sigmoid mode) or its largest; ties go to the lower group."""
+    T, E = score.shape
+    g = np.sort(score.reshape(T, n_group, E // n_group), axis=2)[:, :, ::-1]
+    gs = g[:, :, :2].sum(axis=2) if mode == "sigmoid_bias_renorm" else g[:, :, 0]
+    order = np.argsort(-gs, axis=1, kind="stable")
+    srt = np.take_along_axis(gs, order, axis=1)
+    gap = srt[:, take - 1] - srt[:, take] if take < n_group else np.full(T, np.inf)
+    keep = np.zeros((T, n_group), bool)
+    np.put_along_axis(keep, order[:, :take], True, axis=1)
+    return np.where(np.repeat(keep, E // n_group, axis=1), score, -np.inf), gap
+
+
 def gate_weights(l: np.ndarray, ids: np.ndarray, mode: str, scale: float = 1.0) -> np.ndarray:
     """Routed weights w[T, k] for the chosen ids (in the given id order).
 
@@ -192,6 +207,37 @@ def dequant_nvfp4(codes: np.ndarray, scales: np.ndarray, g: float, block: int = 
     return decode_e2m1(codes) * np.repeat(decode_e4m3(scales), block, axis=0) * float(g)
 
 
+# FP8.  The expert-cache page names FP8 checkpoints beside NVFP4 and INT4 without defining a
+# format; the reading is the block-scaled one DeepSeek-V3-shaped checkpoints are published in:
+# E4M3 weights with an fp32 scale per 128 x 128 block, token rows quantised per 128 elements.
+
+
+def dequant_fp8(codes: np.ndarray, scales: np.ndarray) -> np.ndarray:
+    """W[r, c] = E4M3(code[r, c]) * scale[r // 128, c // 128] in fp64 (exact)."""
+    s = np.asarray(scales, np.float64)
+    return decode_e4m3(codes) * np.repeat(np.repeat(s, 128, axis=0), 128, axis=1)
+
+
+def round_e4m3(v: np.ndarray) -> np.ndarray:
+    """Nearest E4M3 value (ties to even, saturating at 448) of finite v, in fp64."""
+    v = np.asarray(v, np.float64)
+    mag = np.minimum(np.abs(v), 448.0)
+    _, e = np.frexp(mag)                             # mag in [2^(e-1), 2^e)
+    step = np.ldexp(1.0, np.maximum(e - 1, -6) - 3)
+    return np.copysign(np.rint(mag / step) * step, v)
+
+
+def quantize_fp8_rows(x: np.ndarray) -> np.ndarray:
+    """The values FP8 rows stand for: per row and 128 elements, amax = max(|x|, 2^-96),
+    q = e4m3(x * (448 / amax)) in fp32 arithmetic, value q * (amax / 448)."""
+    x = np.asarray(x, np.float32)
+    R, H = x.shape
+    b = x.reshape(R, H // 128, 128)
+    amax = np.maximum(np.abs(b).max(axis=2, keepdims=True), np.float32(2.0 ** -96))
+    q = round_e4m3(b * (np.float32(448) / amax))
+    return (q * (amax / np.float32(448)).astype(np.float64)).reshape(R, H)
+
+
 def expert_matrices(w, group: int = 128):
     """(Wg[H, I], Wu[H, I], Wd[I, H]) as fp64 from a workloads.ExpertWeights."""
     if w.wdtype == "bf16":
@@ -199,18 +245,22 @@ def expert_matrices(w, group: int = 128):
     if w.wdtype == "nvfp4":
         return (dequant_nvfp4(w.wg, w.sg, w.gs[0]), dequant_nvfp4(w.wu, w.su, w.gs[1]),
                 dequant_nvfp4(w.wd, w.sd, w.gs[2]))
+    if w.wdtype == "fp8_b128":
+        return dequant_fp8(w.wg, w.sg), dequant_fp8(w.wu, w.su), dequant_fp8(w.wd, w.sd)
     return (dequant_int4(w.wg, w.sg, group), dequant_int4(w.wu, w.su, group),
             dequant_int4(w.wd, w.sd, group))
 
 
-def swiglu_ffn(xr: np.ndarray, wg: np.ndarray, wu: np.ndarray, wd: np.ndarray):
+def swiglu_ffn(xr: np.ndarray, wg: np.ndarray, wu: np.ndarray, wd: np.ndarray, fp8: bool = False):
     """One SwiGLU expert on rows xr[n, H]:  g = xr Wg, u = xr Wu,
     h = bf16(silu(g) * u) with silu(g) = g / (1 + exp(-g)),  y = bf16(h Wd).
-    Returns (y, h) as fp64 values of bf16 numbers."""
-    xr = np.asarray(xr, np.float64)
+    Returns (y, h) as fp64 values of bf16 numbers.  fp8: x and h are FP8 rows (h rounded to
+    E4M3 with its block scales, not to bf16)."""
+    xr = quantize_fp8_rows(xr) if fp8 else np.asarray(xr, np.float64)
     g = xr @ wg
     u = xr @ wu
-    h = bf16.round_rne(g / (1.0 + np.exp(-g)) * u)
+    h = g / (1.0 + np.exp(-g)) * u
+    h = quantize_fp8_rows(h) if fp8 else bf16.round_rne(h)
     y = bf16.round_rne(h @ wd)
     return y, h
 
@@ -272,11 +322,17 @@ def layer_forward(cfg, layer: int, x_bits: np.ndarray, *, forced_ids=None, rows=
     sel_bias = b if cfg.bias_kind == "select" else None
     l = router_logits(x, w_r, logit_bias)
     score = selection_scores(l, cfg.gating, sel_bias)
-    ids_sel, gap = topk_select(score, cfg.k)
+    if cfg.n_group:
+        open_, group_gap = limit_to_groups(score, cfg.gating, cfg.n_group, cfg.topk_group)
+        ids_sel, gap = topk_select(open_, cfg.k)
+        gap = np.minimum(gap, group_gap)
+    else:
+        ids_sel, gap = topk_select(score, cfg.k)
     ids = ids_sel if forced_ids is None else np.asarray(forced_ids, np.int32)
     w = gate_weights(l, ids, cfg.gating, cfg.scale)
     counts, offsets, pos, src = dispatch(ids, cfg.E)
 
+    fp8 = cfg.wdtype == "fp8_b128"
     rows = np.arange(T) if rows is None else np.asarray(rows)
     want = np.zeros(T, bool)
     want[rows] = True
@@ -290,12 +346,12 @@ def layer_forward(cfg, layer: int, x_bits: np.ndarray, *, forced_ids=None, rows=
         if p.size == 0:
             continue
         wg, wu, wd = expert_matrices(getw(layer, e), cfg.group)
-        y_perm[p], _ = swiglu_ffn(permute(x, src[p], cfg.k), wg, wu, wd)
+        y_perm[p], _ = swiglu_ffn(permute(x, src[p], cfg.k), wg, wu, wd, fp8)
 
     shared_out, g_s = None, None
     if cfg.Is:
         wg, wu, wd = expert_matrices(getw(layer, 0, True), cfg.group)
-        shared_out, _ = swiglu_ffn(x[rows], wg, wu, wd)
+        shared_out, _ = swiglu_ffn(x[rows], wg, wu, wd, fp8)
         if cfg.shared_gate == "sigmoid":
             ws = bf16.decode(wl.shared_gate_vector(cfg, layer))
             g_s = sigmoid(x[rows] @ ws)

@@ -155,3 +155,57 @@ def test_empty_calls_return_without_work(moe):
     moe.moe_grouped_swiglu_fp8(None, None, None, [A], 1, 128, 128, 0, None, None, 0, 0)
     assert moe.moe_grouped_gemm_fp8_workspace_size(8, 300, 64, 64) == 0
     assert moe.moe_grouped_swiglu_fp8_workspace_size(8, 4, 100, 128) == 0
+
+
+def _layer(moe, **kw):
+    d = moe.moe_layer()
+    d.H, d.E, d.k, d.I, d.Is = 256, 16, 4, 128, 0
+    d.gating, d.scale, d.wdtype = moe.MOE_GATING_SOFTMAX, 1.0, moe.WDTYPE["fp8_b128"]
+    for n, v in kw.items():
+        setattr(d, n, v)
+    return d
+
+
+def test_layer_refuses_bad_groups_and_sizes(moe):
+    g = moe.MOE_GATING_SOFTMAX + moe.MOE_GATING_GROUPED
+    ok = dict(gating=g, n_group=4, topk_group=2)
+    assert moe.moe_layer_workspace_size(_layer(moe), 8) > 0
+    assert moe.moe_layer_workspace_size(_layer(moe, **ok), 8) > 0
+    # the groups are read with the flag only
+    assert moe.moe_layer_workspace_size(_layer(moe, n_group=-3, topk_group=99), 8) > 0
+    for bad in (dict(n_group=3), dict(n_group=0), dict(n_group=64), dict(topk_group=0),
+                dict(topk_group=5), dict(n_group=16, topk_group=3)):
+        assert moe.moe_layer_workspace_size(_layer(moe, **{**ok, **bad}), 8) == 0, bad
+    for bad in (dict(H=200), dict(I=100), dict(Is=64), dict(k=9), dict(wdtype=4)):
+        assert moe.moe_layer_workspace_size(_layer(moe, **bad), 8) == 0, bad
+
+
+def test_layer_refuses_forced_ids_with_groups(moe):
+    """Addresses that are never followed: the call returns before any CUDA work."""
+    one = 1 << 20
+    d = _layer(moe, gating=moe.MOE_GATING_SOFTMAX + moe.MOE_GATING_GROUPED, n_group=4,
+               topk_group=2, w_r=one)
+    table = moe.bundle_table([one] * 16)
+    d.bundles = table
+    with pytest.raises(moe.MoEError):
+        moe.moe_layer_forward(d, one, 8, one, None, one, None, one, 1 << 40)
+    d.gating = 3 + moe.MOE_GATING_GROUPED
+    with pytest.raises(moe.MoEError):
+        moe.moe_layer_forward(d, one, 8, None, None, one, None, one, 1 << 40)
+
+
+def test_fp8_recipe_and_rounding():
+    """The workload's codes are finite with the stated deviation; the oracle's rounding is the
+    nearest E4M3 value."""
+    import workloads as wl
+    cfg = wl.custom("f8", H=256, I=128, wdtype="fp8_b128")
+    wg, wu, wd = moe_ref.expert_matrices(wl.expert(cfg, 0, 0))
+    for m, shape in ((wg, (256, 128)), (wu, (256, 128)), (wd, (128, 256))):
+        assert m.shape == shape and np.isfinite(m).all()
+        assert 0.4 * cfg.w_std < m.std() < 1.6 * cfg.w_std
+    vals = np.unique(moe_ref.decode_e4m3(np.arange(0x7F)))
+    mids = (vals[1:] + vals[:-1]) / 2
+    even = np.where(np.arange(len(mids)) % 2 == 0, vals[:-1], vals[1:])
+    assert np.array_equal(moe_ref.round_e4m3(mids), even)
+    assert np.array_equal(moe_ref.round_e4m3(-vals), -vals)
+    assert np.array_equal(moe_ref.round_e4m3(np.array([449.0, 1e9, -500.0])), [448, 448, -448])

@@ -53,7 +53,7 @@ class MoEConfig:
     scale: float = 1.0          # routed weight multiplier (2.5 for the DeepSeek-V3 shape)
     Is: int = 0                 # shared-expert intermediate size, 0 = none
     shared_gate: str = "none"   # "none" | "sigmoid" (Qwen: sigmoid(x . w_s)) | "one"
-    wdtype: str = "bf16"        # "bf16" | "int4_g128" | "nvfp4"
+    wdtype: str = "bf16"        # "bf16" | "int4_g128" | "nvfp4" | "fp8_b128"
     zipf_s: float = 0.0         # expert-popularity exponent, 0 = no popularity offsets
     bias_kind: str = "none"     # "none" | "logit" (added to logits) | "select" (selection only)
     layers: int = 1
@@ -62,6 +62,8 @@ class MoEConfig:
     w_std: float = 0.02
     x_std: float = 1.0
     group: int = 128            # INT4 group size along the reduction dimension
+    n_group: int = 0            # group-limited selection: expert groups, 0 = none
+    topk_group: int = 0         # ... and how many of them a token takes
 
     def with_(self, **kw) -> "MoEConfig":
         return replace(self, **kw)
@@ -84,7 +86,15 @@ STREAMED = MoEConfig("streamed", 4, H=2048, E=60, k=4, I=1408, gating="softmax",
                      shared_gate="sigmoid", zipf_s=1.0, bias_kind="logit", layers=16,
                      Ts=(1, 8, 64))
 
-CONFIGS = {c.name: c for c in (TINY, MIXTRAL, QWEN, DEEPSEEK, STREAMED, QWEN_NVFP4)}
+# the DeepSeek-V3 shape as its FP8 checkpoints run it: E4M3 experts, a token's experts taken from
+# 4 of 8 groups
+DEEPSEEK_FP8 = MoEConfig("deepseek_fp8", 6, H=7168, E=256, k=8, I=2048,
+                         gating="sigmoid_bias_renorm", scale=2.5, Is=2048, shared_gate="one",
+                         wdtype="fp8_b128", zipf_s=1.1, bias_kind="select", n_group=8,
+                         topk_group=4, Ts=(1, 32, 512, 8192))
+
+CONFIGS = {c.name: c for c in (TINY, MIXTRAL, QWEN, DEEPSEEK, STREAMED, QWEN_NVFP4,
+                             DEEPSEEK_FP8)}
 
 # expert-streamed decode recipe: 256 steps, 4 GiB of VRAM slots, trace locality
 STREAM_STEPS = 256
@@ -211,6 +221,26 @@ def _matrix_scales(key, std):
     return (g * (std / (2.93 * 178.0))).astype(np.float32)
 
 
+# FP8 recipe: E4M3 codes uniform over the 254 finite bytes (rms 100.06), one fp32 scale per
+# 128 x 128 block that brings the weight's standard deviation near `std`
+FP8_RMS = 100.06
+
+
+def _fp8_codes(key, shape):
+    n = int(np.prod(shape))
+
+    def fill(g, m):
+        v = g.integers(0, 254, m, dtype=np.uint8)
+        return v + (v >= 0x7F).astype(np.uint8)      # 0x00..0x7E, 0x80..0xFE: no NaN
+    return _blocked(n, fill, key).reshape(shape)
+
+
+def _fp8_scales(key, shape, std):
+    n = int(np.prod(shape))
+    return _blocked(n, lambda g, m: (g.uniform(0.5, 1.5, m) * (std / FP8_RMS)).astype(np.float32),
+                    key).reshape(shape)
+
+
 # ----------------------------------------------------------------------------- tensors
 def tokens(cfg: MoEConfig, T: int, step: int = 0) -> np.ndarray:
     """Activations x[T, H] as bf16 bits, N(0, x_std)."""
@@ -266,6 +296,8 @@ class ExpertWeights:
     elements along the reduction dimension).
     nvfp4: ``wg``/``wu``/``wd`` uint8 E2M1 codes, ``sg``/``su`` [H/16, I] and ``sd`` [I/16, H]
     uint8 E4M3 block scales, ``gs`` float32 [3] matrix scales (gate, up, down).
+    fp8_b128: ``wg``/``wu`` [H, I] and ``wd`` [I, H] uint8 E4M3 codes, ``sg``/``su``
+    [H/128, I/128] and ``sd`` [I/128, H/128] float32 block scales.
     """
     wdtype: str
     wg: np.ndarray
@@ -307,6 +339,15 @@ def expert(cfg: MoEConfig, layer: int, e: int, shared: bool = False) -> ExpertWe
                              _e4m3_scales(key(T_SU), (H // 16, I)),
                              _e4m3_scales(key(T_SD), (I // 16, H)),
                              _matrix_scales(key(T_GS), cfg.w_std))
+    if cfg.wdtype == "fp8_b128":
+        assert H % 128 == 0 and I % 128 == 0
+        return ExpertWeights("fp8_b128",
+                             _fp8_codes(key(T_WG), (H, I)),
+                             _fp8_codes(key(T_WU), (H, I)),
+                             _fp8_codes(key(T_WD), (I, H)),
+                             _fp8_scales(key(T_SG), (H // 128, I // 128), cfg.w_std),
+                             _fp8_scales(key(T_SU), (H // 128, I // 128), cfg.w_std),
+                             _fp8_scales(key(T_SD), (I // 128, H // 128), cfg.w_std))
     raise ValueError(cfg.wdtype)
 
 
