@@ -19,7 +19,7 @@
 //   warp 0     producer: per step 16 KB of token rows by 2-D TMA (128-byte swizzle; a tile that is
 //              not full in boxes of 32 rows) and 32 KB of weights: two bundle tiles by bulk copy
 //              (each is stored as its swizzled shared-memory image), or two TMA boxes of a
-//              row-major weight; four stages;
+//              row-major weight; three stages;
 //   warps 1, 3 MMA issuers, one per 256-column TMEM buffer: four tcgen05.mma (K = 32 each) per
 //              step, the steps in turn;
 //   warp 2     scale factors: xs * ws per token and weight tile of each step, to shared memory;
@@ -28,8 +28,8 @@
 //              (they take the registers warps 0-3 give up).
 //
 // Work: tiles (expert, weight tile pair, token tile), token tile fastest so that CTAs running
-// together share weights through L2.  With few tiles the steps of all tiles, in order, are cut
-// into one equal range per CTA: a tile cut by range ends is finished by the last of its CTAs to
+// together share weights through L2.  With few tiles their steps are cut
+// into equal ranges (see Cut): a tile of several ranges is finished by the last of its CTAs to
 // arrive (a counter per lane quarter), which adds the pieces' fp32 sums in range order, so the
 // result does not depend on the arrival order.
 //
@@ -53,9 +53,12 @@ static_assert(kThreads >= kMaxExperts, "a thread looks up each expert's rows");
 constexpr int kRegsLow = 56, kRegsHigh = 224;
 static_assert(128 * kRegsLow + 256 * kRegsHigh <= kThreads * 168, "within the launch's registers");
 constexpr int kAccCols = 256, kTmemCols = 512;
-// Tiles are cut into equal ranges of steps when there are fewer than kRangeTiles per CTA and the
-// busiest CTA is thereby spared kJoinSteps steps, about what writing and joining the pieces costs.
-constexpr int kRangeTiles = 4, kJoinSteps = 5;
+// Tiles are cut into ranges of steps where that spares the busiest CTA more than it costs, counted
+// in steps: kJoinSteps for writing a piece and joining, kJoinRows for each piece of 128 rows read
+// (few rows: 1 for 16 pieces), kPieceSteps where a CTA may write two pieces.  (1001 rows of 8 experts,
+// 1200 x 1000, 10 steps a tile: joined from four pieces 33 us, whole 20.  One row, 7168 x 4096, 56
+// steps a tile: 9 ranges a tile 19.4 us, ranges over all tiles 21.4.)
+constexpr int kRangeTiles = 4, kJoinSteps = 4, kJoinRows = 3, kPieceSteps = 3;
 
 // Output rows on their way out: per epilogue warp two boxes of 32 rows x 128 bytes.
 constexpr int kBox = 4096, kOutBytes = 8 * 2 * kBox;
@@ -206,18 +209,24 @@ __device__ __forceinline__ void tc_fence_before() {
 __device__ __forceinline__ void tc_fence_after() {
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
-// 32 columns of the warp's 32 lanes, without and with the wait.
-__device__ __forceinline__ void tmem_ld32_nw(uint32_t taddr, uint32_t (&r)[32]) {
+// 64 columns of the warp's 32 lanes, without the wait.
+__device__ __forceinline__ void tmem_ld64_nw(uint32_t taddr, uint32_t (&r)[64]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
       "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, "
-      "%28, %29, %30, %31}, [%32];"
+      "%28, %29, %30, %31, %32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, "
+      "%45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, "
+      "%62, %63}, [%64];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
-        "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
-        "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
-        "=r"(r[31])
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
+        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(r[32]), "=r"(r[33]), "=r"(r[34]),
+        "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]),
+        "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]),
+        "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
+        "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]),
+        "=r"(r[63])
       : "r"(taddr));
 }
 __device__ __forceinline__ void tmem_wait_ld() {
@@ -227,8 +236,8 @@ __device__ __forceinline__ void tmem_wait_ld() {
 // wait are, so that no use of v moves above the wait.  The pairs are put together inside the
 // asm: accumulators kept as 64-bit values make the compiler copy every operand each step
 // (measured, 128 columns by two warps per scheduler: 613 clocks against 345).
-template <int FROM = 0, int TO = 16>
-__device__ __forceinline__ void fma32(float* acc, const uint32_t (&v)[32], uint64_t f) {
+template <int FROM = 0, int TO = 32>
+__device__ __forceinline__ void fma64(float* acc, const uint32_t (&v)[64], uint64_t f) {
 #pragma unroll
   for (int i = FROM; i < TO; ++i)
     asm volatile(
@@ -260,25 +269,52 @@ __device__ __forceinline__ bool expert_rows(const Fp8Params& p, int e, int& r0, 
   return r0 != a || r1 != b;
 }
 
-// The CTA's share of the steps: whole tiles CTA, CTA + G, ... or one range of all tiles' steps,
-// in order: the first `more` CTAs take n + 1 steps, the others n.
+// The CTA's share of the steps: whole tiles CTA, CTA + G, ..., or a range of all tiles' steps in
+// order, the first `more` CTAs taking n + 1 steps and the others n; or, with no more tiles than
+// CTAs, `per` equal ranges of every tile, so that no CTA writes two pieces.
 struct Cut {
-  int on, G, n, more;
-  __device__ __forceinline__ void set(int U, int KB) {
-    G = gridDim.x;
-    on = 0;
-    if (U >= kRangeTiles * G) return;
-    const int W = U * KB;
-    on = (U + G - 1) / G * KB - W / G >= kJoinSteps;
+  int on, G, n, more, per, KB;
+  // by a converged warp; rows: the most rows of any tile
+  __device__ __forceinline__ void set(int U, int KB_, int rows, int lane) {
+    const int ctas = gridDim.x;
+    int best = 0;
+    if (U > 0 && U < kRangeTiles * ctas) {
+      // the busiest CTA's cost, in steps: of whole tiles, of ranges over all tiles, and of 2 .. 33
+      // ranges a tile (one choice a lane); the least, or what comes first here.  (Quotients for the
+      // choice only, so by fast division.)
+      auto up = [](float a, float b) { return __float2uint_ru(__fdividef(a, b) - 1e-3f); };
+      auto join = [&](float pieces) {
+        const float each = rows <= kFewRows ? 0.0625f : kJoinRows / 128.f * rows;
+        return kJoinSteps + __float2uint_rd(pieces * each);
+      };
+      const float fk = KB_, fu = U, fc = ctas;
+      const unsigned whole = up(fu, fc) * KB_ << 8, all = up(fu * fk, fc);
+      const unsigned over = (all + join(__fdividef(fk, all) + 1.f) + kPieceSteps) << 8 | 255u;
+      unsigned c = min(whole, over);
+      const int q = 2 + lane;
+      if (q * U <= ctas && q <= KB_) c = min(c, (up(fk, q) + join(q)) << 8 | (unsigned)q);
+      c = __reduce_min_sync(0xffffffffu, c);
+      best = c & 255;
+    }
+    if (lane) return;
+    per = best == 255 ? 0 : best;
+    KB = KB_;
+    on = best > 0;
+    G = ctas;
     if (!on) return;
-    G = max(1, min(G, W));                      // no empty ranges
-    n = W / G;
-    more = W - n * G;
+    G = per ? U * per : min(ctas, U * KB);      // no empty ranges
+    const int steps = per ? KB : U * KB, parts = per ? per : G;
+    n = steps / parts;
+    more = steps - n * parts;
   }
-  __device__ __forceinline__ int start(int cta) const { return cta * n + min(cta, more); }
+  __device__ __forceinline__ int start(int cta) const {
+    const int u = per ? cta / per : 0, i = cta - u * per;
+    return u * KB + i * n + min(i, more);
+  }
+  __device__ __forceinline__ int count(int cta) const { return n + ((per ? cta % per : cta) < more); }
   __device__ __forceinline__ int owner(int step) const {
-    const int cta = step / (n + 1);
-    return cta < more ? cta : more + (step - more * (n + 1)) / n;
+    const int u = per ? step / KB : 0, s = step - u * KB, i = s / (n + 1);
+    return u * per + (i < more ? i : more + (s - more * (n + 1)) / n);
   }
 };
 struct Walk {
@@ -290,7 +326,7 @@ struct Walk {
     u = (int)blockIdx.x;
     if (cut) {
       const int pos = c.start(u);
-      left = u < G ? c.n + (u < c.more) : 0;
+      left = u < G ? c.count(u) : 0;
       u = pos / KB;
       lo = pos - u * KB;
     }
@@ -520,9 +556,11 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
   }
   __syncthreads();
   if (warp == 2) {
-    int carry = 0;
+    int carry = 0, most = 0;
     for (int base = 0; base < n_act; base += 32) {
-      const int a = base + lane, cnt = a < n_act ? p.NT * ((c.rows[a] + 127) >> 7) : 0;
+      const int a = base + lane, rows = a < n_act ? c.rows[a] : 0,
+                cnt = p.NT * ((rows + 127) >> 7);
+      most = max(most, __reduce_max_sync(0xffffffffu, min(rows, 128)));
       int incl = cnt;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -532,10 +570,8 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
       if (a < n_act) c.pref[a] = carry + incl - cnt;
       carry += __shfl_sync(0xffffffffu, incl, 31);
     }
-    if (lane == 0) {
-      c.pref[n_act] = carry;
-      c.cut.set(carry, p.KB);
-    }
+    if (lane == 0) c.pref[n_act] = carry;
+    c.cut.set(carry, p.KB, most, lane);
   }
   tc_fence_before();
   __syncthreads();
@@ -727,30 +763,26 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
         const uint32_t ta = tmem + ((uint32_t)(q * 32) << 16) + buf * kAccCols + half * 64;
         // straight-line: a condition around any part of it makes the compiler copy the
         // accumulators every step.  (A missing second weight tile leaves old values in its
-        // columns, which are never stored.)  A chunk's load is in flight while the chunk before it
-        // is added; the buffer is handed back, and the next one tried, before the last chunk is.
-        uint32_t v[32], v2[32];
-        tmem_ld32_nw(ta, v);
+        // columns, which are never stored.)  The warp's two loads of 64 columns each cost a latency
+        // that the other warp of the scheduler fills (loads of 32, the next in flight while one is
+        // added: 2% slower); the buffer is handed back, and the next one tried, before the second
+        // half is added.
+        uint32_t v[64];
+        tmem_ld64_nw(ta, v);
         const float2 f = c.f[buf][r];
         const uint64_t f0 = pack(f.x, f.x), f1 = pack(f.y, f.y);
         tmem_wait_ld();
-        tmem_ld32_nw(ta + 32, v2);
-        fma32(acc, v, f0);
-        tmem_wait_ld();
-        tmem_ld32_nw(ta + 128, v);
-        fma32(acc + 32, v2, f0);
-        tmem_wait_ld();
-        tmem_ld32_nw(ta + 160, v2);
-        fma32(acc + 64, v, f1);
+        fma64(acc, v, f0);
+        tmem_ld64_nw(ta + 128, v);
         tmem_wait_ld();
         tc_fence_before();
         __syncwarp();
         warp_arrive(&c.tempty[buf], lane);
         buf ^= 1;
         if (buf == 0) tphase ^= 1;
-        fma32<0, 12>(acc + 96, v2, f1);
+        fma64<0, 24>(acc + 64, v, f1);
         early = mbar_test(&c.tfull[buf], tphase, lane);
-        fma32<12, 16>(acc + 96, v2, f1);
+        fma64<24, 32>(acc + 64, v, f1);
       }
       if (!ok) break;
       if (wk.lo > 0 || wk.hi < KB) {

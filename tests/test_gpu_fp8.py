@@ -226,6 +226,28 @@ def test_grouped_product(moe, counts, N, K):
             check_rows(y[o[e]:o[e + 1]], ref, mag, K, "bf16")
 
 
+@pytest.mark.parametrize("counts,N,K", [
+    ([100], 512, 8192), ([128], 100, 14336), ([3], 512, 8192), ([1, 4, 2], 1000, 7168),
+    ([5, 130, 37], 256, 4112), ([1] * 11, 4096, 2048), ([130] * 8, 2560, 8192),
+    ([90] * 30, 1536, 4096)])
+def test_tiles_in_several_ranges(moe, counts, N, K):
+    """Few tiles with many steps: every way of sharing their steps among the CTAs (pieces of one
+    tile, ranges over tiles, whole tiles), few rows and many."""
+    g = gen(sum(counts) + N + K)
+    q, xs = fp8_rows(g, sum(counts), K)
+    w, ws = fp8_weights(g, len(counts), N, K)
+    off = offsets_of(counts)
+    o = off.tolist()
+    for out in ("fp32", "bf16"):
+        y, scratch = run_gemm(moe, q, xs, w, ws, off, out)
+        assert moe.moe_workspace_error(scratch) == 0
+        y2, _ = run_gemm(moe, q, xs, w, ws, off, out)
+        assert torch.equal(y, y2), "second run differs"
+        for e, n in enumerate(counts):
+            ref, mag = product_ref(q[o[e]:o[e + 1]], xs[o[e]:o[e + 1]], w[e], ws[e])
+            check_rows(y[o[e]:o[e + 1]], ref, mag, K, out)
+
+
 def test_rows_outside_every_expert_stay_as_they_are(moe):
     """offsets[E] below max_rows: the rows past it are not written, whatever they hold."""
     g = gen(3)
@@ -379,6 +401,24 @@ def test_grouped_swiglu_fp8(moe, counts, H, I):
     o = off.tolist()
     ref = torch.cat([swiglu_ref(q[o[e]:o[e + 1]], xs[o[e]:o[e + 1]], w13[e], s13[e], w2[e], s2[e])
                      for e in range(E) if counts[e]])
+    layer_close(y, ref)
+
+
+@pytest.mark.parametrize("counts,H,I", [([70], 8192, 256), ([2, 1], 14336, 128),
+                                        ([200, 3, 64], 7168, 384), ([1] * 5, 4096, 4096)])
+def test_swiglu_tiles_in_several_ranges(moe, counts, H, I):
+    E = len(counts)
+    g = gen(sum(counts) + H + I)
+    q, xs = fp8_rows(g, sum(counts), H)
+    w13, s13 = fp8_weights(g, E, 2 * I, H)
+    w2, s2 = fp8_weights(g, E, H, I)
+    b = bundles_of(moe, H, I, w13, s13, w2, s2)
+    off = offsets_of(counts)
+    y, ws = run_swiglu(moe, q, xs, off, [b[e] for e in range(E)], E, H, I, sum(counts))
+    assert moe.moe_workspace_error(ws) == 0
+    o = off.tolist()
+    ref = torch.cat([swiglu_ref(q[o[e]:o[e + 1]], xs[o[e]:o[e + 1]], w13[e], s13[e], w2[e], s2[e])
+                     for e in range(E)])
     layer_close(y, ref)
 
 
