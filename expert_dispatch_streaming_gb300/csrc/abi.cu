@@ -77,8 +77,8 @@ static int route_topk(const uint16_t* x, const float* w_r, const float* logit_bi
   MOE_REQUIRE(c.ok());
   // the error word (first 4 bytes of ws) starts every call at zero; only the tensor-core
   // router's bounded waits (T >= 256) can set it
-  // (a small group-limited batch's last kernel clears it: a launch less)
-  const bool clear = n_group && rp.small;
+  // (group-limited: its first kernel clears it, a launch less)
+  const bool clear = n_group && T > 0;
   if (!clear) MOE_CUDA_TRY(cudaMemsetAsync(err, 0, sizeof(int32_t), (cudaStream_t)stream));
   RouteArgs a{};
   a.clear_err = clear;
@@ -276,7 +276,7 @@ static int run_fp8(const moe_bundle_layout& lay, Fp8Args gu, const Fp8Plan& pg, 
   int r = launch_fp8(gu, pg, s.part, s.counters, s.err, st);
   if (r != MOE_OK) return r;
   if (between && (r = between()) != MOE_OK) return r;
-  dn.early = !between;
+  dn.after = between ? kAfterAny : kAfterRows;
   return launch_fp8(dn, pd, s.part, s.counters, s.err, st);
 }
 

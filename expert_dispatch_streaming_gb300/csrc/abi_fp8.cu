@@ -59,7 +59,9 @@ int moe_grouped_gemm_fp8(const uint8_t* xq, const float* x_scale, const uint8_t*
   const size_t ctl = c.used;
   float* part = c.take<float>(pl.part_elems);
   MOE_REQUIRE(c.ok());
-  MOE_CUDA_TRY(cudaMemsetAsync(err, 0, ctl, st));
+  const int r = launch_clear(err, ctl, st);
+  if (r != MOE_OK) return r;
+  a.after = kAfterClear;
   return launch_fp8(a, pl, part, ctr, err, st);
 }
 
@@ -104,12 +106,14 @@ int moe_grouped_swiglu_fp8(const uint8_t* xq, const float* x_scale, const int32_
   float* hs = c.take<float>((size_t)max_rows * (I / 128));
   float* part = c.take<float>(std::max(pg.part_elems, pd.part_elems));
   MOE_REQUIRE(c.ok());
-  MOE_CUDA_TRY(cudaMemsetAsync(err, 0, ctl, st));
+  int r = launch_clear(err, ctl, st);
+  if (r != MOE_OK) return r;
+  gu.after = kAfterClear;
   gu.xq = xq; gu.xs = x_scale; gu.offsets = offsets; gu.tab = &tab;
   gu.w_off = lay.gate_up_offset; gu.s_off = lay.gate_up_scale_offset; gu.hq = hq; gu.hs = hs;
-  const int r = launch_fp8(gu, pg, part, ctr, err, st);
+  r = launch_fp8(gu, pg, part, ctr, err, st);
   if (r != MOE_OK) return r;
-  dn.early = true;
+  dn.after = kAfterRows;
   dn.xq = hq; dn.xs = hs; dn.offsets = offsets; dn.tab = &tab;
   dn.w_off = lay.down_offset; dn.s_off = lay.down_scale_offset; dn.y = y_perm;
   return launch_fp8(dn, pd, part, ctr, err, st);

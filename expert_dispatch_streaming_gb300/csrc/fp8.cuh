@@ -34,14 +34,18 @@ inline bool aligned256(const void* p) { return (reinterpret_cast<uintptr_t>(p) &
 //   acc[row][n] = sum_b xs[row][b] ws_e[n / 128][b] sum_{k in block b} xq[row][k] w_e[n][k]
 // fused: w_e = gate rows 0..N-1 and up rows N..2N-1; h = silu(gate) * up is quantised per row
 //        and 128 columns into hq / hs;  else y = acc rounded to bf16, or kept in fp32.
+// What the kernel before a product on the stream writes: anything, so that the product starts when
+// it has ended; or, so that the product may start earlier and waits where it needs that, only the
+// product's token rows and scales (the product before it) or only its counters and error word
+// (launch_clear).
+enum Fp8After { kAfterAny = 0, kAfterRows = 1, kAfterClear = 2 };
 struct Fp8Args {
   const uint8_t* xq;          // [max_rows][K] E4M3
   const float* xs;            // [max_rows][ceil(K / 128)]
   const int32_t* offsets;     // device [E+1], or NULL: one group of max_rows rows
   int E, N, K, max_rows;
   bool fused, y_f32;
-  bool early;                 // the kernel before it on the stream is the product that writes xq
-                              // and xs, and nothing else this one reads (see fp8_gemm.cu)
+  int after;                  // Fp8After: what the kernel before it on the stream does
   // weights: bundles (host table or device table) with the section's codes at w_off and its
   // scales at s_off, or plain row-major w [E][N][K] with ws [E][ceil(N/128)][ceil(K/128)]
   const BundleTable* tab;
@@ -67,6 +71,9 @@ struct Fp8Plan {
 Fp8Plan plan_fp8(const Fp8Args& a);
 int launch_fp8(const Fp8Args& a, const Fp8Plan& pl, float* part, int32_t* counters, int32_t* err,
                cudaStream_t st);
+
+// zeroes the control words of a workspace (bytes: a multiple of 16)
+int launch_clear(void* words, size_t bytes, cudaStream_t st);
 
 int launch_quantize_fp8(const uint16_t* x, const int32_t* src, int rows, int k, int T, int H,
                         uint8_t* q, float* scale, cudaStream_t st);

@@ -82,7 +82,7 @@ struct Fp8Params {
   uint8_t* hq;
   float* hs;
   void* y;
-  int y_f32, early;
+  int y_f32, after;
   float* part;                  // [CTAs][2][quarters][2][32][32 lanes] groups of 4 columns
   int32_t* counters;            // [tiles][4], used when tiles are cut
   int32_t* err;
@@ -147,6 +147,7 @@ __device__ __forceinline__ bool warp_wait(uint64_t* b, uint32_t parity, int32_t*
   for (uint32_t i = 1;; ++i) {
     if (__any_sync(0xffffffffu, mbar_try(bar, parity, lane))) return true;
     if ((i & 255) == 0 && __any_sync(0xffffffffu, globaltimer() - t0 > kWaitNs)) {
+      pdl_wait();                               // (the word may still be being cleared)
       if (lane == 0) atomicExch(err, code);
       return false;
     }
@@ -538,18 +539,22 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
                  "r"(kTmemCols));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
-  // The second product of an FFN starts while the first one ends: of what that writes it reads
-  // the token rows and their scales only, and writes nothing itself, until pdl_wait (below, by
-  // the warps concerned); experts, offsets and weights are older: it is let go only after this
-  // first wait, when whatever wrote them has completed.
-  if (!p.early) pdl_wait();
+  // A product after the clearing of its control words needs those first when it joins pieces; the
+  // second product of an FFN starts while the first one ends: of what that writes it reads the
+  // token rows and their scales only, and writes nothing itself, until pdl_wait (below, by the
+  // warps concerned).  Experts, offsets and weights are older than both: the first product lets
+  // the second go only after this wait, or itself follows a clearing that nothing ran beside.
+  if (p.after == kAfterAny) pdl_wait();
   pdl_trigger();
   const int n_act = p.host_n >= 0 ? p.host_n : p.active ? *p.n_active : p.E;
   // the experts' rows, a thread each (one memory latency), then the prefix of their tile counts
   if ((int)threadIdx.x < n_act) {
     int r0, r1;
     const int a = threadIdx.x, e = expert_of(p, a);
-    if (expert_rows(p, e, r0, r1)) atomicExch(p.err, 8);
+    if (expert_rows(p, e, r0, r1)) {
+      pdl_wait();
+      atomicExch(p.err, 8);
+    }
     c.row0[a] = r0;
     c.rows[a] = r1 - r0;
     c.id[a] = e;
@@ -586,9 +591,9 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
     int stage = 0, issued = 0;
     uint32_t phase = 0;
     bool ok = true;
-    // early: the weights of the first stages are asked for before the token rows may be
+    // the weights of the first stages are asked for before token rows still being written may be
     int ahead = 0;
-    if (p.early && wk.next()) {
+    if (p.after == kAfterRows && wk.next()) {
       const Tile t = tile_of(c, n_act, wk.u);
       for (; ahead < min(kStages, wk.hi - wk.lo); ++ahead) {
         if (elect_one()) {
@@ -599,7 +604,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
         __syncwarp();
       }
     }
-    if (p.early) pdl_wait();
+    if (p.after == kAfterRows) pdl_wait();
     wk = Walk(c.cut, U, KB);
     while (ok && wk.next()) {
       const Tile t = tile_of(c, n_act, wk.u);
@@ -676,7 +681,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
     }
   } else if (warp == 2) {
     // ------------------------------------------------------------ scale factors
-    if (p.early) pdl_wait();
+    if (p.after == kAfterRows) pdl_wait();
     // per step: xs * ws of every token and weight tile into the TMEM buffer's slot
     int buf = 0;
     uint32_t tphase = 0;
@@ -737,7 +742,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
       pphase ^= 1;
       return w;
     };
-    if (p.early) pdl_wait();
+    if (p.after != kAfterAny) pdl_wait();
     while (ok && wk.next()) {
       const Tile t = tile_of(c, n_act, wk.u);
       const int n0 = t.nt * (FUSED ? 128 : 256);
@@ -936,6 +941,13 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
   }
 }
 
+// Zeroes a product's control words.  A kernel, not a memset: the product's CTAs start beside it
+// (a memset before the product: gemm_token's shape 20 us, this 17).
+__global__ void __launch_bounds__(256) clear_kernel(uint4* words, int n) {
+  pdl_trigger();
+  for (int i = threadIdx.x; i < n; i += 256) words[i] = make_uint4(0, 0, 0, 0);
+}
+
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
   if (!fn) {
@@ -978,7 +990,7 @@ int launch_variant(const Fp8Params& p, cudaStream_t st) {
                                       cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem));
     attr = true;
   }
-  if (p.early) {
+  if (p.after != kAfterAny) {
     // scheduled as the CTAs of the kernel before it end (see pdl_wait in the kernel)
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(sm_count());
@@ -1003,6 +1015,13 @@ int launch_variant(const Fp8Params& p, cudaStream_t st) {
 
 // lane quarters a tile can fill
 static int quarters_of(int max_rows) { return ceil_div(std::min(std::max(max_rows, 1), 128), 32); }
+
+int launch_clear(void* words, size_t bytes, cudaStream_t st) {
+  clear_kernel<<<1, 256, 0, st>>>(static_cast<uint4*>(words), (int)(bytes / 16));
+  MOE_COUNT_LAUNCH();
+  MOE_LAUNCH_CHECK();
+  return MOE_OK;
+}
 
 Fp8Plan plan_fp8(const Fp8Args& a) {
   Fp8Plan pl{};
@@ -1032,7 +1051,7 @@ int launch_fp8(const Fp8Args& a, const Fp8Plan&, float* part, int32_t* counters,
   p.dev_tab = a.dev_tab; p.w_off = a.w_off; p.s_off = a.s_off; p.ws = a.ws;
   p.active = a.active; p.n_active = a.n_active; p.host_n = a.host_n;
   for (int i = 0; i < (a.host_n > 0 ? a.host_n : 0); ++i) p.host_ids[i] = (int16_t)a.host_ids[i];
-  p.hq = a.hq; p.hs = a.hs; p.y = a.y; p.y_f32 = a.y_f32; p.early = a.early;
+  p.hq = a.hq; p.hs = a.hs; p.y = a.y; p.y_f32 = a.y_f32; p.after = a.after;
   p.part = part; p.counters = counters; p.err = err;
   if (a.fused) return launch_variant<true, false>(p, st);
   return a.w ? launch_variant<false, true>(p, st) : launch_variant<false, false>(p, st);

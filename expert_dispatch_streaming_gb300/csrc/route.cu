@@ -45,7 +45,7 @@ __global__ void __launch_bounds__(256)
 router_partial_kernel(const uint16_t* __restrict__ x, const float* __restrict__ w_r,
                       const uint16_t* __restrict__ w_gate, int T, int H, int E, int C,
                       int h_per_split, float* __restrict__ part, int32_t* __restrict__ hist,
-                      int hist_n) {
+                      int hist_n, int32_t* __restrict__ err) {
   pdl_trigger();
   pdl_wait();
   __shared__ float xs[R_KH][R_BT + 1];
@@ -55,9 +55,12 @@ router_partial_kernel(const uint16_t* __restrict__ x, const float* __restrict__ 
   const int t0 = blockIdx.x * R_BT, c0 = blockIdx.y * R_BC, split = blockIdx.z;
   const int h_lo = split * h_per_split, h_hi = min(H, h_lo + h_per_split);
 
-  // the first CTA clears the per-tile histogram the gating kernel accumulates into
-  if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0)
+  // the first CTA clears the per-tile histogram the gating kernel accumulates into (and the error
+  // word, where the call leaves it to this kernel)
+  if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) {
     for (int i = tid; i < hist_n; i += blockDim.x) hist[i] = 0;
+    if (tid == 0 && err) *err = 0;
+  }
 
   // The loads of up to kPf 32-row tiles are issued together, into registers, before any of
   // them is used: a CTA's slice of a small batch is a few tiles, and one memory latency per
@@ -162,7 +165,8 @@ constexpr int kPrepM = 64, kPrepK = 64;
 __global__ void __launch_bounds__(256)
 router_prep_kernel(const float* __restrict__ w_r, const uint16_t* __restrict__ w_gate, int H,
                    int E, int Mpad, int T, uint16_t* __restrict__ img, float* __restrict__ w_rT,
-                   int32_t* __restrict__ hist, int hist_n, int32_t* __restrict__ meta) {
+                   int32_t* __restrict__ hist, int hist_n, int32_t* __restrict__ meta,
+                   int32_t* __restrict__ err) {
   pdl_trigger();
   pdl_wait();
   __shared__ float blk[kPrepK][kPrepM + 1];
@@ -170,6 +174,7 @@ router_prep_kernel(const float* __restrict__ w_r, const uint16_t* __restrict__ w
   if (blockIdx.x == 0 && blockIdx.y == 0) {
     for (int i = tid; i < hist_n; i += blockDim.x) hist[i] = 0;
     if (tid == 0) { meta[0] = 0; meta[1] = T; meta[2] = 0; meta[3] = 1; }
+    if (tid == 0 && err) *err = 0;
   }
   // all 16 loads of a thread issued before the first use (one memory latency, not sixteen)
   float ld[kPrepK * kPrepM / 256];
@@ -471,11 +476,13 @@ size_t route_scratch(WsCursor& c, const RoutePlan& r, int T, int E, RouteScratch
 
 int launch_route(const RouteArgs& a, const RoutePlan& r, const RouteScratch& s,
                  cudaStream_t st) {
+  const bool grouped = a.n_group > 0;
+  int32_t* clear = a.clear_err ? a.err : nullptr;
   if (a.T > 0) {
     if (r.tc) {
       MOE_LAUNCH_PDL(router_prep_kernel, dim3(r.Mpad / kPrepM, a.H / kPrepK), dim3(256), 0, st,
                      a.w_r, a.w_gate, a.H, a.E, r.Mpad, a.T, s.img, s.w_rT, s.hist,
-                     r.ntiles * a.E, s.shared_meta);
+                     r.ntiles * a.E, s.shared_meta, clear);
       MOE_COUNT_LAUNCH();
       MOE_LAUNCH_CHECK();
       const int rr = launch_tc_router(a.x, a.T, a.H, s.img, r.Mpad, r.C, s.shared_meta, s.part,
@@ -486,11 +493,12 @@ int launch_route(const RouteArgs& a, const RoutePlan& r, const RouteScratch& s,
         dim3 g1(ceil_div(a.T, R_BT), 1, r.S);
         MOE_LAUNCH_PDL(router_partial_kernel<kRouterSmallC>, g1, dim3(256), 0, st, a.x, a.w_r,
                        a.w_gate, a.T, a.H, a.E, r.C, r.h_per_split, s.part, s.hist,
-                       r.ntiles * a.E);
+                       r.ntiles * a.E, clear);
       } else {
         dim3 g1(ceil_div(a.T, R_BT), ceil_div(r.C, 64), r.S);
         MOE_LAUNCH_PDL(router_partial_kernel<64>, g1, dim3(256), 0, st, a.x, a.w_r, a.w_gate,
-                       a.T, a.H, a.E, r.C, r.h_per_split, s.part, s.hist, r.ntiles * a.E);
+                       a.T, a.H, a.E, r.C, r.h_per_split, s.part, s.hist, r.ntiles * a.E,
+                       clear);
       }
       MOE_COUNT_LAUNCH();
       MOE_LAUNCH_CHECK();
@@ -504,8 +512,7 @@ int launch_route(const RouteArgs& a, const RoutePlan& r, const RouteScratch& s,
       p.shared_gate = a.shared_gate; p.tie_flags = a.tie_flags; p.hist = nullptr;
       if (a.n_group)
         return launch_route_group_tail(p, a.n_group, a.take, a.counts, a.offsets, a.pos, a.src,
-                                       s.active, s.n_active, s.shared_meta, a.x_perm,
-                                       a.clear_err ? a.err : nullptr, st);
+                                       s.active, s.n_active, s.shared_meta, a.x_perm, st);
       MOE_LAUNCH_PDL(route_tail_kernel, dim3(1), dim3(kTailThreads), 0, st, p, a.counts,
                      a.offsets, a.pos, a.src, s.active, s.n_active, s.shared_meta, a.x_perm);
       MOE_COUNT_LAUNCH();
@@ -515,8 +522,8 @@ int launch_route(const RouteArgs& a, const RoutePlan& r, const RouteScratch& s,
     int S_gate = r.S;
     if (r.S > 4) {
       const int n = a.T * r.C;
-      MOE_LAUNCH_PDL(reduce_slices_kernel, dim3(ceil_div(8 * n, 256)), dim3(256), 0, st, s.part,
-                     r.S, n);
+      MOE_LAUNCH_NEXT(grouped, reduce_slices_kernel, dim3(ceil_div(8 * n, 256)), dim3(256), 0, st,
+                      s.part, r.S, n);
       MOE_COUNT_LAUNCH();
       MOE_LAUNCH_CHECK();
       S_gate = 1;
@@ -553,8 +560,9 @@ int launch_route(const RouteArgs& a, const RoutePlan& r, const RouteScratch& s,
       MOE_LAUNCH_CHECK();
     }
   }
-  MOE_LAUNCH_PDL(scan_kernel, dim3(1), dim3(kMaxExperts), 0, st, s.hist, r.ntiles, a.E,
-                 a.counts, a.offsets, s.base, s.active, s.n_active, s.shared_meta, a.T);
+  MOE_LAUNCH_NEXT(grouped && a.T > 0, scan_kernel, dim3(1), dim3(kMaxExperts), 0, st, s.hist,
+                  r.ntiles, a.E, a.counts, a.offsets, s.base, s.active, s.n_active, s.shared_meta,
+                  a.T);
   MOE_COUNT_LAUNCH();
   MOE_LAUNCH_CHECK();
   if (a.T > 0) {
@@ -562,9 +570,9 @@ int launch_route(const RouteArgs& a, const RoutePlan& r, const RouteScratch& s,
     // one warp per destination row over the whole GPU (the per-tile grid is too small)
     const bool fused_copy =
         a.x_perm && (size_t)a.T * a.k * a.H * 2 <= kFusedGatherMaxBytes && a.T < kSeparateGatherMinT;
-    MOE_LAUNCH_PDL(rank_permute_kernel, dim3(r.ntiles), dim3(256), 0, st, a.ids, s.base, a.T,
-                   a.k, a.E, a.H, a.x, a.pos, a.src,
-                   fused_copy ? a.x_perm : static_cast<uint16_t*>(nullptr));
+    MOE_LAUNCH_NEXT(grouped, rank_permute_kernel, dim3(r.ntiles), dim3(256), 0, st, a.ids, s.base,
+                    a.T, a.k, a.E, a.H, a.x, a.pos, a.src,
+                    fused_copy ? a.x_perm : static_cast<uint16_t*>(nullptr));
     MOE_COUNT_LAUNCH();
     MOE_LAUNCH_CHECK();
     if (a.x_perm && !fused_copy) {

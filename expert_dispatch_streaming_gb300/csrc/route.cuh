@@ -77,8 +77,29 @@ struct RouteArgs {
   uint16_t* x_perm;  // nullable: fused gather into expert order
   int32_t* err;      // device error word (bounded waits of the tensor-core router)
   int n_group, take; // group-limited selection: `take` of n_group groups; 0 = no groups
-  int clear_err;     // group-limited, small batch: the kernels clear *err themselves
+  int clear_err;     // group-limited: the first kernel clears *err
 };
+
+// launch_pdl, with programmatic stream serialization whatever MOE_OPT_PDL says when `chained`: for
+// a kernel whose predecessor on the stream is one of the library's that the same call launched
+// (group-limited routing's five launches, 60 experts and 333 tokens: 37 us plain, 31 chained).
+template <typename... KArgs, typename... Args>
+cudaError_t launch_next(bool chained, void (*kernel)(KArgs...), dim3 grid, dim3 block,
+                        size_t smem, cudaStream_t st, Args&&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = chained || g_use_pdl ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+#define MOE_LAUNCH_NEXT(chained, kernel, grid, block, smem, st, ...) \
+  MOE_CUDA_TRY(::moe::launch_next(chained, kernel, grid, block, smem, st, __VA_ARGS__))
 
 RoutePlan plan_route(int T, int H, int E, int k, bool has_gate);
 size_t route_scratch(WsCursor& c, const RoutePlan& r, int T, int E, RouteScratch* out);
@@ -90,7 +111,7 @@ int launch_gate_group(const GateParams& p, int n_group, int take, cudaStream_t s
 int launch_route_group_tail(const GateParams& p, int n_group, int take, int32_t* counts,
                             int32_t* offsets, int32_t* pos, int32_t* src, int32_t* active,
                             int32_t* n_active, int32_t* shared_meta, uint16_t* x_perm,
-                            int32_t* err, cudaStream_t st);
+                            cudaStream_t st);
 int launch_gather(const uint16_t* x, const int32_t* src, int rows, int k, int H,
                   uint16_t* x_perm, cudaStream_t st);
 

@@ -504,7 +504,7 @@ gate_group_kernel(const __grid_constant__ GateParams p, int n_group, int take) {
 
 // Everything after the router product for a batch of at most kSmallT tokens in one CTA, as
 // route_tail_kernel: the slices of every logit summed in a fixed order, one warp a token gating,
-// then the counts, scan, ranks and tables.  err: an error word to clear (NULL: none).
+// then the counts, scan, ranks and tables.
 constexpr int kTailWarps = 32;
 struct GroupTailSmem {
   TailSmem tail;                 // (lrow / exact_s unused)
@@ -519,7 +519,7 @@ route_group_tail_kernel(GateParams p, int n_group, int take, int32_t* __restrict
                         int32_t* __restrict__ offsets, int32_t* __restrict__ pos,
                         int32_t* __restrict__ src, int32_t* __restrict__ active,
                         int32_t* __restrict__ n_active, int32_t* __restrict__ shared_meta,
-                        uint16_t* __restrict__ x_perm, int32_t* __restrict__ err) {
+                        uint16_t* __restrict__ x_perm) {
   pdl_trigger();
   pdl_wait();
   extern __shared__ __align__(16) uint8_t raw_smem[];
@@ -527,7 +527,6 @@ route_group_tail_kernel(GateParams p, int n_group, int take, int32_t* __restrict
   constexpr int NT = kTailWarps * 32;
   const int tid = threadIdx.x, warp = tid >> 5, T = p.T, C = p.C, E = p.E, S = p.S, n = T * C;
   const size_t stride = (size_t)T * C;
-  if (tid == 0 && err) *err = 0;
   // the logits: thread (g, li) sums slices g, g + G, ... of logit li (their loads in flight
   // together, neighbouring logits side by side), then the G sums in order
   const int G = max(1, NT / n);
@@ -634,7 +633,7 @@ route_group_tail_kernel(GateParams p, int n_group, int take, int32_t* __restrict
 int launch_route_group_tail(const GateParams& p, int n_group, int take, int32_t* counts,
                             int32_t* offsets, int32_t* pos, int32_t* src, int32_t* active,
                             int32_t* n_active, int32_t* shared_meta, uint16_t* x_perm,
-                            int32_t* err, cudaStream_t st) {
+                            cudaStream_t st) {
   static bool attr = false;
   if (!attr) {
     MOE_CUDA_TRY(cudaFuncSetAttribute(route_group_tail_kernel,
@@ -642,9 +641,9 @@ int launch_route_group_tail(const GateParams& p, int n_group, int take, int32_t*
                                       (int)sizeof(GroupTailSmem)));
     attr = true;
   }
-  MOE_LAUNCH_PDL(route_group_tail_kernel, dim3(1), dim3(kTailWarps * 32), sizeof(GroupTailSmem),
-                 st, p, n_group, take, counts, offsets, pos, src, active, n_active, shared_meta,
-                 x_perm, err);
+  MOE_LAUNCH_NEXT(true, route_group_tail_kernel, dim3(1), dim3(kTailWarps * 32),
+                  sizeof(GroupTailSmem), st, p, n_group, take, counts, offsets, pos, src, active,
+                  n_active, shared_meta, x_perm);
   MOE_COUNT_LAUNCH();
   MOE_LAUNCH_CHECK();
   return MOE_OK;
@@ -653,10 +652,14 @@ int launch_route_group_tail(const GateParams& p, int n_group, int take, int32_t*
 int launch_gate_group(const GateParams& p, int n_group, int take, cudaStream_t st) {
   const GateParams& q = p;
   const dim3 grid(ceil_div(q.T, G_WARPS)), block(G_WARPS * 32);
-  if (q.E <= 32) MOE_LAUNCH_PDL(gate_group_kernel<1>, grid, block, 0, st, q, n_group, take);
-  else if (q.E <= 64) MOE_LAUNCH_PDL(gate_group_kernel<2>, grid, block, 0, st, q, n_group, take);
-  else if (q.E <= 128) MOE_LAUNCH_PDL(gate_group_kernel<4>, grid, block, 0, st, q, n_group, take);
-  else MOE_LAUNCH_PDL(gate_group_kernel<EC>, grid, block, 0, st, q, n_group, take);
+  if (q.E <= 32)
+    MOE_LAUNCH_NEXT(true, gate_group_kernel<1>, grid, block, 0, st, q, n_group, take);
+  else if (q.E <= 64)
+    MOE_LAUNCH_NEXT(true, gate_group_kernel<2>, grid, block, 0, st, q, n_group, take);
+  else if (q.E <= 128)
+    MOE_LAUNCH_NEXT(true, gate_group_kernel<4>, grid, block, 0, st, q, n_group, take);
+  else
+    MOE_LAUNCH_NEXT(true, gate_group_kernel<EC>, grid, block, 0, st, q, n_group, take);
   MOE_COUNT_LAUNCH();
   MOE_LAUNCH_CHECK();
   return MOE_OK;
