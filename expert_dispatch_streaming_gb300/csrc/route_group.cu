@@ -610,13 +610,14 @@ route_group_tail_kernel(GateParams p, int n_group, int take, int32_t* __restrict
   __syncthreads();
   // ---- stable ranks: pair i goes after every earlier pair of its expert
   if (tid < T * k) {
-    const int e = __ldcg(p.ids + tid);
+    const int t = tid / k, e = sm.g[t].ids[tid - t * k];
     int rank = 0;
-    for (int i = 0; i < tid; ++i) rank += __ldcg(p.ids + i) == e;
+    for (int i = 0; i < t; ++i)
+      for (int j = 0; j < k; ++j) rank += sm.g[i].ids[j] == e;   // (a token's own are distinct)
     const int pp = sm.tail.excl[e] + rank;
     pos[tid] = pp;
     src[pp] = tid;
-    sm.tail.srow[pp] = tid / k;
+    sm.tail.srow[pp] = t;
   }
   if (!x_perm) return;
   __syncthreads();
