@@ -103,18 +103,27 @@ struct GroupRank {
   float score, least, kth, nxt;
   int rank;
 };
-__device__ __noinline__ GroupRank rank_groups(const Groups& G, const GroupSmem& sm) {
+__device__ __forceinline__ GroupRank rank_groups(const Groups& G, const GroupSmem& sm) {
   const int lane = threadIdx.x & 31, g = lane / G.P, part = lane % G.P;
   float m1 = -CUDART_INF_F, m2 = -CUDART_INF_F;
-  if (g < G.n)
+  if (g < G.n) {
+    // eight scores at a time, their loads in flight together
+    const float* s = sm.srow + g * G.gs;
 #pragma unroll 1
-    for (int i = part; i < G.gs; i += G.P) {
-      const float s = sm.srow[g * G.gs + i];
-      m2 = fmaxf(m2, fminf(m1, s));
-      m1 = fmaxf(m1, s);
+    for (int i0 = part; i0 < G.gs; i0 += 8 * G.P) {
+      float v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = i0 + j * G.P < G.gs ? s[i0 + j * G.P] : -CUDART_INF_F;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        m2 = fmaxf(m2, fminf(m1, v[j]));
+        m1 = fmaxf(m1, v[j]);
+      }
     }
-#pragma unroll 1
-  for (int o = 1; o < G.P; o <<= 1) {
+  }
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    if (o >= G.P) break;
     const float a1 = __shfl_xor_sync(0xffffffffu, m1, o), a2 = __shfl_xor_sync(0xffffffffu, m2, o);
     m2 = fmaxf(fmaxf(m2, a2), fminf(m1, a1));
     m1 = fmaxf(m1, a1);
@@ -127,8 +136,14 @@ __device__ __noinline__ GroupRank rank_groups(const Groups& G, const GroupSmem& 
   r.kth = 0.f;
   r.nxt = -CUDART_INF_F;
 #pragma unroll 1
-  for (int q = 0; q < G.n; ++q)
-    r.rank += better(__shfl_sync(0xffffffffu, r.score, G.lane_of(q)), q, r.score, g);
+  for (int q0 = 0; q0 < G.n; q0 += 8) {
+    float o[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)     // (past the last group: a lane of no group, not counted)
+      o[j] = __shfl_sync(0xffffffffu, r.score, G.lane_of(q0 + j) & 31);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) r.rank += q0 + j < G.n && better(o[j], q0 + j, r.score, g);
+  }
   if (g >= G.n) r.rank = 32;
   const unsigned bk = __ballot_sync(0xffffffffu, r.rank == G.take - 1);
   const unsigned bn = __ballot_sync(0xffffffffu, r.rank == G.take);
@@ -160,10 +175,16 @@ __device__ __noinline__ Top top_experts(const Groups& G, const GroupSmem& sm, un
     uint32_t best = 0;
     int id = 0x7fffffff;
 #pragma unroll
+    for (int c = 0; c < NC; ++c) best = max(best, key[c]);
+#pragma unroll
     for (int c = NC - 1; c >= 0; --c)
-      if (key[c] >= best) { best = key[c]; id = lane + 32 * c; }
+      if (key[c] == best) id = lane + 32 * c;
     const uint32_t top = __reduce_max_sync(0xffffffffu, best);
-    id = (int)__reduce_min_sync(0xffffffffu, best == top ? (unsigned)id : 0x7fffffffu);
+    const unsigned ties = __ballot_sync(0xffffffffu, best == top);
+    if ((ties & (ties - 1)) == 0)
+      id = __shfl_sync(0xffffffffu, id, __ffs(ties) - 1);
+    else
+      id = (int)__reduce_min_sync(0xffffffffu, best == top ? (unsigned)id : 0x7fffffffu);
     if (i == k - 1) r.kth = key_score(top);
     if (i == k) r.nxt = key_score(top);
     const bool won = (id & 31) == lane;
@@ -175,18 +196,62 @@ __device__ __noinline__ Top top_experts(const Groups& G, const GroupSmem& sm, un
   return r;
 }
 
+// The same where no boundary is near: the k are taken by the upper 24 bits of their keys, ties to
+// the lower expert (one warp reduction a round, where the exact order takes three dependent ones),
+// then kth and nxt are the exact worst taken and best left.  A wrong choice shows as kth < nxt.
+template <int NC>
+__device__ __forceinline__ Top top_quick(const Groups& G, const GroupSmem& sm, unsigned gm, int E,
+                                         int k) {
+  const int lane = threadIdx.x & 31;
+  uint32_t key[NC], cut[NC];
+  unsigned open = 0, left = 0;
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    const int e = lane + 32 * c;
+    const bool in = e < E && ((gm >> G.lane_of(G.of(e))) & 1);
+    key[c] = score_key(sm.srow[min(e, E - 1)]);
+    cut[c] = in ? (key[c] & ~255u) | (255u - e) : 0u;
+    open |= (unsigned)in << c;
+  }
+#pragma unroll 1
+  for (int i = 0; i < k; ++i) {
+    uint32_t best = 0;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) best = max(best, cut[c]);
+    const uint32_t top = __reduce_max_sync(0xffffffffu, best);
+#pragma unroll
+    for (int c = 0; c < NC; ++c) cut[c] = cut[c] == top ? 0u : cut[c];
+  }
+  uint32_t worst = 0xffffffffu, next = 0u;
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    left |= (unsigned)(cut[c] != 0u) << c;
+    if (cut[c]) next = max(next, key[c]);
+    else if ((open >> c) & 1) worst = min(worst, key[c]);
+  }
+  Top r;
+  r.chosen = open & ~left;
+  r.kth = key_score(__reduce_min_sync(0xffffffffu, worst));
+  next = __reduce_max_sync(0xffffffffu, next);
+  r.nxt = next ? key_score(next) : -CUDART_INF_F;
+  return r;
+}
+
 // The chosen in ascending id order, lane j the j-th, and their weights (those of gate_finish,
 // which has one lane do it, summed in the same order).
-__device__ __noinline__ void finish_token(const GateParams& p, int t, GroupSmem& sm,
-                                          unsigned chosen, int flag) {
+template <int NC>
+__device__ __forceinline__ void finish_token(const GateParams& p, int t, GroupSmem& sm,
+                                             unsigned chosen, int flag) {
   const int lane = threadIdx.x & 31, E = p.E, k = p.k;
   const bool sig = p.mode == MOE_GATING_SIGMOID_BIAS_RENORM;
+  unsigned m[NC];
+#pragma unroll
+  for (int c = 0; c < NC; ++c) m[c] = __ballot_sync(0xffffffffu, (chosen >> c) & 1);
   int base = 0;
-#pragma unroll 1
-  for (int c = 0; 32 * c < E; ++c) {
-    const unsigned m = __ballot_sync(0xffffffffu, (chosen >> c) & 1);
-    if ((chosen >> c) & 1) sm.ids[base + __popc(m & ((1u << lane) - 1u))] = lane + 32 * c;
-    base += __popc(m);
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    if ((chosen >> c) & 1) sm.ids[base + __popc(m[c] & ((1u << lane) - 1u))] = lane + 32 * c;
+    base += __popc(m[c]);
   }
   __syncwarp();
   const int id = lane < k ? sm.ids[lane] : 0;
@@ -208,9 +273,13 @@ __device__ __noinline__ void finish_token(const GateParams& p, int t, GroupSmem&
       denom = warp_sum(denom);
     }
   }
-  if (!all)
-#pragma unroll 1
-    for (int j = 0; j < k; ++j) denom += __shfl_sync(0xffffffffu, v, j);
+  if (!all) {
+    float o[kMaxK];
+#pragma unroll
+    for (int j = 0; j < kMaxK; ++j) o[j] = __shfl_sync(0xffffffffu, v, j);
+#pragma unroll
+    for (int j = 0; j < kMaxK; ++j) denom += j < k ? o[j] : 0.f;
+  }
   // a token whose chosen scores are all zero (every expert left to it is masked) would get
   // 0 / 0: its weights are zero instead
   const float has = lane >= k ? 0.f : sig ? v : (lj == -CUDART_INF_F ? 0.f : 1.f);
@@ -234,9 +303,9 @@ __device__ __forceinline__ bool gate_quick(const GateParams& p, const Groups& G,
   const GroupRank r = rank_groups(G, sm);
   if (r.kth - r.nxt <= (G.pairs ? 2.f * kTau : kTau)) return false;
   const unsigned lead = __ballot_sync(0xffffffffu, r.rank < G.take);
-  const Top top = top_experts<NC>(G, sm, lead, p.E, p.k);
+  const Top top = top_quick<NC>(G, sm, lead, p.E, p.k);
   if (top.kth - top.nxt <= kTau) return false;
-  finish_token(p, t, sm, top.chosen, 0);
+  finish_token<NC>(p, t, sm, top.chosen, 0);
   return true;
 }
 
@@ -456,7 +525,7 @@ __device__ __noinline__ void gate_slow(const GateParams& p, const Groups& G, int
     }
     top.chosen = chosen;
   }
-  finish_token(p, t, sm, top.chosen, flag);
+  finish_token<NC>(p, t, sm, top.chosen, flag);
 }
 
 // The tokens of the CTA's warps that need re-scoring (bit w of `slow`: warp w's, t0 + w), one after
