@@ -20,10 +20,14 @@ constexpr int kFp8TileBytes = 16384;    // 128 rows x 128 k
 // conversions merge into one register without extracting and shifting 16-bit values.)
 __device__ __forceinline__ uint32_t fp8_pack4(float a, float b, float c, float d, float inv) {
   uint32_t r;
-  asm("{\n.reg .b16 l, h;\ncvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n"
-      "cvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\nmov.b32 %0, {l, h};\n}\n"
+  asm("{\n.reg .b64 p, q, s;\n.reg .f32 e, f, g, i;\n.reg .b16 l, h;\n"
+      "mov.b64 p, {%1, %2};\nmov.b64 q, {%3, %4};\nmov.b64 s, {%5, %5};\n"
+      "mul.rn.f32x2 p, p, s;\nmul.rn.f32x2 q, q, s;\n"
+      "mov.b64 {e, f}, p;\nmov.b64 {g, i}, q;\n"
+      "cvt.rn.satfinite.e4m3x2.f32 l, f, e;\ncvt.rn.satfinite.e4m3x2.f32 h, i, g;\n"
+      "mov.b32 %0, {l, h};\n}\n"
       : "=r"(r)
-      : "f"(a * inv), "f"(b * inv), "f"(c * inv), "f"(d * inv));
+      : "f"(a), "f"(b), "f"(c), "f"(d), "f"(inv));
   return r;
 }
 

@@ -12,11 +12,10 @@ namespace {
 // The largest magnitude of bf16 values is taken in bf16, which is exact and skips NaNs.
 constexpr int kCols = 1024;
 
+// The larger magnitudes of two pairs, in one instruction; the signs are of no meaning.
 __device__ __forceinline__ uint32_t abs_max2(uint32_t a, uint32_t b) {
   uint32_t d;
-  asm("{\n.reg .b32 s, t;\nabs.bf16x2 s, %1;\nabs.bf16x2 t, %2;\nmax.bf16x2 %0, s, t;\n}\n"
-      : "=r"(d)
-      : "r"(a), "r"(b));
+  asm("max.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
 
@@ -64,7 +63,7 @@ quantize_fp8_kernel(const uint16_t* __restrict__ x, const int32_t* __restrict__ 
   // one division a lane: of a block's eight lanes, the first four take 448 / amax and amax / 448
   // of the two halves
   const int kind = lane & 3;
-  const float m = fmaxf(kind < 2 ? mf.x : mf.y, kFp8MinAmax);
+  const float m = fmaxf(fabsf(kind < 2 ? mf.x : mf.y), kFp8MinAmax);
   const float d = __fdiv_rn(kind & 1 ? m : kFp8Max, kind & 1 ? kFp8Max : m);
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
