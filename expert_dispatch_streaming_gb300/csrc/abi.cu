@@ -57,6 +57,19 @@ static bool valid_groups(int E, int k, int n_group, int take) {
          take <= n_group && k <= take * (E / n_group);
 }
 
+static size_t route_workspace(int T, int H, int E, int k, bool grouped) {
+  // the slice count depends on whether the shared-expert gate column is present: size for both
+  WsCursor a(nullptr, 0), b(nullptr, 0);
+  a.take<int32_t>(64);
+  b.take<int32_t>(64);
+  return std::max(route_scratch(a, plan_route(T, H, E, k, true, grouped), T, E, nullptr),
+                  route_scratch(b, plan_route(T, H, E, k, false, grouped), T, E, nullptr));
+}
+
+size_t route_workspace_ungrouped(int T, int H, int E, int k) {
+  return valid_route_shape(T, H, E, k) ? route_workspace(T, H, E, k, false) : 0;
+}
+
 // moe_route_topk and moe_route_topk_grouped (n_group = 0: no groups)
 static int route_topk(const uint16_t* x, const float* w_r, const float* logit_bias,
                       const float* sel_bias, const uint16_t* w_gate, const int32_t* forced_ids,
@@ -69,7 +82,7 @@ static int route_topk(const uint16_t* x, const float* w_r, const float* logit_bi
   MOE_REQUIRE(counts && offsets && ws);
   MOE_REQUIRE(T == 0 || (x && w_r && ids && w && pos && src));
   MOE_REQUIRE(!w_gate || shared_gate);
-  const RoutePlan rp = plan_route(T, H, E, k, w_gate != nullptr);
+  const RoutePlan rp = plan_route(T, H, E, k, w_gate != nullptr, n_group > 0);
   WsCursor c(ws, ws_bytes);
   int32_t* err = c.take<int32_t>(64);
   RouteScratch s{};
@@ -159,7 +172,7 @@ static int make_plan(const moe_layer* L, int T, LayerPlan* P) {
   if (L->Is && moe_bundle_layout_of(L->H, L->Is, L->wdtype, &P->slay) != MOE_OK)
     return MOE_ERR_INVALID_ARG;
   const int rows = T * L->k;
-  P->rp = plan_route(T, L->H, L->E, L->k, L->Is > 0 && L->shared_gate_sigmoid);
+  P->rp = plan_route(T, L->H, L->E, L->k, L->Is > 0 && L->shared_gate_sigmoid, grouped(L));
   if (L->wdtype == MOE_W_FP8_B128) {
     P->fp8 = 1;
     P->qgu = plan_fp8(fp8_args(P->lay, true, L->H, L->I, L->E, rows));
@@ -415,12 +428,7 @@ int moe_workspace_error(const void* ws, int32_t* code, void* stream) {
 
 size_t moe_route_workspace_size(int T, int H, int E, int k) {
   if (!valid_route_shape(T, H, E, k)) return 0;
-  // the slice count depends on whether the shared-expert gate column is present: size for both
-  WsCursor a(nullptr, 0), b(nullptr, 0);
-  a.take<int32_t>(64);
-  b.take<int32_t>(64);
-  return std::max(route_scratch(a, plan_route(T, H, E, k, true), T, E, nullptr),
-                  route_scratch(b, plan_route(T, H, E, k, false), T, E, nullptr));
+  return std::max(route_workspace(T, H, E, k, false), route_workspace(T, H, E, k, true));
 }
 
 int moe_route_topk(const uint16_t* x, const float* w_r, const float* logit_bias,
@@ -555,6 +563,11 @@ int moe_layer_forward(const moe_layer* L, const uint16_t* x, int T, const int32_
   MOE_REQUIRE(!cache || (cache_live(cache) && cache->E == L->E && L->layer_index >= 0 &&
                          L->layer_index < cache->L &&
                          cache->slot_bytes >= P.lay.total_bytes));
+  if (P.fp8) {   // (copied from by TMA: 16-byte aligned bundles)
+    MOE_REQUIRE(!cache || cache->slot_bytes % 16 == 0);
+    MOE_REQUIRE(aligned16(L->shared_bundle));
+    for (int e = 0; !cache && e < L->E; ++e) MOE_REQUIRE(aligned16(L->bundles[e]));
+  }
   void* const* pev = st ? st->phase_events : nullptr;
   if (st) {
     std::memset(st, 0, sizeof(*st));

@@ -428,8 +428,9 @@ route_tail_kernel(GateParams p, int32_t* __restrict__ counts, int32_t* __restric
 }
 
 // ------------------------------------------------------------------------------ host side
-RoutePlan plan_route(int T, int H, int E, int k, bool has_gate) {
+RoutePlan plan_route(int T, int H, int E, int k, bool has_gate, bool grouped) {
   RoutePlan r{};
+  r.own_tc = grouped && T >= kOwnTcMinT && H % 64 == 0;
   r.C = E + (has_gate ? 1 : 0);
   r.ntiles = ceil_div(T, kTileT);
   if (T >= kTcRouterMinT && H % 64 == 0) {
@@ -437,7 +438,7 @@ RoutePlan plan_route(int T, int H, int E, int k, bool has_gate) {
     r.Mpad = (int)round_up(r.C, 128);
     r.S = 1;
     r.h_per_split = H;
-    r.tc_S = tc_router_splits(T, H, r.Mpad);
+    r.tc_S = r.own_tc ? route_tc_parts(T, H, r.Mpad) : tc_router_splits(T, H, r.Mpad);
     return r;
   }
   const int tiles = ceil_div(T, R_BT) * ceil_div(r.C, r.C <= kRouterSmallC ? kRouterSmallC : 64);
@@ -466,7 +467,7 @@ size_t route_scratch(WsCursor& c, const RoutePlan& r, int T, int E, RouteScratch
   if (r.tc) {
     s.img = c.take<uint16_t>((size_t)3 * r.Mpad * r.h_per_split);
     s.w_rT = c.take<float>((size_t)E * r.h_per_split);
-    if (r.tc_S > 1) {
+    if (r.tc_S > 1 || r.own_tc) {
       s.tc_part = c.take<float>((size_t)r.tc_S * T * r.Mpad);
     }
   }
@@ -485,8 +486,10 @@ int launch_route(const RouteArgs& a, const RoutePlan& r, const RouteScratch& s,
                      r.ntiles * a.E, s.shared_meta, clear);
       MOE_COUNT_LAUNCH();
       MOE_LAUNCH_CHECK();
-      const int rr = launch_tc_router(a.x, a.T, a.H, s.img, r.Mpad, r.C, s.shared_meta, s.part,
-                                      s.tc_part, a.err, st);
+      const int rr = r.own_tc ? launch_route_tc(a.x, a.T, a.H, s.img, r.Mpad, r.tc_S, s.tc_part,
+                                                a.err, st)
+                              : launch_tc_router(a.x, a.T, a.H, s.img, r.Mpad, r.C, s.shared_meta,
+                                                s.part, s.tc_part, a.err, st);
       if (rr != MOE_OK) return rr;
     } else {
       if (r.C <= kRouterSmallC) {
@@ -530,7 +533,7 @@ int launch_route(const RouteArgs& a, const RoutePlan& r, const RouteScratch& s,
     }
     GateParams p{};
     p.part = s.part; p.S = S_gate; p.C = r.C; p.ldp = r.C;
-    if (r.tc && r.tc_S > 1) {
+    if (r.tc && (r.tc_S > 1 || r.own_tc)) {
       // the router GEMM's split partials, [tc_S][T][Mpad]: summed here, in split order
       p.part = s.tc_part;
       p.S = r.tc_S;

@@ -38,11 +38,16 @@ struct RoutePlan {
   int tc;           // 1: router product on the tensor cores (bf16 x 3 pieces), S = 1
   int Mpad;         // rows of the tensor-core router image (C rounded up to 128)
   int tc_S;         // K splits of the tensor-core router product
+  int own_tc;       // 1: the router product is route_tc.cu's, in tc_S >= 1 parts
   int small;        // 1: gating, scan, ranks and row copy in one CTA (T <= kSmallT)
 };
 
 // batches of at least this many tokens compute the router product on the tensor cores
 constexpr int kTcRouterMinT = 256;
+// ... and group-limited ones of at least this many by route_tc.cu's kernel (the whole routing of
+// 7168 x 256 experts: 512 tokens 49 us instead of 56, 1024 57 / 68, 8192 151 / 184).  It is the
+// faster one for 256 tokens too (53 / 62), but there the logits stay moe_route_topk's to the bit.
+constexpr int kOwnTcMinT = 512;
 // batches of at most this many tokens run everything after the router product in one CTA
 constexpr int kSmallT = 16;
 // batches of at least this many tokens gather x_perm in a separate, GPU-wide kernel
@@ -60,7 +65,7 @@ struct RouteScratch {
   int32_t* shared_meta;  // {0, T, 0, 1}: offsets / active list / count of the shared expert
   uint16_t* img;         // tensor-core router: [Mpad x 3H] tiled bf16 pieces
   float* w_rT;           // tensor-core router: [E][H] fp32
-  float* tc_part;        // tensor-core router, tc_S > 1: [tc_S][T][Mpad] fp32 partials
+  float* tc_part;        // tensor-core router, tc_S > 1 or own_tc: [tc_S][T][Mpad] fp32 partials
 };
 
 struct RouteArgs {
@@ -101,7 +106,13 @@ cudaError_t launch_next(bool chained, void (*kernel)(KArgs...), dim3 grid, dim3 
 #define MOE_LAUNCH_NEXT(chained, kernel, grid, block, smem, st, ...) \
   MOE_CUDA_TRY(::moe::launch_next(chained, kernel, grid, block, smem, st, __VA_ARGS__))
 
-RoutePlan plan_route(int T, int H, int E, int k, bool has_gate);
+RoutePlan plan_route(int T, int H, int E, int k, bool has_gate, bool grouped = false);
+// moe_route_workspace_size without what group-limited routing needs beyond the rest
+size_t route_workspace_ungrouped(int T, int H, int E, int k);
+// The router product of a large group-limited batch (csrc/route_tc.cu): part [S][T][Mpad].
+int route_tc_parts(int T, int H, int Mpad);
+int launch_route_tc(const uint16_t* x, int T, int H, const uint16_t* img, int Mpad, int S,
+                    float* part, int32_t* err, cudaStream_t st);
 size_t route_scratch(WsCursor& c, const RoutePlan& r, int T, int E, RouteScratch* out);
 int launch_route(const RouteArgs& a, const RoutePlan& r, const RouteScratch& s,
                  cudaStream_t st);

@@ -58,7 +58,7 @@ extern "C" int moe_route_topk_static(const uint16_t* x, const float* w_r, const 
                                      int32_t* counts, int32_t* offsets, int32_t* pos,
                                      int32_t* src, float* logits, float* shared_gate,
                                      int32_t* tie_flags, void* stream) {
-  const size_t need = moe_route_workspace_size(T, H, E, k);
+  const size_t need = moe::route_workspace_ungrouped(T, H, E, k);
   if (need == 0) return MOE_ERR_INVALID_ARG;
   if (need > moe::kStaticRouteScratchBytes) return MOE_ERR_CAPACITY;
   void* scratch = nullptr;

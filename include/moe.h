@@ -86,6 +86,8 @@ int moe_set_option(int option, int value);
  *   9    a bounded wait inside the fused decode kernel ran out of time;
  *   8    an expert's row range [offsets[e], offsets[e+1]) reached outside [0, max_rows)
  *        (moe_grouped_swiglu) and was clipped to it;
+ *   10   an expert with rows had no bundle (moe_grouped_swiglu_fp8, MOE_W_FP8_B128 layers): its
+ *        output rows were not written;
  *   20   a device-LRU cache request needed more distinct bundles than slots.
  * Blocking (test and debug use). */
 int moe_workspace_error(const void* ws, int32_t* code, void* stream);
@@ -296,8 +298,8 @@ int moe_route_topk_grouped(const uint16_t* x, const float* w_r, const float* log
  *
  * Arguments, outputs and results are those of moe_route_topk; the scratch is a fixed 8 MiB
  * array in the library's device memory (one per GPU that loads the library, held until the
- * process exits).  Returns MOE_ERR_CAPACITY when moe_route_workspace_size(T, H, E, k) exceeds
- * 8 MiB: batches of fewer than 256 tokens fit for E <= 256 and H <= 8192, while larger batches
+ * process exits).  Returns MOE_ERR_CAPACITY when what moe_route_topk uses of
+ * moe_route_workspace_size(T, H, E, k) exceeds 8 MiB: batches of fewer than 256 tokens fit for E <= 256 and H <= 8192, while larger batches
  * route on the tensor cores, whose split router image needs 6*H*E' bytes (E' = E + 1 rounded up
  * to 128) plus 4*H*E (for example 23 MiB at H = 7168, E = 256).  Calls no
  * allocating routine.  The first call on a device looks up the array's device address once
@@ -404,7 +406,8 @@ int moe_grouped_gemm_fp8(const uint8_t* xq, const float* x_scale, const uint8_t*
  *   h = silu(x Wg) * (x Wu) in fp32, quantised to FP8 rows as moe_quantize_fp8 does (directly
  *   from fp32), y_perm = bf16(h Wd), both products as in moe_grouped_gemm_fp8.
  *  xq, x_scale device FP8 rows [max_rows][H] in expert order; offsets device [E+1];
- *  bundles HOST array [E] of device pointers (NULL allowed for experts without rows);
+ *  bundles HOST array [E] of device pointers, 16-byte aligned (NULL allowed for experts without
+ *  rows; with rows they are skipped and error 10 is recorded);
  *  y_perm device [max_rows][H] bf16; max_rows, error word and clipping as above;
  *  ws device scratch of moe_grouped_swiglu_fp8_workspace_size(max_rows, E, H, I) bytes,
  *  256-byte aligned.

@@ -250,6 +250,29 @@ def test_shared_gate_and_logits(moe, T):
     assert np.all(np.abs(got["sg"] - 1 / (1 + np.exp(-z))) <= zb + 2.0 ** -20)
 
 
+@pytest.mark.parametrize("T,H,E,groups,gate", [
+    (511, 320, 64, 8, True), (512, 64, 16, 4, False), (515, 7168, 256, 8, True),
+    (1025, 2048, 60, 6, False), (700, 320, 250, 5, True), (20001, 128, 64, 8, False),
+    (640, 4096, 8, 2, True), (8200, 192, 256, 32, False)])
+def test_batches_on_the_tensor_cores(moe, T, H, E, groups, gate):
+    """One and two column tiles and the gate column's third, ragged token tiles, more tiles than
+    SMs, one to many parts of H; every logit."""
+    x, w_r, lb, sb = inputs(T, T, H, E, MODES[0])
+    wg = (torch.from_numpy(np.random.default_rng(1).standard_normal(H)) * 0.05).to(torch.bfloat16)
+    a = dict(w_gate=wg if gate else None)
+    got = run(moe, x, w_r, lb, sb, E, 4, groups, max(1, groups // 2), MODES[0], **a)
+    ref = reference(x, w_r, lb, sb, 4, groups, max(1, groups // 2), MODES[0], 1.0)
+    check(got, ref, 4, E)
+    l = x.double().numpy() @ w_r.astype(np.float64)
+    assert np.all(np.abs(got["logits"] - l) <= ref[5][:, None])
+    if gate:
+        z = x.double().numpy() @ wg.double().numpy()
+        zb = (2 * H + 64) * 2.0 ** -24 * (np.abs(x.double().numpy()) @ np.abs(wg.double().numpy()))
+        assert np.all(np.abs(got["sg"] - 1 / (1 + np.exp(-z))) <= zb + 2.0 ** -20)
+    again = run(moe, x, w_r, lb, sb, E, 4, groups, max(1, groups // 2), MODES[0], **a)
+    assert all(np.array_equal(got[n], again[n]) for n in got)
+
+
 def test_empty_batch(moe):
     i32 = dict(dtype=torch.int32, device="cuda")
     counts, offsets = torch.full((16,), -1, **i32), torch.full((17,), -1, **i32)
