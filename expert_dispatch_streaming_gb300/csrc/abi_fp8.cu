@@ -94,7 +94,10 @@ int moe_grouped_swiglu_fp8(const uint8_t* xq, const float* x_scale, const int32_
               aligned256(ws));
   cudaStream_t st = (cudaStream_t)stream;
   BundleTable tab{};
-  for (int e = 0; e < E; ++e) tab.p[e] = bundles[e];
+  for (int e = 0; e < E; ++e) {
+    MOE_REQUIRE(aligned16(bundles[e]));
+    tab.p[e] = bundles[e];
+  }
   Fp8Args gu = gemm_args_fp8(E, I, H, max_rows), dn = gemm_args_fp8(E, H, I, max_rows);
   gu.fused = true;
   const Fp8Plan pg = plan_fp8(gu), pd = plan_fp8(dn);

@@ -555,6 +555,11 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
       pdl_wait();
       atomicExch(p.err, 8);
     }
+    if (!PLAIN && r1 > r0 && !(p.dev_tab ? p.dev_tab[e] : p.tab.p[e])) {
+      r1 = r0;                                  // no weights: none of its rows is computed
+      pdl_wait();
+      atomicCAS(p.err, 0, 10);
+    }
     c.row0[a] = r0;
     c.rows[a] = r1 - r0;
     c.id[a] = e;

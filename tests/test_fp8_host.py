@@ -209,3 +209,18 @@ def test_fp8_recipe_and_rounding():
     assert np.array_equal(moe_ref.round_e4m3(mids), even)
     assert np.array_equal(moe_ref.round_e4m3(-vals), -vals)
     assert np.array_equal(moe_ref.round_e4m3(np.array([449.0, 1e9, -500.0])), [448, 448, -448])
+
+
+def test_misaligned_bundles_are_refused(moe):
+    """As above, addresses that are never followed."""
+    one = 1 << 20
+    d = _layer(moe, w_r=one)
+    d.bundles = moe.bundle_table([one] * 15 + [one + 8])
+    with pytest.raises(moe.MoEError):
+        moe.moe_layer_forward(d, one, 8, None, None, one, None, one, 1 << 40)
+    d = _layer(moe, w_r=one, Is=128, shared_bundle=one + 4)
+    d.bundles = moe.bundle_table([one] * 16)
+    with pytest.raises(moe.MoEError):
+        moe.moe_layer_forward(d, one, 8, None, None, one, None, one, 1 << 40)
+    with pytest.raises(moe.MoEError):
+        moe.moe_grouped_swiglu_fp8(one, one, one, [one, one + 8], 2, 256, 128, 8, one, one, 1 << 40)

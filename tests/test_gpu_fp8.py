@@ -445,6 +445,21 @@ def test_grouped_swiglu_fp8_full_shapes(moe, T, E, k, H, I):
     layer_close(y, ref)
 
 
+def test_an_expert_with_rows_but_no_bundle_is_skipped(moe):
+    H, I, counts = 256, 256, [3, 40, 0, 150]
+    g = gen(21)
+    q, xs = fp8_rows(g, sum(counts), H)
+    w13, s13 = fp8_weights(g, 4, 2 * I, H)
+    w2, s2 = fp8_weights(g, 4, H, I)
+    b = bundles_of(moe, H, I, w13, s13, w2, s2)
+    y, ws = run_swiglu(moe, q, xs, offsets_of(counts), [b[0], None, None, b[3]], 4, H, I,
+                       sum(counts))
+    assert moe.moe_workspace_error(ws) == 10
+    assert (y[3:43] == -77).all()
+    layer_close(y[:3], swiglu_ref(q[:3], xs[:3], w13[0], s13[0], w2[0], s2[0]))
+    layer_close(y[43:], swiglu_ref(q[43:], xs[43:], w13[3], s13[3], w2[3], s2[3]))
+
+
 def test_zero_and_nan_rows_through_the_experts(moe):
     """A row of zeros gives zeros; a NaN row gives NaN there and nowhere else."""
     H, I = 256, 256

@@ -174,6 +174,20 @@ def test_fp8_bundles_through_the_cache(moe, syn, mode, T):
         moe.moe_expert_cache_destroy(cache)
 
 
+def test_device_lru_with_too_few_slots(moe, syn):
+    """The error word says so, and the experts that got no slot are skipped."""
+    cfg = SMALL[2]
+    cache, store, table = make_cache(moe, syn, cfg, 2, device_lru=1)
+    try:
+        dl = syn.DeviceLayer(cfg, cached=True)
+        ws = dl.workspace(6)
+        dl.forward(syn.to_device_bits(wl.tokens(cfg, 6)), ws, cache=cache)
+        torch.cuda.synchronize()
+        assert moe.moe_workspace_error(ws) == 20
+    finally:
+        moe.moe_expert_cache_destroy(cache)
+
+
 def test_fp8_layer_graph_replay(moe, syn):
     """Captured once on a side stream, replayed on other tokens: equal to the eager calls."""
     cfg, T = SMALL[2], 5
