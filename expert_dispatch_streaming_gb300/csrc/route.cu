@@ -456,7 +456,7 @@ RoutePlan plan_route(int T, int H, int E, int k, bool has_gate, bool grouped) {
 size_t route_scratch(WsCursor& c, const RoutePlan& r, int T, int E, RouteScratch* out) {
   RouteScratch s{};
   s.part = c.take<float>((size_t)r.S * T * r.C);
-  s.hist = c.take<int32_t>((size_t)std::max(r.ntiles, 1) * E);
+  s.hist = c.take<int32_t>((size_t)std::max(r.ntiles, 1) * E + (r.own_tc ? T + 1 : 0));
   s.base = c.take<int32_t>((size_t)std::max(r.ntiles, 1) * E);
   s.active = c.take<int32_t>(kMaxExperts);
   s.n_active = c.take<int32_t>(32);
@@ -483,7 +483,7 @@ int launch_route(const RouteArgs& a, const RoutePlan& r, const RouteScratch& s,
     if (r.tc) {
       MOE_LAUNCH_PDL(router_prep_kernel, dim3(r.Mpad / kPrepM, a.H / kPrepK), dim3(256), 0, st,
                      a.w_r, a.w_gate, a.H, a.E, r.Mpad, a.T, s.img, s.w_rT, s.hist,
-                     r.ntiles * a.E, s.shared_meta, clear);
+                     r.ntiles * a.E + r.own_tc, s.shared_meta, clear);
       MOE_COUNT_LAUNCH();
       MOE_LAUNCH_CHECK();
       const int rr = r.own_tc ? launch_route_tc(a.x, a.T, a.H, s.img, r.Mpad, r.tc_S, s.tc_part,
@@ -544,7 +544,8 @@ int launch_route(const RouteArgs& a, const RoutePlan& r, const RouteScratch& s,
     p.scale = a.scale; p.ids = a.ids; p.w = a.w; p.logits = a.logits;
     p.shared_gate = a.shared_gate; p.tie_flags = a.tie_flags; p.hist = s.hist;
     if (a.n_group) {
-      const int rr = launch_gate_group(p, a.n_group, a.take, st);
+      const int rr = launch_gate_group(p, a.n_group, a.take,
+                                       r.own_tc ? s.hist + r.ntiles * a.E : nullptr, st);
       if (rr != MOE_OK) return rr;
     } else if (a.T <= kGateCtaMaxT && (a.E > kGateWarpMaxE || a.T < kGateWarpMinT)) {
       const int ctas = std::min(a.T, kGateCtasPerSm * sm_count());

@@ -58,7 +58,7 @@ constexpr size_t kFusedGatherMaxBytes = size_t(512) << 10;
 
 struct RouteScratch {
   float* part;      // [S][T][C]
-  int32_t* hist;    // [ntiles][E]
+  int32_t* hist;    // [ntiles][E] (own_tc: followed by the count and list of tokens to re-score)
   int32_t* base;    // [ntiles][E]
   int32_t* active;  // [E] experts with rows, ascending
   int32_t* n_active;
@@ -118,7 +118,9 @@ int launch_route(const RouteArgs& a, const RoutePlan& r, const RouteScratch& s,
                  cudaStream_t st);
 // Group-limited gating of p.T tokens (csrc/route_group.cu).
 constexpr int kMaxGroups = 32;
-int launch_gate_group(const GateParams& p, int n_group, int take, cudaStream_t st);
+// list: [1 + T], its first element zero; or NULL: tokens that need re-scoring are finished by the
+// CTA that met them.
+int launch_gate_group(const GateParams& p, int n_group, int take, int32_t* list, cudaStream_t st);
 int launch_route_group_tail(const GateParams& p, int n_group, int take, int32_t* counts,
                             int32_t* offsets, int32_t* pos, int32_t* src, int32_t* active,
                             int32_t* n_active, int32_t* shared_meta, uint16_t* x_perm,

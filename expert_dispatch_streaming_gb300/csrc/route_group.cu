@@ -553,6 +553,10 @@ __device__ __forceinline__ void gate_slow_all(const GateParams& p, const Groups&
   }
 }
 
+// Batches of at least this many tokens and more than kListMinE experts gate in two steps (see
+// gate_group_list_kernel).
+constexpr int kListMinT = 4096, kListMinE = 128;
+
 template <int NC>
 __global__ void __launch_bounds__(G_WARPS * 32)
 gate_group_kernel(const __grid_constant__ GateParams p, int n_group, int take) {
@@ -569,6 +573,41 @@ gate_group_kernel(const __grid_constant__ GateParams p, int n_group, int take) {
     atomicOr(&slow, 1u << warp);
   __syncthreads();
   gate_slow_all<NC>(p, G, t0, slow, sm, sv);
+}
+
+// Large batches in two steps: the tokens that need re-scoring, one or two in a hundred, each take
+// several times as long as the others, and their CTAs would be the last; so the first kernel lists
+// them and a second gives each a CTA of its own (the whole routing of 256 experts: 8192 tokens 152
+// us with one kernel, 137 with two, 4096 107 / 104, 2048 81 / 82; of 60 experts, where fewer scores
+// are close, 8192 tokens 60 / 63: one token alone takes 12 us).  The list's order varies from run to run; nothing else depends on it.
+template <int NC>
+__global__ void __launch_bounds__(G_WARPS * 32)
+gate_group_list_kernel(const __grid_constant__ GateParams p, int n_group, int take,
+                       int32_t* __restrict__ list) {
+  pdl_trigger();
+  pdl_wait();
+  __shared__ GroupSmem sm[G_WARPS];
+  const int warp = threadIdx.x >> 5, t = blockIdx.x * G_WARPS + warp;
+  const Groups G(n_group, take, p.E, p.mode == MOE_GATING_SIGMOID_BIAS_RENORM);
+  if (t < p.T && !gate_quick<NC>(p, G, t, nullptr, sm[warp]) && (threadIdx.x & 31) == 0)
+    list[1 + atomicAdd(list, 1)] = t;
+}
+template <int NC>
+__global__ void __launch_bounds__(G_WARPS * 32)
+gate_group_rest_kernel(const __grid_constant__ GateParams p, int n_group, int take,
+                       const int32_t* __restrict__ list) {
+  pdl_trigger();
+  pdl_wait();
+  __shared__ GroupSmem sm;
+  __shared__ Service sv;
+  const Groups G(n_group, take, p.E, p.mode == MOE_GATING_SIGMOID_BIAS_RENORM);
+  const int n = __ldcg(list);
+#pragma unroll 1
+  for (int i = blockIdx.x; i < n; i += gridDim.x) {
+    const int t = __ldcg(list + 1 + i);
+    if (threadIdx.x < 32) score_token<NC>(p, t, nullptr, sm);
+    gate_slow_all<NC>(p, G, t, 1u, &sm, sv);
+  }
 }
 
 // Everything after the router product for a batch of at most kSmallT tokens in one CTA, as
@@ -719,20 +758,29 @@ int launch_route_group_tail(const GateParams& p, int n_group, int take, int32_t*
   return MOE_OK;
 }
 
-int launch_gate_group(const GateParams& p, int n_group, int take, cudaStream_t st) {
-  const GateParams& q = p;
-  const dim3 grid(ceil_div(q.T, G_WARPS)), block(G_WARPS * 32);
-  if (q.E <= 32)
-    MOE_LAUNCH_NEXT(true, gate_group_kernel<1>, grid, block, 0, st, q, n_group, take);
-  else if (q.E <= 64)
-    MOE_LAUNCH_NEXT(true, gate_group_kernel<2>, grid, block, 0, st, q, n_group, take);
-  else if (q.E <= 128)
-    MOE_LAUNCH_NEXT(true, gate_group_kernel<4>, grid, block, 0, st, q, n_group, take);
-  else
-    MOE_LAUNCH_NEXT(true, gate_group_kernel<EC>, grid, block, 0, st, q, n_group, take);
+template <int NC>
+static int launch_gate_group_nc(const GateParams& p, int n_group, int take, int32_t* list,
+                                cudaStream_t st) {
+  const dim3 grid(ceil_div(p.T, G_WARPS)), block(G_WARPS * 32);
+  if (!list || p.T < kListMinT || p.E <= kListMinE) {
+    MOE_LAUNCH_NEXT(true, gate_group_kernel<NC>, grid, block, 0, st, p, n_group, take);
+  } else {
+    MOE_LAUNCH_NEXT(true, gate_group_list_kernel<NC>, grid, block, 0, st, p, n_group, take, list);
+    MOE_COUNT_LAUNCH();
+    MOE_LAUNCH_CHECK();
+    MOE_LAUNCH_NEXT(true, gate_group_rest_kernel<NC>, dim3(2 * sm_count()), block, 0, st, p,
+                    n_group, take, list);
+  }
   MOE_COUNT_LAUNCH();
   MOE_LAUNCH_CHECK();
   return MOE_OK;
+}
+
+int launch_gate_group(const GateParams& p, int n_group, int take, int32_t* list, cudaStream_t st) {
+  if (p.E <= 32) return launch_gate_group_nc<1>(p, n_group, take, list, st);
+  if (p.E <= 64) return launch_gate_group_nc<2>(p, n_group, take, list, st);
+  if (p.E <= 128) return launch_gate_group_nc<4>(p, n_group, take, list, st);
+  return launch_gate_group_nc<EC>(p, n_group, take, list, st);
 }
 
 }  // namespace moe
