@@ -7,8 +7,10 @@ namespace {
 
 // A lane holds 16 consecutive columns (two 16-byte loads, one 16-byte store), eight lanes a block,
 // a warp 512 columns at a time; a warp takes one row's kCols columns, both halves' loads in
-// flight together.  Bound by memory: 2 bytes in (gathered rows mostly from L2: the codes are
-// stored with a streaming hint so that they do not push x out of it) and 1 byte out per value.
+// flight together.  It needs 2 bytes in (gathered rows mostly from L2: the codes are stored with a
+// streaming hint so that they do not push x out of it) and 1 byte out per value; 8192 x 7168 rows
+// gathered eightfold take 136 us, 66% of the copy bandwidth, with the issue slots 75% busy:
+// converting each value (unpack, multiply, convert, pack, its part of the maximum) bounds it.
 // The largest magnitude of bf16 values is taken in bf16, which is exact and skips NaNs.
 constexpr int kCols = 1024;
 

@@ -5,7 +5,7 @@
 //
 // each block's 192 products a column summed by the tensor cores from zero and added in fp32
 // registers.  (One sum over all 3 H products inside the tensor cores is cut off, not rounded, at
-// every addition: an error of 2.6e-6 of the weights at H = 7168, against 3e-7 this way.)
+// every addition: the weights are off by 2.6e-6 at H = 7168 that way, by 7e-8 this way.)
 //
 // Tile: 128 tokens (M, a TMEM lane each) x up to 256 router columns (N), split over H so that the
 // tiles fill the GPU; a CTA runs one part of one tile, 384 threads:
@@ -16,7 +16,9 @@
 //               at the end the sums leave through shared memory by rows.
 //
 // Bound by shared memory and its filling: a block reads 12 x 12 KB of operands and takes in 112 KB
-// for 1536 clocks of tensor work.  Every wait is bounded (2 s; then an error word and the end).
+// for 1536 clocks of tensor work.  8192 tokens x 7168 x 256 columns (two parts, 128 CTAs): 66 us,
+// 1.4 PFLOP/s of the three pieces' products (ungrouped routing's kernel, weights as M: 94 us).
+// Every wait is bounded (2 s; then an error word and the end).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 

@@ -189,6 +189,19 @@ def test_close_groups_and_experts_are_resolved_exactly(moe, T):
         assert (got["tie"] >= 1).all()
 
 
+def test_large_batch_with_every_token_rescored(moe):
+    H, E, groups, T = 128, 256, 8, 4100
+    rng = np.random.default_rng(4)
+    x = torch.from_numpy(rng.standard_normal((T, H)).astype(np.float32)).to(torch.bfloat16)
+    base = np.tile((rng.standard_normal((H, 32)) * 0.05).astype(np.float32), (1, groups))
+    w_r = (base + rng.standard_normal((H, E)).astype(np.float32) * 1e-6).astype(np.float32)
+    got = run(moe, x, w_r, None, None, E, 5, groups, 3, MODES[0])
+    check(got, reference(x, w_r, None, None, 5, groups, 3, MODES[0], 1.0), 5, E)
+    assert (got["tie"] >= 1).all()
+    again = run(moe, x, w_r, None, None, E, 5, groups, 3, MODES[0])
+    assert all(np.array_equal(got[n], again[n]) for n in got)
+
+
 @pytest.mark.parametrize("T", [2, 30, 300])
 @pytest.mark.parametrize("mode", MODES)
 def test_masked_experts_and_groups(moe, mode, T):
