@@ -449,6 +449,7 @@ int moe_route_topk_grouped(const uint16_t* x, const float* w_r, const float* log
                            int32_t* pos, int32_t* src, float* logits, float* shared_gate,
                            int32_t* tie_flags, void* ws, size_t ws_bytes, void* stream) {
   MOE_REQUIRE(valid_route_shape(T, H, E, k) && valid_groups(E, k, n_group, topk_group));
+  MOE_REQUIRE(aligned16(x) && aligned256(ws));
   return route_topk(x, w_r, logit_bias, sel_bias, w_gate, nullptr, T, H, E, k, n_group,
                     topk_group, gating, scale, ids, w, counts, offsets, pos, src, logits,
                     shared_gate, tie_flags, ws, ws_bytes, stream);

@@ -282,7 +282,7 @@ int moe_route_topk(const uint16_t* x, const float* w_r, const float* logit_bias,
  * Arguments, outputs and workspace (moe_route_workspace_size(T, H, E, k)) as in moe_route_topk,
  * without forced ids.
  * Limits: those of moe_route_topk, 1 <= n_group <= 32 dividing E, 1 <= topk_group <= n_group,
- * k <= topk_group * E / n_group; MOE_ERR_INVALID_ARG otherwise.  The pages describe no groups. */
+ * k <= topk_group * E / n_group, x 16-byte and ws 256-byte aligned; MOE_ERR_INVALID_ARG otherwise.  The pages describe no groups. */
 int moe_route_topk_grouped(const uint16_t* x, const float* w_r, const float* logit_bias,
                            const float* sel_bias, const uint16_t* w_gate, int T, int H, int E,
                            int k, int n_group, int topk_group, int gating, float scale,
@@ -299,7 +299,8 @@ int moe_route_topk_grouped(const uint16_t* x, const float* w_r, const float* log
  * Arguments, outputs and results are those of moe_route_topk; the scratch is a fixed 8 MiB
  * array in the library's device memory (one per GPU that loads the library, held until the
  * process exits).  Returns MOE_ERR_CAPACITY when what moe_route_topk uses of
- * moe_route_workspace_size(T, H, E, k) exceeds 8 MiB: batches of fewer than 256 tokens fit for E <= 256 and H <= 8192, while larger batches
+ * moe_route_workspace_size(T, H, E, k) exceeds 8 MiB: batches of fewer than 256 tokens fit for
+ * E <= 256 and H <= 8192, while larger batches
  * route on the tensor cores, whose split router image needs 6*H*E' bytes (E' = E + 1 rounded up
  * to 128) plus 4*H*E (for example 23 MiB at H = 7168, E = 256).  Calls no
  * allocating routine.  The first call on a device looks up the array's device address once

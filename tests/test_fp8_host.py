@@ -224,3 +224,8 @@ def test_misaligned_bundles_are_refused(moe):
         moe.moe_layer_forward(d, one, 8, None, None, one, None, one, 1 << 40)
     with pytest.raises(moe.MoEError):
         moe.moe_grouped_swiglu_fp8(one, one, one, [one, one + 8], 2, 256, 128, 8, one, one, 1 << 40)
+
+
+@pytest.mark.parametrize("bad", [dict(x=A + 8), dict(ws=A + 16)])
+def test_route_grouped_refuses_misaligned_rows_and_workspaces(moe, bad):
+    test_route_grouped_refusals(moe, bad)
