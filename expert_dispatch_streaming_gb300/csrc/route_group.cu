@@ -543,11 +543,14 @@ __device__ __forceinline__ void gate_slow_all(const GateParams& p, const Groups&
       if ((threadIdx.x & 31) == 0) sv.n = 0;
       __syncthreads();
     } else {
+      // (sv.n is read between a batch's two barriers only: once the second has passed, the asking
+      // warp may write the next request)
       for (int i0 = 0;;) {
         __syncthreads();
-        if (sv.n == 0) break;
+        const int n = sv.n;
+        if (n == 0) break;
         dots(p, sv, i0);
-        i0 = i0 + kBatch < sv.n ? i0 + kBatch : 0;
+        i0 = i0 + kBatch < n ? i0 + kBatch : 0;
       }
     }
     __syncthreads();
