@@ -99,7 +99,8 @@ __device__ __forceinline__ void score_token(const GateParams& p, int t, const fl
 
 // Scores of the groups and the `take` best: of this lane's group (lane / P) its score, the score an
 // expert needs to be among its deciding ones, and its rank; kth / nxt: the take-th score and the
-// next (nxt = -infinity when every group is taken).
+// next (nxt = -infinity when every group is taken).  A sum of two scores is held as half of it:
+// halves are exact, and two of the lowest finite value (a mask) do not add up to -infinity.
 struct GroupRank {
   float score, least, kth, nxt;
   int rank;
@@ -130,7 +131,7 @@ __device__ __forceinline__ GroupRank rank_groups(const Groups& G, const GroupSme
     m1 = fmaxf(m1, a1);
   }
   GroupRank r;
-  r.score = G.pairs ? m1 + m2 : m1;
+  r.score = G.pairs ? 0.5f * m1 + 0.5f * m2 : m1;
   if (r.score != r.score) r.score = -CUDART_INF_F;
   r.least = (G.pairs ? m2 : m1) - kTau;
   r.rank = 0;
@@ -302,7 +303,7 @@ __device__ __forceinline__ bool gate_quick(const GateParams& p, const Groups& G,
                                            const float* raw, GroupSmem& sm) {
   score_token<NC>(p, t, raw, sm);
   const GroupRank r = rank_groups(G, sm);
-  if (r.kth - r.nxt <= (G.pairs ? 2.f * kTau : kTau)) return false;
+  if (r.kth - r.nxt <= kTau) return false;
   const unsigned lead = __ballot_sync(0xffffffffu, r.rank < G.take);
   const Top top = top_quick<NC>(G, sm, lead, p.E, p.k);
   if (top.kth - top.nxt <= kTau) return false;
@@ -432,12 +433,11 @@ __device__ __noinline__ void gate_slow(const GateParams& p, const Groups& G, int
   int flag = 0;
   const GroupRank r = rank_groups(G, sm);
   bool kept = r.rank < G.take;
-  const float tau = G.pairs ? 2.f * kTau : kTau;
-  if (r.kth - r.nxt <= tau) {
+  if (r.kth - r.nxt <= kTau) {
     flag = 1;
     // groups clear of the boundary stay; the band is decided by its exact scores
-    const bool in = g < G.n, def = kept && r.score - r.nxt > tau;
-    const bool band = in && !def && r.score >= r.kth - tau;
+    const bool in = g < G.n, def = kept && r.score - r.nxt > kTau;
+    const bool band = in && !def && r.score >= r.kth - kTau;
     const unsigned bm = __ballot_sync(0xffffffffu, band);
     rescore(p, t, sm, sv, [&](int e) {
       const int ll = G.lane_of(G.of(e));

@@ -1,0 +1,38 @@
+"""GPU tests of group-limited routing at the edges of fp32: biases near the largest finite values,
+against the 64-bit form of test_gpu_route_group."""
+import numpy as np
+import pytest
+import torch  # noqa: F401
+
+from test_gpu_route_group import MODES, check, inputs, reference, run
+
+pytestmark = pytest.mark.gpu
+
+LOW = np.finfo(np.float32).min
+INF = np.float32(np.inf)
+
+
+@pytest.fixture(scope="module")
+def moe():
+    import expert_dispatch_streaming_gb300 as m
+    return m
+
+
+@pytest.mark.parametrize("T", [2, 30, 300, 600])
+@pytest.mark.parametrize("first,second,third", [
+    (-INF, LOW, 0.75 * LOW), (-INF, LOW, LOW), (LOW, -INF, 0.6 * LOW), (-LOW, -INF, INF),
+    (-0.75 * LOW, -LOW, -LOW)])
+@pytest.mark.parametrize("mode", MODES)
+def test_masks_of_the_largest_finite_values(moe, mode, T, first, second, third):
+    """One group of ordinary experts, two places and eight experts: the second group is one whose
+    experts are all masked, by -infinity, by the lowest value or by a part of it (two of which add
+    up past fp32's range); or, with the signs turned, favoured."""
+    H, E, groups, take, k = 128, 32, 8, 2, 8
+    rng = np.random.default_rng(8)
+    b = (0.1 * rng.standard_normal(E)).astype(np.float32)
+    for g, v in ((0, first), (1, second), (2, third), (3, -INF), (4, -INF), (6, -INF), (7, -INF)):
+        b[4 * g:4 * g + 4] = v
+    lb, sb = (None, b) if mode == MODES[0] else (b, None)
+    x, w_r, _, _ = inputs(T, T, H, E, mode)
+    got = run(moe, x, w_r, lb, sb, E, k, groups, take, mode)
+    check(got, reference(x, w_r, lb, sb, k, groups, take, mode, 1.0), k, E)
