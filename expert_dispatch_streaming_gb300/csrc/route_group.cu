@@ -275,12 +275,21 @@ __device__ __forceinline__ void finish_token(const GateParams& p, int t, GroupSm
       denom = warp_sum(denom);
     }
   }
-  if (!all) {
-    float o[kMaxK];
+  auto sum = [&] {   // of the chosen's v, in order
+    float o[kMaxK], s = 0.f;
 #pragma unroll
     for (int j = 0; j < kMaxK; ++j) o[j] = __shfl_sync(0xffffffffu, v, j);
 #pragma unroll
-    for (int j = 0; j < kMaxK; ++j) denom += j < k ? o[j] : 0.f;
+    for (int j = 0; j < kMaxK; ++j) s += j < k ? o[j] : 0.f;
+    return s;
+  };
+  if (!all) denom = sum();
+  if (sig && denom < 0x1p-64f) {
+    // sigmoids that fp32 is about to lose (logits below -44): e^l is their ratio to 2^-64, as far
+    // as 64 bits hold them; beyond, they are zero
+    const float top = warp_max(lj);
+    v = top > -709.f ? expf(lj - top) : 0.f;
+    denom = sum();
   }
   // a token whose chosen scores are all zero (every expert left to it is masked) would get
   // 0 / 0: its weights are zero instead

@@ -275,7 +275,9 @@ int moe_route_topk(const uint16_t* x, const float* w_r, const float* logit_bias,
  * largest c inside them, ties to the lower expert.  Weights, scale, dispatch outputs and their
  * order are those of moe_route_topk (SOFTMAX normalises over all E experts, taken or not).
  * A NaN score counts as -infinity.  A token whose chosen experts all have zero weight (every
- * expert open to it masked by a logit_bias of -infinity) gets weights 0, and still k ids.
+ * expert open to it masked by a logit_bias of -infinity; SIGMOID_BIAS_RENORM: every sigmoid zero
+ * in 64 bits, logits below -709) gets weights 0, and still k ids.  Sigmoids below fp32's range keep
+ * their ratios.
  * Exact selection as in moe_route_topk, for groups and for experts: scores within the fp32
  * error margin of a boundary are re-scored; tie_flags: 1 = re-scored at either boundary, 2 =
  * the re-scored gap of either was below 1e-6.

@@ -1,5 +1,5 @@
-"""GPU tests of group-limited routing at the edges of fp32: biases near the largest finite values,
-against the 64-bit form of test_gpu_route_group."""
+"""GPU tests of group-limited routing at the edges of fp32: biases near the largest finite values
+and sigmoids below the smallest, against the 64-bit form of test_gpu_route_group."""
 import numpy as np
 import pytest
 import torch  # noqa: F401
@@ -36,3 +36,21 @@ def test_masks_of_the_largest_finite_values(moe, mode, T, first, second, third):
     x, w_r, _, _ = inputs(T, T, H, E, mode)
     got = run(moe, x, w_r, lb, sb, E, k, groups, take, mode)
     check(got, reference(x, w_r, lb, sb, k, groups, take, mode, 1.0), k, E)
+
+
+@pytest.mark.parametrize("T", [1, 30, 300, 600])
+@pytest.mark.parametrize("k", [1, 4])
+@pytest.mark.parametrize("level", [-70, -87, -88, -88.3, -89, -104, -300, -680])
+def test_weights_of_far_negative_logits(moe, level, k, T):
+    """Sigmoids below fp32's range: their ratios are not."""
+    H, E = 64, 32
+    x, w_r, _, sb = inputs(T, T, H, E, MODES[0])
+    lb = (level + 0.3 * np.random.default_rng(1).standard_normal(E)).astype(np.float32)
+    got = run(moe, x, w_r, lb, sb, E, k, 8, 3, MODES[0], 2.5)
+    ids, w, ggap, egap, c, bound = reference(x, w_r, lb, sb, k, 8, 3, MODES[0], 2.5)
+    clear = np.fmin(ggap, egap) > 1e-6
+    assert clear.mean() > 0.9 and np.array_equal(got["ids"][clear], ids[clear])
+    # a logit is off by its product's error and half a step of its own size (adding the bias), a
+    # weight by twice that relatively, and the functions' own 2^-20
+    tol = w * (2.5 * bound[:, None] + 2 * 2.0 ** -24 * (abs(level) + 8) + 2.0 ** -20)
+    assert np.all(np.abs(got["w"] - w)[clear] <= tol[clear])
