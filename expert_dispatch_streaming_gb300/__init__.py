@@ -373,6 +373,12 @@ def moe_grouped_swiglu_fp8_workspace_size(max_rows, E, H, I) -> int:
 
 def moe_grouped_swiglu_fp8(xq, x_scale, offsets, bundles, E, H, I, max_rows, y_perm, ws, ws_bytes,
                            stream=None) -> None:
+    """bundles: a bundle_table of at least E entries, or a sequence (filled up to E with NULL)."""
+    if isinstance(bundles, C.Array):
+        if len(bundles) < E:
+            raise MoEError(MOE_ERR_INVALID_ARG, "moe_grouped_swiglu_fp8")
+    else:
+        bundles = list(bundles) + [None] * (min(E, 256) - len(bundles))
     _check(_lib.moe_grouped_swiglu_fp8(ptr(xq), ptr(x_scale), ptr(offsets), bundle_table(bundles),
                                        E, H, I, max_rows, ptr(y_perm), ptr(ws), ws_bytes,
                                        stream_handle(stream)), "moe_grouped_swiglu_fp8")
