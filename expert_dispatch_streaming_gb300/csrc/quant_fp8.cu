@@ -146,10 +146,18 @@ int moe_pack_bundle_fp8_device(int H, int I, const uint8_t* w_gate_up, const flo
                                                                      b + lay.down_offset);
   MOE_COUNT_LAUNCH();
   MOE_LAUNCH_CHECK();
-  MOE_CUDA_TRY(cudaMemcpyAsync(b + lay.gate_up_scale_offset, s_gate_up, gu / 16384 * sizeof(float),
+  // the scales, and zeros in what rounding their sections up to 256 bytes leaves (as on the host: a
+  // bundle's checksum covers it)
+  const size_t sg = gu / 16384 * sizeof(float), sd = dn / 16384 * sizeof(float);
+  const size_t end_g = lay.gate_up_scale_offset + sg, end_d = lay.down_scale_offset + sd;
+  MOE_CUDA_TRY(cudaMemcpyAsync(b + lay.gate_up_scale_offset, s_gate_up, sg,
                                cudaMemcpyDeviceToDevice, st));
-  MOE_CUDA_TRY(cudaMemcpyAsync(b + lay.down_scale_offset, s_down, dn / 16384 * sizeof(float),
-                               cudaMemcpyDeviceToDevice, st));
+  MOE_CUDA_TRY(cudaMemcpyAsync(b + lay.down_scale_offset, s_down, sd, cudaMemcpyDeviceToDevice,
+                               st));
+  if (end_g < lay.down_scale_offset)
+    MOE_CUDA_TRY(cudaMemsetAsync(b + end_g, 0, lay.down_scale_offset - end_g, st));
+  if (end_d < lay.total_bytes)
+    MOE_CUDA_TRY(cudaMemsetAsync(b + end_d, 0, lay.total_bytes - end_d, st));
   return MOE_OK;
 }
 

@@ -208,8 +208,8 @@ int moe_pack_bundle_nvfp4(int H, int I, const uint8_t* wg, const uint8_t* wu, co
 int moe_pack_bundle_fp8(int H, int I, const uint8_t* w_gate_up, const float* s_gate_up,
                         const uint8_t* w_down, const float* s_down, void* dst);
 /* The same from device tensors into a device bundle, by kernels on `stream` (asynchronous; for
- * experts that stay resident).  Pointers 16-byte aligned.  NaN codes and non-finite scales are
- * copied as they are. */
+ * experts that stay resident): byte for byte the host packer's bundle.  Codes and dst 16-byte
+ * aligned.  NaN codes and non-finite scales are copied as they are. */
 int moe_pack_bundle_fp8_device(int H, int I, const uint8_t* w_gate_up, const float* s_gate_up,
                                const uint8_t* w_down, const float* s_down, void* dst,
                                void* stream);
