@@ -43,15 +43,12 @@
 // tile tables and first load take 3-5 us before the first product, joining pieces 2-5 after the last.
 //
 // Every wait is bounded (2 s; then an error word and the kernel ends).
-#include <cuda.h>
-#include <cudaTypedefs.h>
-
 #include "fp8.cuh"
+#include "tc_ptx.cuh"
 
 namespace moe {
 namespace {
 
-constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr int kStages = 3;
 constexpr int kABytes = kFp8TileBytes, kBBytes = 2 * kFp8TileBytes;
 constexpr int kStageBytes = kABytes + kBBytes;
@@ -98,104 +95,6 @@ struct Fp8Params {
 };
 static_assert(sizeof(Fp8Params) <= 4096, "kernel parameters stay within 4 KB");
 
-__device__ __forceinline__ uint32_t smem_u32(const void* p) {
-  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
-__device__ __forceinline__ uint64_t globaltimer() {
-  uint64_t t;
-  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-  return t;
-}
-__device__ __forceinline__ void mbar_init(uint64_t* bar, uint32_t count) {
-  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(count));
-}
-// One arrival of the warp: lane 0, by predicate (a branch would cost a reconvergence).
-__device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
-  asm volatile(
-      "{\n.reg .pred q;\nsetp.eq.s32 q, %1, 0;\n"
-      "@q mbarrier.arrive.shared::cta.b64 _, [%0];\n}\n" ::"r"(smem_u32(bar)),
-      "r"(lane)
-      : "memory");
-}
-__device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)),
-               "r"(bytes)
-               : "memory");
-}
-// One try of lane 0 only, by predicate: 32 lanes polling one barrier are 32 operations on it.
-__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity, int lane) {
-  uint32_t ok;
-  asm volatile(
-      "{\n.reg .pred p, q;\nsetp.eq.s32 q, %3, 0;\nsetp.ne.s32 p, 0, 0;\n"
-      "@q mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity), "r"(lane)
-      : "memory");
-  return ok != 0;
-}
-// The same without suspending the thread, for a look ahead of the wait.
-__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity, int lane) {
-  uint32_t ok;
-  asm volatile(
-      "{\n.reg .pred p, q;\nsetp.eq.s32 q, %3, 0;\nsetp.ne.s32 p, 0, 0;\n"
-      "@q mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity), "r"(lane)
-      : "memory");
-  return ok != 0;
-}
-// Bounded wait of a converged warp (votes decide: the warp never diverges); `early`: the result of
-// a look at this phase already taken, whose latency other work has covered.
-__device__ __forceinline__ bool warp_wait(uint64_t* b, uint32_t parity, int32_t* err, int code,
-                                          bool early = false) {
-  const uint32_t bar = smem_u32(b);
-  const int lane = threadIdx.x & 31;
-  if (__any_sync(0xffffffffu, early)) return true;
-  if (__any_sync(0xffffffffu, mbar_try(bar, parity, lane))) return true;
-  const uint64_t t0 = globaltimer();
-  for (uint32_t i = 1;; ++i) {
-    if (__any_sync(0xffffffffu, mbar_try(bar, parity, lane))) return true;
-    if ((i & 255) == 0 && __any_sync(0xffffffffu, globaltimer() - t0 > kWaitNs)) {
-      pdl_wait();                               // (the word may still be being cleared)
-      if (lane == 0) atomicExch(err, code);
-      return false;
-    }
-  }
-}
-__device__ __forceinline__ void bulk_g2s(uint32_t dst, const void* src, uint32_t bytes,
-                                         uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-      ::"r"(dst), "l"(src), "r"(bytes), "r"(smem_u32(bar))
-      : "memory");
-}
-__device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map, int c0, int c1,
-                                       uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, "
-      "{%2, %3}], [%4];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(smem_u32(bar))
-      : "memory");
-}
-__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
-  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
-}
-__device__ __forceinline__ bool elect_one() {
-  uint32_t pred = 0;
-  asm volatile(
-      "{\n.reg .pred p;\n.reg .b32 r;\nelect.sync r|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(pred));
-  return pred != 0;
-}
-// Shared-memory matrix descriptor: K-major, 128-byte swizzle, 8-row groups 1024 B apart.
-__device__ __forceinline__ uint64_t sdesc_sw128(uint32_t saddr) {
-  uint64_t d = (uint64_t)((saddr & 0x3FFFFu) >> 4);
-  d |= (uint64_t)1 << 16;
-  d |= (uint64_t)(1024 >> 4) << 32;
-  d |= (uint64_t)1 << 46;
-  d |= (uint64_t)2 << 61;
-  return d;
-}
 // Instruction descriptor of kind::f8f6f4: E4M3 A and B (type 0), fp32 D, both K-major, M x N.
 __device__ __forceinline__ uint32_t idesc_e4m3(int M, int N) {
   return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
@@ -206,18 +105,6 @@ __device__ __forceinline__ void mma_fp8(uint32_t d_tmem, uint64_t a, uint64_t b,
       "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
       "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
       "l"(a), "l"(b), "r"(idesc), "r"(accumulate));
-}
-__device__ __forceinline__ void mma_commit(uint64_t* bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-          smem_u32(bar))
-      : "memory");
-}
-__device__ __forceinline__ void tc_fence_before() {
-  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void tc_fence_after() {
-  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
 // 64 columns of the warp's 32 lanes, without the wait.
 __device__ __forceinline__ void tmem_ld64_nw(uint32_t taddr, uint32_t (&r)[64]) {
@@ -238,9 +125,6 @@ __device__ __forceinline__ void tmem_ld64_nw(uint32_t taddr, uint32_t (&r)[64]) 
         "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]),
         "=r"(r[63])
       : "r"(taddr));
-}
-__device__ __forceinline__ void tmem_wait_ld() {
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 // acc[i] += v[i] * f, two at a time (fma.rn.f32x2: one issue slot).  Volatile, as the load and its
 // wait are, so that no use of v moves above the wait.  The pairs are put together inside the
@@ -960,19 +844,6 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
 __global__ void __launch_bounds__(256) clear_kernel(uint4* words, int n) {
   pdl_trigger();
   for (int i = threadIdx.x; i < n; i += 256) words[i] = make_uint4(0, 0, 0, 0);
-}
-
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  if (!fn) {
-    void* ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-  }
-  return fn;
 }
 
 // Map of byte rows [rows][K] with boxes of box_rows x 128 bytes, 128-byte swizzle; reads past K

@@ -19,15 +19,12 @@
 // for 1536 clocks of tensor work.  8192 tokens x 7168 x 256 columns (two parts, 128 CTAs): 66 us,
 // 1.4 PFLOP/s of the three pieces' products (ungrouped routing's kernel, weights as M: 94 us).
 // Every wait is bounded (2 s; then an error word and the end).
-#include <cuda.h>
-#include <cudaTypedefs.h>
-
 #include "route.cuh"
+#include "tc_ptx.cuh"
 
 namespace moe {
 namespace {
 
-constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr int kA = 3, kB = 5;                   // ring slots
 constexpr int kABytes = 16384, kBBytes = 32768;
 constexpr int kThreads = 384;
@@ -52,86 +49,12 @@ constexpr int kSmem = kRing + 1024 + (int)sizeof(Ctl);
 static_assert(kSmem <= 232448, "over the 227 KB shared-memory limit of a CTA");
 static_assert(8 * 32 * 128 * 4 <= kRing, "the sums leave through the rings");
 
-__device__ __forceinline__ uint32_t smem_u32(const void* p) {
-  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
-__device__ __forceinline__ void mbar_init(uint64_t* bar, uint32_t count) {
-  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(count));
-}
-__device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
-  asm volatile(
-      "{\n.reg .pred q;\nsetp.eq.s32 q, %1, 0;\n"
-      "@q mbarrier.arrive.shared::cta.b64 _, [%0];\n}\n" ::"r"(smem_u32(bar)),
-      "r"(lane)
-      : "memory");
-}
-__device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)),
-               "r"(bytes)
-               : "memory");
-}
-__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity, int lane) {
-  uint32_t ok;
-  asm volatile(
-      "{\n.reg .pred p, q;\nsetp.eq.s32 q, %3, 0;\nsetp.ne.s32 p, 0, 0;\n"
-      "@q mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity), "r"(lane)
-      : "memory");
-  return ok != 0;
-}
-// Bounded wait of a converged warp (lane 0 polls, votes decide).
-__device__ __forceinline__ bool warp_wait(uint64_t* b, uint32_t parity, int32_t* err, int code) {
-  const uint32_t bar = smem_u32(b);
-  const int lane = threadIdx.x & 31;
-  if (__any_sync(0xffffffffu, mbar_try(bar, parity, lane))) return true;
-  uint64_t t0, t;
-  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
-  for (uint32_t i = 1;; ++i) {
-    if (__any_sync(0xffffffffu, mbar_try(bar, parity, lane))) return true;
-    if ((i & 255) == 0) {
-      asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-      if (__any_sync(0xffffffffu, t - t0 > kWaitNs)) {
-        if (lane == 0) atomicExch(err, code);
-        return false;
-      }
-    }
-  }
-}
-__device__ __forceinline__ bool elect_one() {
-  uint32_t pred = 0;
-  asm volatile(
-      "{\n.reg .pred p;\n.reg .b32 r;\nelect.sync r|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(pred));
-  return pred != 0;
-}
-// Shared-memory matrix descriptor: K-major, 128-byte swizzle, 8-row groups 1024 B apart.
-__device__ __forceinline__ uint64_t sdesc_sw128(uint32_t saddr) {
-  uint64_t d = (uint64_t)((saddr & 0x3FFFFu) >> 4);
-  d |= (uint64_t)1 << 16;
-  d |= (uint64_t)(1024 >> 4) << 32;
-  d |= (uint64_t)1 << 46;
-  d |= (uint64_t)2 << 61;
-  return d;
-}
 __device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc,
                                          uint32_t accumulate) {
   asm volatile(
       "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
       "l"(a), "l"(b), "r"(idesc), "r"(accumulate));
-}
-__device__ __forceinline__ void mma_commit(uint64_t* bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-          smem_u32(bar))
-      : "memory");
-}
-__device__ __forceinline__ void tc_fence_before() {
-  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void tc_fence_after() {
-  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
 // 32 columns of the warp's 32 lanes, without the wait.
 __device__ __forceinline__ void tmem_ld32_nw(uint32_t taddr, uint32_t (&r)[32]) {
@@ -146,9 +69,6 @@ __device__ __forceinline__ void tmem_ld32_nw(uint32_t taddr, uint32_t (&r)[32]) 
         "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
         "=r"(r[31])
       : "r"(taddr));
-}
-__device__ __forceinline__ void tmem_wait_ld() {
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 // acc[i] += v[i]; volatile, as the load and its wait are, so that no use of v moves above the wait.
 __device__ __forceinline__ void add32(float* acc, const uint32_t (&v)[32]) {
@@ -189,8 +109,7 @@ router_tc_kernel(const __grid_constant__ TcParams p) {
     mbar_init(&c.drain, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (threadIdx.x == 32)
-    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.tm_x)) : "memory");
+  if (threadIdx.x == 32) prefetch_map(&p.tm_x);
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_u32(&c.tmem)),
@@ -213,12 +132,7 @@ router_tc_kernel(const __grid_constant__ TcParams p) {
       if (!(ok = warp_wait(&c.aempty[as], ap ^ 1, p.err, 1))) break;
       if (elect_one()) {
         mbar_expect_tx(&c.afull[as], kABytes);
-        asm volatile(
-            "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], "
-            "[%1, {%2, %3}], [%4];" ::"r"(smem_u32(smem + as * kABytes)),
-            "l"(reinterpret_cast<uint64_t>(&p.tm_x)), "r"(kt * 64), "r"(t0),
-            "r"(smem_u32(&c.afull[as]))
-            : "memory");
+        tma_2d(smem_u32(smem + as * kABytes), &p.tm_x, kt * 64, t0, &c.afull[as]);
       }
       __syncwarp();
       ++na;
@@ -228,12 +142,9 @@ router_tc_kernel(const __grid_constant__ TcParams p) {
         if (elect_one()) {
           mbar_expect_tx(&c.bfull[bs], two ? kBBytes : kBBytes / 2);
           for (int i = 0; i < 1 + (int)two; ++i)
-            asm volatile(
-                "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], "
-                "%2, [%3];" ::"r"(smem_u32(ring_b + bs * kBBytes + i * (kBBytes / 2))),
-                "l"(p.img + ((size_t)(mt0 + i) * (3 * p.KT) + q * p.KT + kt) * 8192),
-                "r"(kBBytes / 2), "r"(smem_u32(&c.bfull[bs]))
-                : "memory");
+            bulk_g2s(smem_u32(ring_b + bs * kBBytes + i * (kBBytes / 2)),
+                     p.img + ((size_t)(mt0 + i) * (3 * p.KT) + q * p.KT + kt) * 8192, kBBytes / 2,
+                     &c.bfull[bs]);
         }
         __syncwarp();
         ++nb;
@@ -344,19 +255,6 @@ router_tc_kernel(const __grid_constant__ TcParams p) {
   if (warp == 1)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
                  "r"(kTmemCols));
-}
-
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  if (!fn) {
-    void* ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
-  }
-  return fn;
 }
 
 }  // namespace
