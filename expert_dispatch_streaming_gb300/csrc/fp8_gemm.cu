@@ -486,6 +486,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
   if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLow));
   if (warp == 0) {
     // ------------------------------------------------------------ producer
+    const int who = !elect_one();               // 0: the lane that waits and issues
     int stage = 0, issued = 0;
     uint32_t phase = 0;
     bool ok = true;
@@ -509,7 +510,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
       const int nsub = t.rows > 96 ? 0 : (t.rows + 31) >> 5;
       const uint32_t bytes = load_bytes<FUSED>(p, t);
       for (int kb = wk.lo; kb < wk.hi; ++kb) {
-        if (!(ok = warp_wait(&c.empty[stage], phase ^ 1, p.err, 1))) break;
+        if (!(ok = lead_wait(&c.empty[stage], phase ^ 1, p.err, 1, who))) break;
         uint64_t* fb = &c.full[stage];
         const uint32_t sa = smem_u32(smem + stage * kStageBytes);
         if (elect_one()) {
@@ -534,7 +535,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
     // (bounded) for the last of each stage
     for (int i = 0; !ok && i < min(issued, kStages); ++i) {
       if (--stage < 0) { stage = kStages - 1; phase ^= 1; }
-      warp_wait(&c.full[stage], phase, p.err, 1);
+      lead_wait(&c.full[stage], phase, p.err, 1, who);
     }
   } else if (warp == 1 || warp == 3) {
     // ------------------------------------------------------------ MMA issuers
@@ -543,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
     // a tile is needed but its steps (where a tile has one weight tile only, the second's
     // columns take what the stage held and are not stored).
     const uint32_t idesc = idesc_e4m3(128, kAccCols);
-    const int buf = warp >> 1;
+    const int buf = warp >> 1, who = !elect_one();
     const uint32_t d = tmem + buf * kAccCols;
     int stage = 0, turn = 0;
     uint32_t phase = 0, tphase = 0;
@@ -555,8 +556,8 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
           // so has s - 3, the stage's last use, which the other issuer waited for.  Looked at
           // before that, the stage's barrier may still be two phases behind, where its parity
           // reads as complete.
-          if (!(ok = warp_wait(&c.tempty[buf], tphase ^ 1, p.err, 2))) break;
-          if (!(ok = warp_wait(&c.full[stage], phase, p.err, 3))) break;
+          if (!(ok = lead_wait(&c.tempty[buf], tphase ^ 1, p.err, 2, who))) break;
+          if (!(ok = lead_wait(&c.full[stage], phase, p.err, 3, who))) break;
           const uint32_t sa = smem_u32(smem + stage * kStageBytes);
           const uint64_t da = sdesc_sw128(sa), db = sdesc_sw128(sa + kABytes);
           if (elect_one()) {
@@ -575,7 +576,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
     if (!ok) {   // after a failed wait: the products still running write TMEM until they end
       if (elect_one()) mma_commit(&c.drain[buf]);
       __syncwarp();
-      warp_wait(&c.drain[buf], 0, p.err, 7);
+      lead_wait(&c.drain[buf], 0, p.err, 7, who);
     }
   } else if (warp == 2) {
     // ------------------------------------------------------------ scale factors
@@ -652,7 +653,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
       if (!here) {
         // no token of the tile on this warp's lanes: only pass the buffers on
         for (int kb = wk.lo; kb < wk.hi; ++kb) {
-          if (!(ok = warp_wait(&c.tfull[buf], tphase, p.err, 4))) break;
+          if (!(ok = lead_wait(&c.tfull[buf], tphase, p.err, 4, lane))) break;
           warp_arrive(&c.tempty[buf], lane);
           buf ^= 1;
           if (buf == 0) tphase ^= 1;

@@ -125,11 +125,12 @@ router_tc_kernel(const __grid_constant__ TcParams p) {
   if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLow));
   if (warp == 0) {
     // ------------------------------------------------------------ producer
+    const int who = !elect_one();               // 0: the lane that waits and issues
     int as = 0, bs = 0, na = 0, nb = 0;
     uint32_t ap = 0, bp = 0;
     bool ok = true;
     for (int kt = lo; ok && kt < hi; ++kt) {
-      if (!(ok = warp_wait(&c.aempty[as], ap ^ 1, p.err, 1))) break;
+      if (!(ok = lead_wait(&c.aempty[as], ap ^ 1, p.err, 1, who))) break;
       if (elect_one()) {
         mbar_expect_tx(&c.afull[as], kABytes);
         tma_2d(smem_u32(smem + as * kABytes), &p.tm_x, kt * 64, t0, &c.afull[as]);
@@ -138,7 +139,7 @@ router_tc_kernel(const __grid_constant__ TcParams p) {
       ++na;
       if (++as == kA) { as = 0; ap ^= 1; }
       for (int q = 0; q < 3; ++q) {
-        if (!(ok = warp_wait(&c.bempty[bs], bp ^ 1, p.err, 2))) break;
+        if (!(ok = lead_wait(&c.bempty[bs], bp ^ 1, p.err, 2, who))) break;
         if (elect_one()) {
           mbar_expect_tx(&c.bfull[bs], two ? kBBytes : kBBytes / 2);
           for (int i = 0; i < 1 + (int)two; ++i)
@@ -155,11 +156,11 @@ router_tc_kernel(const __grid_constant__ TcParams p) {
     // slot
     for (int i = 0; !ok && i < min(na, kA); ++i) {
       if (--as < 0) { as = kA - 1; ap ^= 1; }
-      warp_wait(&c.afull[as], ap, p.err, 1);
+      lead_wait(&c.afull[as], ap, p.err, 1, who);
     }
     for (int i = 0; !ok && i < min(nb, kB); ++i) {
       if (--bs < 0) { bs = kB - 1; bp ^= 1; }
-      warp_wait(&c.bfull[bs], bp, p.err, 2);
+      lead_wait(&c.bfull[bs], bp, p.err, 2, who);
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
@@ -167,16 +168,17 @@ router_tc_kernel(const __grid_constant__ TcParams p) {
     // and are not stored)
     const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((256u >> 3) << 17) |
                            ((128u >> 4) << 24);
+    const int who = !elect_one();
     int as = 0, bs = 0, buf = 0;
     uint32_t ap = 0, bp = 0, tp = 0;
     bool ok = true;
     for (int kt = lo; ok && kt < hi; ++kt) {
-      if (!(ok = warp_wait(&c.tempty[buf], tp ^ 1, p.err, 3))) break;
-      if (!(ok = warp_wait(&c.afull[as], ap, p.err, 4))) break;
+      if (!(ok = lead_wait(&c.tempty[buf], tp ^ 1, p.err, 3, who))) break;
+      if (!(ok = lead_wait(&c.afull[as], ap, p.err, 4, who))) break;
       const uint64_t da = sdesc_sw128(smem_u32(smem + as * kABytes));
       const uint32_t d = tmem + buf * kAccCols;
       for (int q = 0; q < 3; ++q) {
-        if (!(ok = warp_wait(&c.bfull[bs], bp, p.err, 4))) break;
+        if (!(ok = lead_wait(&c.bfull[bs], bp, p.err, 4, who))) break;
         const uint64_t db = sdesc_sw128(smem_u32(ring_b + bs * kBBytes));
         if (elect_one()) {
           tc_fence_after();
@@ -198,7 +200,7 @@ router_tc_kernel(const __grid_constant__ TcParams p) {
     if (!ok) {   // after a failed wait: the products still running write TMEM until they end
       if (elect_one()) mma_commit(&c.drain);
       __syncwarp();
-      warp_wait(&c.drain, 0, p.err, 7);
+      lead_wait(&c.drain, 0, p.err, 7, who);
     }
   } else if (warp >= 4) {
     // ------------------------------------------------------------ sums

@@ -34,45 +34,53 @@ static __device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t by
                "r"(bytes)
                : "memory");
 }
-// One try of lane 0 only, by predicate: 32 lanes polling one barrier are 32 operations on it.
-static __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity, int lane) {
+// One try by the lane whose `who` is 0 only, by predicate: 32 lanes polling one barrier are 32
+// operations on it.
+static __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity, int who) {
   uint32_t ok;
   asm volatile(
       "{\n.reg .pred p, q;\nsetp.eq.s32 q, %3, 0;\nsetp.ne.s32 p, 0, 0;\n"
       "@q mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}\n"
       : "=r"(ok)
-      : "r"(bar), "r"(parity), "r"(lane)
+      : "r"(bar), "r"(parity), "r"(who)
       : "memory");
   return ok != 0;
 }
 // The same without suspending the thread, for a look ahead of the wait.
-static __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity, int lane) {
+static __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity, int who) {
   uint32_t ok;
   asm volatile(
       "{\n.reg .pred p, q;\nsetp.eq.s32 q, %3, 0;\nsetp.ne.s32 p, 0, 0;\n"
       "@q mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}\n"
       : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity), "r"(lane)
+      : "r"(smem_u32(bar)), "r"(parity), "r"(who)
       : "memory");
   return ok != 0;
 }
 // Bounded wait of a converged warp (votes decide: the warp never diverges); `early`: the result of
-// a look at this phase already taken, whose latency other work has covered.
-static __device__ __forceinline__ bool warp_wait(uint64_t* b, uint32_t parity, int32_t* err,
-                                                 int code, bool early = false) {
+// a look at this phase already taken, whose latency other work has covered.  A vote orders no
+// memory: what the barrier guards is only the polling lane's (`who` 0) to touch.
+static __device__ __forceinline__ bool lead_wait(uint64_t* b, uint32_t parity, int32_t* err,
+                                                 int code, int who, bool early = false) {
   const uint32_t bar = smem_u32(b);
-  const int lane = threadIdx.x & 31;
   if (__any_sync(0xffffffffu, early)) return true;
-  if (__any_sync(0xffffffffu, mbar_try(bar, parity, lane))) return true;
+  if (__any_sync(0xffffffffu, mbar_try(bar, parity, who))) return true;
   const uint64_t t0 = globaltimer();
   for (uint32_t i = 1;; ++i) {
-    if (__any_sync(0xffffffffu, mbar_try(bar, parity, lane))) return true;
+    if (__any_sync(0xffffffffu, mbar_try(bar, parity, who))) return true;
     if ((i & 255) == 0 && __any_sync(0xffffffffu, globaltimer() - t0 > kTcWaitNs)) {
       pdl_wait();                               // (the word may still be being cleared)
-      if (lane == 0) atomicExch(err, code);
+      if (who == 0) atomicExch(err, code);
       return false;
     }
   }
+}
+// The same for all lanes: __syncwarp passes on to them what lane 0 has acquired.
+static __device__ __forceinline__ bool warp_wait(uint64_t* b, uint32_t parity, int32_t* err,
+                                                 int code, bool early = false) {
+  const bool ok = lead_wait(b, parity, err, code, threadIdx.x & 31, early);
+  __syncwarp();
+  return ok;
 }
 static __device__ __forceinline__ void bulk_g2s(uint32_t dst, const void* src, uint32_t bytes,
                                                 uint64_t* bar) {
@@ -92,6 +100,7 @@ static __device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* m
 static __device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
+// One lane of a converged warp, the same one every time.
 static __device__ __forceinline__ bool elect_one() {
   uint32_t pred = 0;
   asm volatile(
