@@ -297,7 +297,6 @@ __device__ __forceinline__ void finish_token(const GateParams& p, int t, GroupSm
   const bool none = __all_sync(0xffffffffu, has == 0.f);
   if (lane < k) {
     p.ids[(size_t)t * k + lane] = id;
-    if (p.ids_local) p.ids_local[lane] = id;
     p.w[(size_t)t * k + lane] = none ? 0.f : v * (p.scale / denom);
     atomicAdd(&p.hist[(t / kTileT) * E + id], 1);
   }
