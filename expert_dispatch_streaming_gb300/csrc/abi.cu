@@ -277,20 +277,19 @@ struct DevExperts {
 
 // The two FP8 products of an expert FFN (`gu` holds the caller's rows, tables and expert list).
 // Without work between the two, the down product may start while gate/up ends (see Fp8Args).
-static int run_fp8(const moe_bundle_layout& lay, Fp8Args gu, const Fp8Plan& pg, const Fp8Plan& pd,
-                   uint8_t* hq, float* hs, uint16_t* y, const LayerScratch& s, cudaStream_t st,
-                   const std::function<int()>& between) {
+static int run_fp8(const moe_bundle_layout& lay, Fp8Args gu, uint8_t* hq, float* hs, uint16_t* y,
+                   const LayerScratch& s, cudaStream_t st, const std::function<int()>& between) {
   Fp8Args dn = fp8_args(lay, false, gu.N, gu.K, gu.E, gu.max_rows);
   dn.offsets = gu.offsets; dn.tab = gu.tab; dn.dev_tab = gu.dev_tab;
   dn.active = gu.active; dn.n_active = gu.n_active; dn.host_n = gu.host_n;
   dn.host_ids = gu.host_ids;
   gu.hq = hq; gu.hs = hs;
   dn.xq = hq; dn.xs = hs; dn.y = y;
-  int r = launch_fp8(gu, pg, s.part, s.counters, s.err, st);
+  int r = launch_fp8(gu, s.part, s.counters, s.err, st);
   if (r != MOE_OK) return r;
   if (between && (r = between()) != MOE_OK) return r;
   dn.after = between ? kAfterAny : kAfterRows;
-  return launch_fp8(dn, pd, s.part, s.counters, s.err, st);
+  return launch_fp8(dn, s.part, s.counters, s.err, st);
 }
 
 static int run_experts(const moe_layer* L, const LayerPlan& P, const LayerScratch& s,
@@ -304,7 +303,7 @@ static int run_experts(const moe_layer* L, const LayerPlan& P, const LayerScratc
     Fp8Args q = fp8_args(P.lay, true, L->H, L->I, L->E, rows);
     q.xq = s.xq; q.xs = s.xs; q.offsets = s.offsets; q.active = act; q.n_active = nact;
     q.tab = &tab; q.dev_tab = dx.tab; q.host_n = host_n; q.host_ids = host_ids;
-    return run_fp8(P.lay, q, P.qgu, P.qdn, s.hq, s.hs, s.y_perm, s, st, between);
+    return run_fp8(P.lay, q, s.hq, s.hs, s.y_perm, s, st, between);
   }
   GemmArgs gu = gemm_args(P.lay, L->wdtype, true, L->H, L->I, L->E, rows, T);
   gu.xin = s.x_perm; gu.offsets = s.offsets; gu.active = act;
@@ -362,7 +361,7 @@ static int run_shared(const moe_layer* L, const LayerPlan& P, const LayerScratch
     if (q != MOE_OK) return q;
     Fp8Args a = fp8_args(P.slay, true, L->H, L->Is, 1, T);   // one group: every token's row
     a.xq = s.xq_s; a.xs = s.xs_s; a.tab = &tab;
-    return run_fp8(P.slay, a, P.qsgu, P.qsdn, s.hq_s, s.hs_s, s.s, s, st, nullptr);
+    return run_fp8(P.slay, a, s.hq_s, s.hs_s, s.s, s, st, nullptr);
   }
   GemmArgs gu = gemm_args(P.slay, L->wdtype, true, L->H, L->Is, 1, T);
   gu.xin = x; gu.offsets = meta; gu.active = meta + 2; gu.n_active = meta + 3;

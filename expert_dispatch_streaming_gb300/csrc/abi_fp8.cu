@@ -62,7 +62,7 @@ int moe_grouped_gemm_fp8(const uint8_t* xq, const float* x_scale, const uint8_t*
   const int r = launch_clear(err, ctl, st);
   if (r != MOE_OK) return r;
   a.after = kAfterClear;
-  return launch_fp8(a, pl, part, ctr, err, st);
+  return launch_fp8(a, part, ctr, err, st);
 }
 
 size_t moe_grouped_swiglu_fp8_workspace_size(int max_rows, int E, int H, int I) {
@@ -114,12 +114,12 @@ int moe_grouped_swiglu_fp8(const uint8_t* xq, const float* x_scale, const int32_
   gu.after = kAfterClear;
   gu.xq = xq; gu.xs = x_scale; gu.offsets = offsets; gu.tab = &tab;
   gu.w_off = lay.gate_up_offset; gu.s_off = lay.gate_up_scale_offset; gu.hq = hq; gu.hs = hs;
-  r = launch_fp8(gu, pg, part, ctr, err, st);
+  r = launch_fp8(gu, part, ctr, err, st);
   if (r != MOE_OK) return r;
   dn.after = kAfterRows;
   dn.xq = hq; dn.xs = hs; dn.offsets = offsets; dn.tab = &tab;
   dn.w_off = lay.down_offset; dn.s_off = lay.down_scale_offset; dn.y = y_perm;
-  return launch_fp8(dn, pd, part, ctr, err, st);
+  return launch_fp8(dn, part, ctr, err, st);
 }
 
 }  // extern "C"

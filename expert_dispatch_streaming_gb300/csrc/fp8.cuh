@@ -73,8 +73,7 @@ struct Fp8Plan {
 
 // counters must be zero on entry and are zero again when the launch has finished
 Fp8Plan plan_fp8(const Fp8Args& a);
-int launch_fp8(const Fp8Args& a, const Fp8Plan& pl, float* part, int32_t* counters, int32_t* err,
-               cudaStream_t st);
+int launch_fp8(const Fp8Args& a, float* part, int32_t* counters, int32_t* err, cudaStream_t st);
 
 // zeroes the control words of a workspace (bytes: a multiple of 16)
 int launch_clear(void* words, size_t bytes, cudaStream_t st);

@@ -917,8 +917,7 @@ Fp8Plan plan_fp8(const Fp8Args& a) {
   return pl;
 }
 
-int launch_fp8(const Fp8Args& a, const Fp8Plan&, float* part, int32_t* counters, int32_t* err,
-               cudaStream_t st) {
+int launch_fp8(const Fp8Args& a, float* part, int32_t* counters, int32_t* err, cudaStream_t st) {
   if (a.max_rows <= 0 || a.host_n == 0) return MOE_OK;
   if (!encode_fn()) return MOE_ERR_UNSUPPORTED;
   Fp8Params p{};
