@@ -455,7 +455,7 @@ RoutePlan plan_route(int T, int H, int E, int k, bool has_gate, bool grouped) {
 
 size_t route_scratch(WsCursor& c, const RoutePlan& r, int T, int E, RouteScratch* out) {
   RouteScratch s{};
-  s.part = c.take<float>((size_t)r.S * T * r.C);
+  s.part = c.take<float>(r.own_tc ? 0 : (size_t)r.S * T * r.C);
   s.hist = c.take<int32_t>((size_t)std::max(r.ntiles, 1) * E + (r.own_tc ? T + 1 : 0));
   s.base = c.take<int32_t>((size_t)std::max(r.ntiles, 1) * E);
   s.active = c.take<int32_t>(kMaxExperts);

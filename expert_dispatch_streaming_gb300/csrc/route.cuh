@@ -57,7 +57,7 @@ constexpr int kSeparateGatherMinT = 1024;
 constexpr size_t kFusedGatherMaxBytes = size_t(512) << 10;
 
 struct RouteScratch {
-  float* part;      // [S][T][C]
+  float* part;      // [S][T][C] (own_tc: none)
   int32_t* hist;    // [ntiles][E] (own_tc: followed by the count and list of tokens to re-score)
   int32_t* base;    // [ntiles][E]
   int32_t* active;  // [E] experts with rows, ascending
