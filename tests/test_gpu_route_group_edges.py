@@ -54,3 +54,40 @@ def test_weights_of_far_negative_logits(moe, level, k, T):
     # weight by twice that relatively, and the functions' own 2^-20
     tol = w * (2.5 * bound[:, None] + 2 * 2.0 ** -24 * (abs(level) + 8) + 2.0 ** -20)
     assert np.all(np.abs(got["w"] - w)[clear] <= tol[clear])
+
+
+@pytest.mark.parametrize("T,E,groups", [(600, 60, 6), (4100, 256, 8)])
+def test_nan_rows_of_large_batches(moe, T, E, groups):
+    """A NaN activation on the tensor-core product: its own token takes the first experts, the
+    others are untouched."""
+    x, w_r, lb, sb = inputs(T, T, 128, E, MODES[0])
+    bad = [0, 1, 127, 128, T - 1]
+    x[bad, [0, 5, 63, 64, 127]] = float("nan")
+    got = run(moe, x, w_r, lb, sb, E, 4, groups, 3, MODES[0])
+    assert np.array_equal(got["ids"][bad], np.tile(np.arange(4), (5, 1)))
+    keep = np.setdiff1d(np.arange(T), bad)
+    x2, _, _, _ = inputs(T, T, 128, E, MODES[0])
+    want = run(moe, x2, w_r, lb, sb, E, 4, groups, 3, MODES[0])
+    assert np.array_equal(got["ids"][keep], want["ids"][keep])
+    assert np.array_equal(got["w"][keep], want["w"][keep])
+
+
+@pytest.mark.parametrize("mode", MODES)
+@pytest.mark.parametrize("pattern", ["thirds", "groups", "all", "low"])
+def test_masks_of_large_batches(moe, pattern, mode):
+    T, H, E, groups, take, k = 4100, 128, 256, 8, 3, 6
+    b = (0.1 * np.random.default_rng(5).standard_normal(E)).astype(np.float32)
+    if pattern == "thirds":
+        b[::3] = -np.inf
+    elif pattern == "groups":
+        b[40:] = -np.inf                            # one group and a quarter for three places
+    elif pattern == "all":
+        b[:] = -np.inf
+    else:
+        b[:224] = LOW
+    lb, sb = (None, b) if mode == MODES[0] else (b, None)
+    x, w_r, _, _ = inputs(1, T, H, E, mode)
+    got = run(moe, x, w_r, lb, sb, E, k, groups, take, mode)
+    check(got, reference(x, w_r, lb, sb, k, groups, take, mode, 1.0), k, E)
+    if pattern == "all" and mode != MODES[0]:
+        assert (got["w"] == 0).all()
