@@ -33,13 +33,14 @@
 // arrive (a counter per lane quarter), which adds the pieces' fp32 sums in range order, so the
 // result does not depend on the arrival order.
 //
-// Measured: 8192 rows of 8 experts x 4096 x 14336 at 2.3 PFLOP/s; 65,536 rows of 256 SwiGLU experts
-// of 7168 x 2048 in 3.4 ms (1.7 PFLOP/s, 3.7 TB/s of necessary bytes); 32 tokens of the same layer
-// at the copy bandwidth of HBM.  What bounds the large ones is a step's way through shared memory (48 KB
+// Measured, inputs changing from call to call: 8192 rows of 8 experts x 4096 x 14336 in 457 us (2.1
+// PFLOP/s); 65,536 rows of 256 SwiGLU experts of 7168 x 2048 in 3.6 ms (1.6 PFLOP/s, 3.5 TB/s of
+// necessary bytes); 32 tokens of the same layer in 874 us, the copy bandwidth of HBM.  (The same
+// inputs again and again: 418 us and 3.4 ms.)  What bounds the large ones is a step's way through shared memory (48 KB
 // in, 48 KB out to the tensor cores: without the epilogue 2.8-3.0 PFLOP/s) and the epilogue warps'
 // chain of wait, TMEM load, multiply-add and release, about 1000 clocks a step against 540 of
 // tensor work (tensor pipe 52% busy, issue slots 42%).  Sixteen epilogue warps of half the columns
-// were slower (468 us against 428), half-step TMEM buffers no faster.  Of the small ones, launch,
+// were slower (468 us against 428 on the same inputs), half-step TMEM buffers no faster.  Of the small ones, launch,
 // tile tables and first load take 3-5 us before the first product, joining pieces 2-5 after the last.
 //
 // Every wait is bounded (2 s; then an error word and the kernel ends).

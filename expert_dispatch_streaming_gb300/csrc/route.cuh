@@ -45,8 +45,9 @@ struct RoutePlan {
 // batches of at least this many tokens compute the router product on the tensor cores
 constexpr int kTcRouterMinT = 256;
 // ... and group-limited ones of at least this many by route_tc.cu's kernel (the whole routing of
-// 7168 x 256 experts: 512 tokens 49 us instead of 56, 1024 57 / 68, 8192 151 / 184).  It is the
-// faster one for 256 tokens too (53 / 62), but there the logits stay moe_route_topk's to the bit.
+// 7168 x 256 experts: 512 tokens 56 us instead of 65, 1024 71 / 82, 2048 80 / 93, 8192 140 / 180).
+// It is the faster one for 256 tokens too (56 / 64), but there the logits stay moe_route_topk's to
+// the bit.
 constexpr int kOwnTcMinT = 512;
 // batches of at most this many tokens run everything after the router product in one CTA
 constexpr int kSmallT = 16;

@@ -19,7 +19,7 @@
 // 32 / n_group lanes (rounded down to a power of two) scan a group, each keeping the two largest
 // it saw.  What costs here is latency: a lane's loads go out together, a token takes 5,600 clocks
 // (scores 1,950, groups 930, experts 1,420, weights and tables 1,300), and the few tokens that need
-// re-scoring, 12 us each, are shared by their whole CTA.
+// re-scoring, 12 us each by device clock stamps, are shared by their whole CTA.
 #include "gate.cuh"
 #include "route.cuh"
 
@@ -590,8 +590,8 @@ gate_group_kernel(const __grid_constant__ GateParams p, int n_group, int take) {
 // Large batches in two steps: the tokens that need re-scoring, one or two in a hundred, each take
 // several times as long as the others, and their CTAs would be the last; so the first kernel lists
 // them and a second gives each a CTA of its own.  (The whole routing of 256 experts: 8192 tokens
-// 152 us with one kernel, 137 with two, 4096 107 / 104, 2048 81 / 82; of 60 experts, where fewer
-// scores are close, 8192 tokens 60 / 63.)  The list's order varies from run to run; nothing else
+// 147 us with one kernel, 140 with two, 4096 104 / 98, 2048 80 / 86; of 60 experts, where fewer
+// scores are close, 8192 tokens 65 / 67.)  The list's order varies from run to run; nothing else
 // depends on it.
 template <int NC>
 __global__ void __launch_bounds__(G_WARPS * 32)

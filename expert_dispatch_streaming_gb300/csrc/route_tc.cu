@@ -16,8 +16,9 @@
 //               at the end the sums leave through shared memory by rows.
 //
 // Bound by shared memory and its filling: a block reads 12 x 12 KB of operands and takes in 112 KB
-// for 1536 clocks of tensor work.  8192 tokens x 7168 x 256 columns (two parts, 128 CTAs): 66 us,
-// 1.4 PFLOP/s of the three pieces' products (ungrouped routing's kernel, weights as M: 94 us).
+// for 1536 clocks of tensor work.  8192 tokens x 7168 x 256 columns (two parts, 128 CTAs): 68 us,
+// 1.3 PFLOP/s of the three pieces' products, tensor pipe 70% busy on the SMs in use (ungrouped
+// routing's kernel, weights as M: 94 us).
 // Every wait is bounded (2 s; then an error word and the end).
 #include "route.cuh"
 #include "tc_ptx.cuh"
