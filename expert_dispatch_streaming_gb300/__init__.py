@@ -129,6 +129,8 @@ _SIGS = {
     "moe_route_topk_static": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _f,
                                    _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
     "moe_route_static_error": (_i, [C.POINTER(C.c_int32), _vp]),
+    "moe_sort_tokens_workspace_size": (_sz, [_i, _i, _i]),
+    "moe_sort_tokens": (_i, [_vp, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
     "moe_permute": (_i, [_vp, _vp, _i, _i, _i, _vp, _vp]),
     "moe_grouped_swiglu_workspace_size": (_sz, [_i, _i, _i, _i, _i]),
     "moe_grouped_swiglu": (_i, [_vp, _vp, C.POINTER(_vp), _i, _i, _i, _i, _i, _vp, _vp, _sz,
@@ -140,6 +142,13 @@ _SIGS = {
     "moe_grouped_swiglu_fp8_workspace_size": (_sz, [_i, _i, _i, _i]),
     "moe_grouped_swiglu_fp8": (_i, [_vp, _vp, _vp, C.POINTER(_vp), _i, _i, _i, _i, _vp, _vp,
                                     _sz, _vp]),
+    "moe_grouped_gemv_int4_workspace_size": (_sz, [_i, _i, _i, _i]),
+    "moe_grouped_gemv_int4": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp, _vp, _sz,
+                                   _vp]),
+    "moe_permute_backward": (_i, [_vp, _vp, _vp, _i, _i, _i, _i, _vp, _vp]),
+    "moe_combine_backward": (_i, [_vp, _vp, _vp, _vp, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp,
+                                  _vp]),
+    "moe_gate_backward": (_i, [_vp, _vp, _vp, _i, _i, _i, _i, _f, _vp, _vp]),
     "moe_combine": (_i, [_vp, _vp, _vp, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _f, _vp]),
     "moe_expert_cache_create": (_i, [C.POINTER(moe_expert_cache_config), C.POINTER(_vp),
                                      C.POINTER(C.c_int64)]),
@@ -328,6 +337,16 @@ def moe_route_static_error(stream=None) -> int:
     return code.value
 
 
+def moe_sort_tokens_workspace_size(T, E, k) -> int:
+    return _lib.moe_sort_tokens_workspace_size(T, E, k)
+
+
+def moe_sort_tokens(ids, T, E, k, counts, offsets, pos, src, ws, ws_bytes, stream=None) -> None:
+    """Dispatch of ids [T][k]; ids outside [0, E) are slots without a row (pos -1)."""
+    _check(_lib.moe_sort_tokens(ptr(ids), T, E, k, ptr(counts), ptr(offsets), ptr(pos), ptr(src),
+                                ptr(ws), ws_bytes, stream_handle(stream)), "moe_sort_tokens")
+
+
 def moe_permute(x, src, T, k, H, x_perm, stream=None) -> None:
     _check(_lib.moe_permute(ptr(x), ptr(src), T, k, H, ptr(x_perm), stream_handle(stream)),
            "moe_permute")
@@ -398,6 +417,42 @@ def moe_combine(y_perm, pos, w, T, k, H, shared, shared_gate, residual, out, str
                             ptr(shared_gate), ptr(residual), ptr(out), ptr(out_normed),
                             float(norm_eps), stream_handle(stream)),
            "moe_combine")
+
+
+def moe_grouped_gemv_int4_workspace_size(max_rows, E, N, K) -> int:
+    return _lib.moe_grouped_gemv_int4_workspace_size(max_rows, E, N, K)
+
+
+def moe_grouped_gemv_int4(x, w, w_scale, w_zero, offsets, E, N, K, group, max_rows, out, y, ws,
+                          ws_bytes, stream=None) -> None:
+    """w [E][N][K/2] uint8 (two codes a byte, the lower half first), w_scale [E][N][K/group] bf16,
+    w_zero the same in uint8 or None (8); out: 'bf16' or 'fp32' (the type of y)."""
+    _check(_lib.moe_grouped_gemv_int4(ptr(x), ptr(w), ptr(w_scale), ptr(w_zero), ptr(offsets), E, N,
+                                      K, group, max_rows, OUT_DTYPE.get(out, out), ptr(y), ptr(ws),
+                                      ws_bytes, stream_handle(stream)), "moe_grouped_gemv_int4")
+
+
+def moe_permute_backward(dx_perm, pos, add, T, k, H, out, dx, stream=None) -> None:
+    """dx[t] = sum of dx_perm's rows pos[t] (+ add[t]); out: 'bf16' or 'fp32' (the type of dx)."""
+    _check(_lib.moe_permute_backward(ptr(dx_perm), ptr(pos), ptr(add), T, k, H,
+                                     OUT_DTYPE.get(out, out), ptr(dx), stream_handle(stream)),
+           "moe_permute_backward")
+
+
+def moe_combine_backward(dout, y_perm, pos, w, T, k, H, shared, shared_gate, dy_perm, dw,
+                         dshared=None, dshared_gate=None, stream=None) -> None:
+    """Gradients of moe_combine; outputs that are None are not computed."""
+    _check(_lib.moe_combine_backward(ptr(dout), ptr(y_perm), ptr(pos), ptr(w), T, k, H, ptr(shared),
+                                     ptr(shared_gate), ptr(dy_perm), ptr(dw), ptr(dshared),
+                                     ptr(dshared_gate), stream_handle(stream)),
+           "moe_combine_backward")
+
+
+def moe_gate_backward(logits, ids, dw, T, E, k, gating, scale, dlogits, stream=None) -> None:
+    """dlogits [T][E] of the weights' gradient dw [T][k] at the chosen ids."""
+    _check(_lib.moe_gate_backward(ptr(logits), ptr(ids), ptr(dw), T, E, k,
+                                  GATING.get(gating, gating), float(scale), ptr(dlogits),
+                                  stream_handle(stream)), "moe_gate_backward")
 
 
 def moe_expert_cache_create(cfg: moe_expert_cache_config) -> int:

@@ -31,9 +31,6 @@ __device__ __forceinline__ uint32_t fp8_pack4(float a, float b, float c, float d
   return r;
 }
 
-inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
-inline bool aligned256(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 255u) == 0; }
-
 // One grouped product over FP8 operands:
 //   acc[row][n] = sum_b xs[row][b] ws_e[n / 128][b] sum_{k in block b} xq[row][k] w_e[n][k]
 // fused: w_e = gate rows 0..N-1 and up rows N..2N-1; h = silu(gate) * up is quantised per row

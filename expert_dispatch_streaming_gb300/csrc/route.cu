@@ -369,9 +369,13 @@ gather_rows_kernel(const uint16_t* __restrict__ x, const int32_t* __restrict__ s
   pdl_wait();
   const int warp = (blockIdx.x * blockDim.x + threadIdx.x) >> 5, lane = threadIdx.x & 31;
   if (warp >= rows) return;
-  const int nvec = H / 8;
-  const uint4* s = reinterpret_cast<const uint4*>(x + (size_t)(src[warp] / k) * H);
+  const int nvec = H / 8, from = src[warp];
   uint4* d = reinterpret_cast<uint4*>(x_perm + (size_t)warp * H);
+  if ((unsigned)from >= (unsigned)rows) {   // a row that no slot takes: zeros
+    for (int v = lane; v < nvec; v += 32) d[v] = make_uint4(0u, 0u, 0u, 0u);
+    return;
+  }
+  const uint4* s = reinterpret_cast<const uint4*>(x + (size_t)(from / k) * H);
 #pragma unroll 4
   for (int v = lane; v < nvec; v += 32) d[v] = __ldg(s + v);
 }

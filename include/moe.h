@@ -85,7 +85,7 @@ int moe_set_option(int option, int value);
  *   1-7  a bounded wait inside a tensor-core kernel ran out of time;
  *   9    a bounded wait inside the fused decode kernel ran out of time;
  *   8    an expert's row range [offsets[e], offsets[e+1]) reached outside [0, max_rows)
- *        (moe_grouped_swiglu) and was clipped to it;
+ *        (moe_grouped_swiglu, the grouped products) and was clipped to it;
  *   10   an expert with rows had no bundle (moe_grouped_swiglu_fp8, MOE_W_FP8_B128 layers): its
  *        output rows were not written;
  *   20   a device-LRU cache request needed more distinct bundles than slots.
@@ -326,9 +326,26 @@ int moe_route_topk_static(const uint16_t* x, const float* w_r, const float* logi
  * stream can overwrite the word. */
 int moe_route_static_error(int32_t* code, void* stream);
 
+/* moe_sort_tokens -- the dispatch outputs of moe_route_topk for expert ids that come from elsewhere
+ * (another router, a hash, a batch with padding).
+ *  ids     device [T][k] int32.  An id outside [0, E) marks a slot without an expert (padding):
+ *          it has no row.  An expert may stand in a token's row more than once; each slot is a row.
+ *  outputs (device): counts [E] and offsets [E+1] of the slots that have a row; pos [T][k]: the
+ *          slot's row in expert order, stable in t * k + j, or -1; src [T*k]: src[pos[t][j]] =
+ *          t*k + j, and -1 in the entries from offsets[E] on.
+ *  ws      device scratch of moe_sort_tokens_workspace_size(T, E, k) bytes, 4-byte aligned
+ * moe_permute, moe_quantize_fp8, moe_combine and the gradients below take such pos and src.
+ * Limits: 1 <= E <= 256, 1 <= k <= 8, T >= 0 (T == 0 writes zero counts and offsets; ids, pos, src
+ * and ws may be NULL then), T * k < 2^31.  The dispatch is that of "NovaLLM ...", "3. Optimization
+ * #1 -- Expert-Level Streaming"; the pages do not say how a token's rows are found. */
+size_t moe_sort_tokens_workspace_size(int T, int E, int k);
+int moe_sort_tokens(const int32_t* ids, int T, int E, int k, int32_t* counts, int32_t* offsets,
+                    int32_t* pos, int32_t* src, void* ws, size_t ws_bytes, void* stream);
+
 /* ------------------------------------------------------------------ step 4: permute
  * x_perm[p][:] = x[src[p] / k][:] for p in [0, T*k).
  *  x device [T][H] bf16, src device [T*k] int32, x_perm device [T*k][H] bf16.
+ * A row whose src lies outside [0, T*k) is written as zeros.
  * H a multiple of 8.  The pages define no permutation step: it is the gather that puts each
  * expert's tokens next to each other so that every selected expert's weights are read once per
  * batch ("NovaLLM ...", "3. Optimization #1 -- Expert-Level Streaming" asks only that the
@@ -420,6 +437,36 @@ int moe_grouped_swiglu_fp8(const uint8_t* xq, const float* x_scale, const int32_
                            const void* const* bundles, int E, int H, int I, int max_rows,
                            uint16_t* y_perm, void* ws, size_t ws_bytes, void* stream);
 
+/* moe_grouped_gemv_int4 -- products of few rows with 4-bit weights (a decode step's rows; the
+ * weights are read once): for every expert e with rows [offsets[e], offsets[e+1]):
+ *   y[row][n] = sum over groups g of `group` k:  w_scale[e][n][g] *
+ *               sum_{k in g} (q[e][n][k] - zero[e][n][g]) * x[row][k]
+ * with fp32 sums, one group's products summed before its scale is applied.
+ *  x        device [max_rows][K] bf16
+ *  w        device [E][N][K/2]: weight rows of two codes a byte, k even in the lower four bits,
+ *           codes 0..15
+ *  w_scale  device [E][N][ceil(K/group)] bf16
+ *  w_zero   device [E][N][ceil(K/group)] uint8, values 0..127, or NULL: 8 everywhere
+ *  group    32, 64 or 128; a row's last group may be shorter
+ *  offsets  device [E+1] int32 (from moe_route_topk or moe_sort_tokens), or NULL with E == 1: one
+ *           dense product of max_rows rows
+ *  y        device [max_rows][N], bf16 (out_f32 = 0, rounded once) or fp32 (out_f32 = 1); rows
+ *           outside every expert's range are left as they are
+ *  max_rows upper bound of offsets[E]; ranges reaching outside [0, max_rows) are clipped and
+ *           error 8 is recorded (moe_workspace_error)
+ *  ws       device scratch of moe_grouped_gemv_int4_workspace_size(max_rows, E, N, K) bytes,
+ *           256-byte aligned
+ * Limits: 1 <= E <= 256, N >= 1, K a multiple of 32; x, w, y 16-byte, w_scale 2-byte aligned.  Any
+ * number of rows is computed; from some dozens per expert on the products bound it, not the reads.
+ * A NaN or infinite product reaches the outputs of its token row and weight row only.
+ * "Running 35B MoE Models on 8GB GPUs ...", "Technical Insight" names 4-bit checkpoints; the layout
+ * is the row-major one with zero points that such checkpoints are published in, not a bundle's. */
+size_t moe_grouped_gemv_int4_workspace_size(int max_rows, int E, int N, int K);
+int moe_grouped_gemv_int4(const uint16_t* x, const uint8_t* w, const uint16_t* w_scale,
+                          const uint8_t* w_zero, const int32_t* offsets, int E, int N, int K,
+                          int group, int max_rows, int out_f32, void* y, void* ws,
+                          size_t ws_bytes, void* stream);
+
 /* ------------------------------------------------------------------ step 6: combine
  * out[t] = bf16( sum_{j<k} w[t][j] * y_perm[pos[t][j]] + g_t * shared[t] ), fp32 inside,
  * j in order 0..k-1, g_t = shared_gate[t] (1 when shared_gate is NULL; the shared term is
@@ -429,12 +476,58 @@ int moe_grouped_swiglu_fp8(const uint8_t* xq, const float* x_scale, const int32_
  *   out_normed[t] = bf16( out[t] / sqrt(mean_h out[t][h]^2 + norm_eps) )
  * computed from the bf16 values of out[t] (sum of squares in fp32); H <= 32768 then.
  *  y_perm device [T*k][H] bf16; pos, w device [T][k]; shared, residual, out device [T][H].
+ * A slot whose pos lies outside [0, T*k) has no term, whatever its weight.
  * The pages define no combine step: it is the gate-weighted sum that undoes the permutation,
  * the usual form of a top-k MoE layer's output. */
 int moe_combine(const uint16_t* y_perm, const int32_t* pos, const float* w, int T, int k,
                 int H, const uint16_t* shared, const float* shared_gate,
                 const uint16_t* residual, uint16_t* out, uint16_t* out_normed, float norm_eps,
                 void* stream);
+
+/* ------------------------------------------------------------------ gradients
+ * Of the way into expert order, of the weighted way back and of the gating: what training a router
+ * (or experts of one's own) around this layer's dispatch needs.  pos as moe_route_topk or
+ * moe_sort_tokens give it; a slot whose pos lies outside [0, T*k) has no row.  All sums in fp32 and
+ * in a fixed order.  The pages describe inference only.
+ *
+ * moe_permute_backward -- of moe_permute:  dx[t] = sum_{j<k} dx_perm[pos[t][j]] + add[t], j in order.
+ *  dx_perm device [T*k][H] bf16; add device [T][H] bf16 or NULL (a gradient that reaches x on
+ *  another way: the residual, the shared expert, the router); dx device [T][H], bf16 (out_f32 = 0,
+ *  rounded once) or fp32 (out_f32 = 1).  H a multiple of 8; dx_perm, add, dx 16-byte aligned; k <= 8. */
+int moe_permute_backward(const uint16_t* dx_perm, const int32_t* pos, const uint16_t* add, int T,
+                         int k, int H, int out_f32, void* dx, void* stream);
+
+/* moe_combine_backward -- of moe_combine (without out_normed; the roundings of out and of the
+ * residual's sum count as the identity, so the residual's gradient is dout):
+ *   dy_perm[pos[t][j]] = bf16( w[t][j] * dout[t] )    rows that no slot takes are left as they are
+ *   dw[t][j]           = <dout[t], y_perm[pos[t][j]]>  0 for a slot without a row
+ *   dshared[t]         = bf16( shared_gate[t] * dout[t] )   (1 when shared_gate is NULL)
+ *   dshared_gate[t]    = <dout[t], shared[t]>
+ *  dout, shared, dshared device [T][H] bf16; y_perm, dy_perm device [T*k][H] bf16; w, dw device
+ *  [T][k] fp32; shared_gate, dshared_gate device [T] fp32.  Any of the four outputs may be NULL
+ *  (not all); y_perm is read for dw only, shared for dshared_gate only (which needs shared and
+ *  shared_gate).  dy_perm must not overlap the inputs.
+ *  H a multiple of 8; bf16 rows 16-byte aligned; k <= 8. */
+int moe_combine_backward(const uint16_t* dout, const uint16_t* y_perm, const int32_t* pos,
+                         const float* w, int T, int k, int H, const uint16_t* shared,
+                         const float* shared_gate, uint16_t* dy_perm, float* dw,
+                         uint16_t* dshared, float* dshared_gate, void* stream);
+
+/* moe_gate_backward -- of the weights w of moe_route_topk and moe_route_topk_grouped with respect to
+ * the logits, for the chosen ids (the choice itself has no gradient):
+ *   SOFTMAX_RENORM:      dl[id_j] = scale r_j (dw_j - D)
+ *   SIGMOID_BIAS_RENORM: dl[id_j] = scale r_j (dw_j - D) (1 - sigmoid(l[id_j]))
+ *   SOFTMAX:             dl[e]    = scale p_e ( [e = id_j] dw_j - D ),  r = p
+ * with r_j = w_j / scale and D = sum_j r_j dw_j; zero for every other expert.
+ *  logits device [T][E] fp32 (incl. logit_bias, as moe_route_topk writes them); ids device [T][k]
+ *  int32, dw device [T][k] fp32; dlogits device [T][E] fp32, every element written; gating: enum
+ *  moe_gating without MOE_GATING_GROUPED.
+ * An id outside [0, E) is a slot without an expert: its dw is not read and it is in no sum.  An id
+ * that stands twice in a row counts as two slots.  A token whose weights are all zero (every score
+ * open to it -infinity, see moe_route_topk_grouped) gets zero gradients.
+ * Limits: E <= 256, k <= min(E, 8). */
+int moe_gate_backward(const float* logits, const int32_t* ids, const float* dw, int T, int E,
+                      int k, int gating, float scale, float* dlogits, void* stream);
 
 /* ------------------------------------------------------------------ expert-slot cache
  * A fixed pool of VRAM slots, each holding one expert bundle, filled from pinned host
