@@ -179,24 +179,36 @@ EXPORTED = tuple(_SIGS)
 # ----------------------------------------------------------------------------- marshalling
 def ptr(x) -> int | None:
     """Device/host address of a tensor / array / int (None -> NULL)."""
-    if x is None:
-        return None
-    if isinstance(x, int):
+    if x is None or isinstance(x, int):
         return x
-    if hasattr(x, "data_ptr"):
+    try:
         return x.data_ptr()
+    except AttributeError:
+        pass
     if hasattr(x, "ctypes"):
         return x.ctypes.data
     raise TypeError(type(x))
 
 
+def _current_stream() -> int | None:
+    """Handle of torch's current stream on the current device, None without torch or a GPU.  (The
+    first call replaces this function by the two lookups alone: torch.cuda.current_stream()
+    builds a stream object, 3 us a call on Grace against 0.2.)"""
+    global _current_stream
+    try:
+        import torch
+        handle = torch.cuda.current_stream().cuda_stream
+        raw, device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+        if raw(device()) == handle:
+            _current_stream = lambda: raw(device())  # noqa: E731
+        return handle
+    except Exception:
+        return None
+
+
 def stream_handle(s) -> int | None:
     if s is None:
-        try:
-            import torch
-            return torch.cuda.current_stream().cuda_stream
-        except Exception:
-            return None
+        return _current_stream()
     if isinstance(s, int):
         return s
     return s.cuda_stream

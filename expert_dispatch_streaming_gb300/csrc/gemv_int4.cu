@@ -3,38 +3,55 @@
 //   y[r][n] = sum_g s[e][n][g] * sum_{k in group g} (q[e][n][k] - z[e][n][g]) x[r][k]
 //
 // for the rows r of expert e; q a 4-bit code, s a bf16 scale and z a zero point of `G` codes along
-// K.  A weight is read once and used for at most a few rows, so reading the codes bounds it.
+// K.  A weight is read once and used for a few rows, so reading the codes bounds it.
 //
-// m16n8k16 products of bf16 values: 16 weight rows against eight token rows.  q - z is exact in
-// bf16: 0x4300 | q is 128 + q, and (128 + q) - (128 + z) loses nothing.  One group's products are
-// added in fp32 before its scale is applied, in fp32, as moe_grouped_gemm_fp8 does.
+// m16n8k16 products of bf16 values: 16 weight rows against eight token rows.  (tcgen05's smallest
+// tile has 128 weight rows and wants its operand written to shared memory or TMEM first, which costs
+// more than the few token rows' products.)  One group's products are added in fp32 before its scale
+// is applied, in fp32, as moe_grouped_gemm_fp8 does.
+//
+// Codes to bf16.  Masked with 0x000F000F a code word is two bf16 of value q * 2^-133 (the bits of an
+// integer below 256 read as a bf16 are that integer times 2^-133: subnormals and the first normal
+// binade are one linear range), masked with 0x00F000F0 two of 16 q * 2^-133.  One bf16 fma,
+// times 2^127 or 2^123 minus z 2^-6, gives (q - z) 2^-6 exactly; the sum is multiplied by 2^6 at the
+// end.  Four pairs of a word take one shift, four masks and four fmas.
 //
 // The order of K inside a product is free as long as both operands agree.  A lane's codes for
 // weight row n are the 8 of one 32-bit word, words of the four lanes of a row next to each other:
-// nibble pairs (i, i + 4) come out of one shift and one mask, and the token row's eight values from
-// one 16-byte load.  With 128-code groups a lane loads 16 bytes (four words of one group), with
-// 64-code groups twice 8, with 32-code groups four times 4, so that the four lanes of a row hold
-// the same group in every product.
+// 32 codes, which one group covers whatever its size.  Nibble pairs (i, i + 4) come out together,
+// and the token row's eight values come from one 16-byte load.
 //
-// A CTA takes 16 weight rows of one expert, its eight warps 128-code steps of K in turn; the warps'
-// sums are added in warp order in shared memory.
+// An item is 16, 32 or 48 weight rows of one expert against eight token rows, over the whole of K, so
+// that no sum crosses CTAs; the height is the one that leaves the fewest CTAs without work.  A CTA's
+// eight warps share an item's K, 256 codes at a time, and keep a step's token values in registers
+// for all its weight rows.  Each warp has a ring of its own in shared memory, filled by TMA
+// (boxes of the item's rows x 128 bytes, swizzled, so that the lanes' words lie in different
+// banks) and running on from one item to the next; token values and scales are loaded ahead of their
+// use.  The warps' sums are added in warp order in shared memory.
 #include "common.cuh"
 #include "route.cuh"
+#include "tc_ptx.cuh"
 
 #include <type_traits>
 
 namespace moe {
 namespace {
 
-constexpr int kGvWarps = 8, kGvThreads = kGvWarps * 32, kGvRows = 16, kGvStep = 128;
+constexpr int kGvWarps = 8, kGvThreads = kGvWarps * 32;
+constexpr int kGvUnit = 16;              // weight rows of a product
+constexpr int kGvMaxTile = 3;            // units of an item at most
+constexpr int kGvStep = 256;             // codes of K of a box (128 bytes a row)
+constexpr int kGvWarpRing = 12288;       // bytes of a warp's ring: 6, 3 or 2 boxes
+constexpr int kGvRing = kGvWarps * kGvWarpRing + 1024;
+constexpr int kGvErrWait = 6;            // error word: a wait for weights ran out of time
 
 struct GemvArgs {
   const uint16_t* x;
-  const uint8_t* w;
   const uint16_t* s;
   const uint8_t* z;
   const int32_t* offsets;
   int E, N, K, ng, max_rows;
+  bool f32, wide;                              // wide: a step's scales of a row are one aligned load
   void* y;
   int32_t* err;
 };
@@ -47,18 +64,37 @@ __device__ __forceinline__ void mma_bf16(float* d, uint32_t a0, uint32_t a1, uin
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Codes I and I + 4 of a word as the bf16 pair q - z; zp: 128 + z in both halves.
+// The four pairs of a code word as (q - z) 2^-6; nz: -z 2^-6 in both halves.
+__device__ __forceinline__ void code_pairs(uint32_t w, uint32_t nz, uint32_t (&p)[4]) {
+  const uint32_t h = w >> 8;
+  const uint32_t v[4] = {w & 0x000F000Fu, w & 0x00F000F0u, h & 0x000F000Fu, h & 0x00F000F0u};
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;"
+        : "=r"(p[i])
+        : "r"(v[i]), "r"(i & 1 ? 0x7D007D00u : 0x7F007F00u), "r"(nz));
+}
+// -z 2^-6 in both halves, z = byte I of `zeros`, 0..127: 128 + z by its bits, then an exact fma.
 template <int I>
-__device__ __forceinline__ uint32_t code_pair(uint32_t word, uint32_t zp) {
-  const uint32_t v = ((word >> (4 * I)) & 0x000F000Fu) | 0x43004300u;
+__device__ __forceinline__ uint32_t zero_pair(uint32_t zeros) {
+  const uint32_t v = __byte_perm(zeros, 0x43434343u, 0x4040 | (I << 8) | I);
   uint32_t d;
-  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(v), "r"(zp));
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(v), "r"(0xBC80BC80u), "r"(0x40004000u));
   return d;
 }
 
-// The experts with rows, ascending, in `act`, their row ranges in lo / hi; returns their number.
-// CTA 0 records in the error word whether a range was clipped.
-__device__ int active_experts(const GemvArgs& a, int16_t* act, int* lo, int* hi, int* wsum) {
+struct GemvSmem {
+  uint64_t full[kGvWarps][6];
+  float red[kGvWarps][4][kGvMaxTile * kGvUnit + 4];   // the warps' sums of four token rows
+  int lo[kMaxExperts], hi[kMaxExperts];        // token rows of the experts that have some
+  int passes[kMaxExperts + 1];                 // eights of token rows of the experts before
+  int16_t act[kMaxExperts];
+  int wsum[2][kGvWarps];
+};
+
+// The experts with rows, ascending, with their ranges; returns how many there are.  CTA 0 records in
+// the error word whether a range was clipped.
+__device__ int active_experts(const GemvArgs& a, GemvSmem& sm) {
   const int e = threadIdx.x, lane = e & 31, warp = e >> 5;
   int b = 0, n = 0;
   bool clipped = false;
@@ -73,159 +109,335 @@ __device__ int active_experts(const GemvArgs& a, int16_t* act, int* lo, int* hi,
     b = cb;
     n = max(ce - cb, 0);
   }
+  const int mine = (n + 7) / 8;
+  int before = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, before, o);
+    if (lane >= o) before += v;
+  }
   const unsigned m = __ballot_sync(0xffffffffu, n > 0);
-  if (lane == 0) wsum[warp] = __popc(m);
+  if (lane == 31) {
+    sm.wsum[0][warp] = __popc(m);
+    sm.wsum[1][warp] = before;
+  }
+  before -= mine;
   const int any = __syncthreads_or(clipped);
   if (blockIdx.x == 0 && threadIdx.x == 0) *a.err = any ? 8 : 0;
-  int at = __popc(m & ((1u << lane) - 1u)), total = 0;
+  int at = __popc(m & ((1u << lane) - 1u)), total = 0, all = 0;
 #pragma unroll
   for (int i = 0; i < kGvWarps; ++i) {
-    at += i < warp ? wsum[i] : 0;
-    total += wsum[i];
+    at += i < warp ? sm.wsum[0][i] : 0;
+    before += i < warp ? sm.wsum[1][i] : 0;
+    total += sm.wsum[0][i];
+    all += sm.wsum[1][i];
   }
   if (n > 0) {
-    act[at] = (int16_t)e;
-    lo[at] = b;
-    hi[at] = b + n;
+    sm.act[at] = (int16_t)e;
+    sm.lo[at] = b;
+    sm.hi[at] = b + n;
+    sm.passes[at] = before;
   }
+  if (threadIdx.x == 0) sm.passes[total] = all;
   __syncthreads();
   return total;
 }
 
-// G: codes a scale covers; RT: groups of eight token rows that pass through the weights together.
-template <int G, bool ZERO, bool F32, int RT>
-__global__ void __launch_bounds__(kGvThreads)
-gemv_int4_kernel(const GemvArgs a) {
-  constexpr int NG = kGvStep / G;          // groups of a step
-  constexpr int WPL = G / 32;              // words of a lane in one group
+__device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2,
+                                       uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, "
+      "{%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar))
+      : "memory");
+}
+
+
+// The words of four 8 x 16-byte blocks: a lane gets word t of row gr of each.
+__device__ __forceinline__ void load_words(uint32_t (&w)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+               : "r"(addr)
+               : "memory");
+}
+// An item: weight rows from n0 on of expert e against token rows [rb, hi) (at most eight).
+struct GemvItem {
+  int e, n0, rb, hi;
+};
+template <int NT>
+__device__ __forceinline__ GemvItem gemv_item(const GemvSmem& sm, long long it, int ntile, int n_act) {
+  const int pass = (int)(it / ntile);
+  int a = 0, b = n_act;                        // the last expert whose passes start at or before it
+  while (b - a > 1) {
+    const int c = (a + b) >> 1;
+    if (sm.passes[c] <= pass) a = c;
+    else b = c;
+  }
+  const int rb = sm.lo[a] + 8 * (pass - sm.passes[a]);
+  return {sm.act[a], (int)(it - (long long)pass * ntile) * (NT * kGvUnit), rb, min(sm.hi[a], rb + 8)};
+}
+
+// G: codes a scale covers; NT: units of an item.
+template <int G, bool ZERO, int NT>
+__global__ void __launch_bounds__(kGvThreads, 2)
+gemv_int4_kernel(const GemvArgs a, const __grid_constant__ CUtensorMap tm) {
+  constexpr int NG = kGvStep / G;              // groups of a step: 2, 4, 8
+  constexpr int CG = G / 32;                   // 32-code chunks of a group
+  constexpr int kBox = NT * kGvUnit * kGvStep / 2, kBoxes = kGvWarpRing / kBox;
   static_assert(kMaxExperts <= kGvThreads, "one thread per expert");
-  __shared__ int16_t act[kMaxExperts];
-  __shared__ int e_lo[kMaxExperts], e_hi[kMaxExperts], wsum[kGvWarps];
-  __shared__ float red[kGvWarps][8 * RT][kGvRows + 1];
+  extern __shared__ uint8_t ring_raw[];
+  __shared__ GemvSmem sm;
+  const int lane = threadIdx.x & 31, gr = lane >> 2, t = lane & 3;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);   // (the same for every lane)
+  uint64_t* full = sm.full[warp];
+  // (the swizzle goes by address bits: the ring starts on a 1024-byte boundary)
+  const uint32_t ring = ((smem_u32(ring_raw) + 1023u) & ~1023u) + warp * kGvWarpRing;
   pdl_trigger();
+  if (lane == 0) {
+    for (int i = 0; i < kBoxes; ++i) mbar_init(full + i, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    prefetch_map(&tm);
+  }
   pdl_wait();
-  const int n_act = active_experts(a, act, e_lo, e_hi, wsum);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gr = lane >> 2, t = lane & 3;
-  const int ntile = (a.N + kGvRows - 1) / kGvRows;
+  const int n_act = __shfl_sync(0xffffffffu, active_experts(a, sm), 0);
+  const int ntile = (a.N + NT * kGvUnit - 1) / (NT * kGvUnit);
   const int steps = (a.K + kGvStep - 1) / kGvStep;
-  const size_t row_bytes = (size_t)a.K / 2;
-  const long long items = (long long)n_act * ntile;
+  const long long items = (long long)sm.passes[n_act] * ntile;
+  // A warp's steps of an item are first, first + 8, ...: dealt out from where the last item's ended.
+  auto following = [&](int first) { return (first + kGvWarps - steps % kGvWarps) % kGvWarps; };
+
+  // the next box to ask for
+  long long a_it = blockIdx.x;
+  int a_first = warp, a_st = warp, put = 0, place = 0;
+  GemvItem ai{0, 0, 0, 0};
+  if (a_it < items) ai = gemv_item<NT>(sm, a_it, ntile, n_act);
+  auto ask = [&] {
+    while (a_st >= steps) {
+      a_it += gridDim.x;
+      if (a_it >= items) break;
+      ai = gemv_item<NT>(sm, a_it, ntile, n_act);
+      a_st = a_first = following(a_first);
+    }
+    if (a_it >= items) return;
+    if (lane == 0) {
+      mbar_expect_tx(full + place, kBox);
+      tma_3d(ring + place * kBox, &tm, a_st * (kGvStep / 2), ai.n0, ai.e, full + place);
+    }
+    ++put;
+    place = place + 1 == kBoxes ? 0 : place + 1;
+    a_st += kGvWarps;
+  };
+  for (int i = 0; i < kBoxes; ++i) ask();
+  int got = 0, dead = -1;                      // boxes used; the first that did not come in time
+  int slot = 0;
+  uint32_t phase = 0;
+
+  // Where the values of a step come from.  Token values: lane (gr, t) those of row gr that its words'
+  // codes meet; rows past the item's last read that one (their sums are not stored), and what lies
+  // past the end of K is set to zero when it is used.  A step's scales of the weight rows gr and gr + 8 of
+  // a unit: lanes t = 0 and 1, two in a register; their zero points: lanes t = 2 and 3, four in a
+  // register.  Rows and groups past the end read the last ones (those rows are not stored, those
+  // groups' products are zero).
+  struct Source {
+    const uint16_t* x;
+    size_t s;
+    int row, st;                               // the last weight row, counted from the item's first
+  };
+  auto source = [&](const GemvItem& i, int st) {
+    return Source{a.x + (size_t)min(i.rb + gr, i.hi - 1) * a.K, ((size_t)i.e * a.N + i.n0) * a.ng,
+                  a.N - 1 - i.n0, st};
+  };
+  uint4 xv[8];
+  auto token_value = [&](const Source& f, int c) {
+    const int k = f.st * kGvStep + 8 * t;
+    xv[c] = __ldg(reinterpret_cast<const uint4*>(f.x + min(k + 32 * c, a.K - 8)));
+  };
+  uint32_t rv[NG / 2];
+  auto scale_values = [&](const Source& f, int i) {
+    const size_t at = f.s + (size_t)((uint32_t)min(16 * i + gr + 8 * (t & 1), f.row) * a.ng);
+    const int g0 = f.st * NG;
+    if (a.wide) {
+      const uint16_t* s = a.s + at + g0;
+      const uint8_t* z = a.z + at + g0;
+      if (t < 2) {
+        if (NG == 2) {
+          rv[0] = __ldg(reinterpret_cast<const uint32_t*>(s));
+        } else if (NG == 4) {
+          const uint2 v = __ldg(reinterpret_cast<const uint2*>(s));
+          rv[0] = v.x;
+          rv[1 % (NG / 2)] = v.y;
+        } else {
+          const uint4 v = __ldg(reinterpret_cast<const uint4*>(s));
+          rv[0] = v.x;
+          rv[1 % (NG / 2)] = v.y;
+          rv[2 % (NG / 2)] = v.z;
+          rv[3 % (NG / 2)] = v.w;
+        }
+      } else if (ZERO) {
+        if (NG == 2) {
+          rv[0] = __ldg(reinterpret_cast<const uint16_t*>(z));
+        } else if (NG == 4) {
+          rv[0] = __ldg(reinterpret_cast<const uint32_t*>(z));
+        } else {
+          const uint2 v = __ldg(reinterpret_cast<const uint2*>(z));
+          rv[0] = v.x;
+          rv[1 % (NG / 2)] = v.y;
+        }
+      }
+    } else if (t < 2) {
+#pragma unroll
+      for (int j = 0; j < NG / 2; ++j) {
+        const uint32_t lo = __ldg(a.s + at + min(g0 + 2 * j, a.ng - 1));
+        rv[j] = lo | (uint32_t)__ldg(a.s + at + min(g0 + 2 * j + 1, a.ng - 1)) << 16;
+      }
+    } else if (ZERO) {
+#pragma unroll
+      for (int j = 0; j < (NG + 3) / 4; ++j) {
+        uint32_t v = 0u;
+#pragma unroll
+        for (int b = 0; b < 4; ++b) v |= (uint32_t)__ldg(a.z + at + min(g0 + 4 * j + b, a.ng - 1)) << (8 * b);
+        rv[j] = v;
+      }
+    }
+  };
+  // where the lane points ldmatrix: chunks 2 c, 2 c + 1 of weight rows 0..7 and 8..15
+  uint32_t wa[4];
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+    wa[c] = ring + (lane & 15) * 128 + (((2 * c + (lane >> 4)) ^ (lane & 7)) << 4);
+
+  int first = warp;
+  bool loaded = false;                         // are the item's first values under way?
+  GemvItem next{0, 0, 0, 0};
+  if (blockIdx.x < items) next = gemv_item<NT>(sm, blockIdx.x, ntile, n_act);
   for (long long it = blockIdx.x; it < items; it += gridDim.x) {
-    const int ai = (int)(it / ntile), n0 = (int)(it % ntile) * kGvRows;
-    const int e = act[ai], hi = e_hi[ai];
-    // the lane's two weight rows (those past the end read the last one; not stored)
-    const size_t r0 = (size_t)e * a.N + min(n0 + gr, a.N - 1);
-    const size_t r1 = (size_t)e * a.N + min(n0 + gr + 8, a.N - 1);
-    const uint8_t* w0 = a.w + r0 * row_bytes;
-    const uint8_t* w1 = a.w + r1 * row_bytes;
-    const uint16_t *s0 = a.s + r0 * a.ng, *s1 = a.s + r1 * a.ng;
-    const uint8_t *z0 = ZERO ? a.z + r0 * a.ng : nullptr, *z1 = ZERO ? a.z + r1 * a.ng : nullptr;
-    for (int rb = e_lo[ai]; rb < hi; rb += 8 * RT) {
-      float acc[RT][4];
+    const GemvItem cur = next;
+    if (it + gridDim.x < items) next = gemv_item<NT>(sm, it + gridDim.x, ntile, n_act);
+    Source src = source(cur, first);
+    if (!loaded && first < steps) {
 #pragma unroll
-      for (int i = 0; i < RT; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
-      for (int st = warp; st < steps; st += kGvWarps) {
-        const int k0 = st * kGvStep;
-        uint32_t q0[4], q1[4];
+      for (int c = 0; c < 8; ++c) token_value(src, c);
+      scale_values(src, 0);
+    }
+    first = following(first);
+    loaded = false;
+    float acc[NT][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) q0[i] = q1[i] = 0u;
+    for (int i = 0; i < NT; ++i)
 #pragma unroll
-        for (int j = 0; j < NG; ++j) {
-          const int k = k0 + j * G + t * 8 * WPL;
-          if (k < a.K) {
-            const uint8_t *p0 = w0 + k / 2, *p1 = w1 + k / 2;
-            if (WPL == 4) {
-              const uint4 u = __ldcs(reinterpret_cast<const uint4*>(p0));
-              const uint4 v = __ldcs(reinterpret_cast<const uint4*>(p1));
-              q0[0] = u.x; q0[1] = u.y; q0[2] = u.z; q0[3] = u.w;
-              q1[0] = v.x; q1[1] = v.y; q1[2] = v.z; q1[3] = v.w;
-            } else if (WPL == 2) {
-              const uint2 u = __ldg(reinterpret_cast<const uint2*>(p0));
-              const uint2 v = __ldg(reinterpret_cast<const uint2*>(p1));
-              q0[2 * j] = u.x; q0[2 * j + 1] = u.y;
-              q1[2 * j] = v.x; q1[2 * j + 1] = v.y;
-            } else {
-              q0[j] = __ldg(reinterpret_cast<const uint32_t*>(p0));
-              q1[j] = __ldg(reinterpret_cast<const uint32_t*>(p1));
-            }
-          }
-        }
-        // lane t of a row reads the scale of the step's group t (mod NG)
-        const int gi = st * NG + (t & (NG - 1));
-        float f0 = 0.f, f1 = 0.f;
-        uint32_t y0 = 8, y1 = 8;
-        if (gi < a.ng) {
-          f0 = bf16_bits_to_float(__ldg(s0 + gi));
-          f1 = bf16_bits_to_float(__ldg(s1 + gi));
-          if (ZERO) {
-            y0 = __ldg(z0 + gi);
-            y1 = __ldg(z1 + gi);
-          }
-        }
-#pragma unroll
-        for (int j = 0; j < NG; ++j) {
-          const int from = (lane & 28) | j;
-          const float sc0 = NG == 1 ? f0 : __shfl_sync(0xffffffffu, f0, from);
-          const float sc1 = NG == 1 ? f1 : __shfl_sync(0xffffffffu, f1, from);
-          uint32_t zp0 = 0x43084308u, zp1 = 0x43084308u;
-          if (ZERO) {
-            zp0 = 0x43004300u | (NG == 1 ? y0 : __shfl_sync(0xffffffffu, y0, from)) * 0x10001u;
-            zp1 = 0x43004300u | (NG == 1 ? y1 : __shfl_sync(0xffffffffu, y1, from)) * 0x10001u;
-          }
-          float d[RT][4];
-#pragma unroll
-          for (int i = 0; i < RT; ++i) d[i][0] = d[i][1] = d[i][2] = d[i][3] = 0.f;
-#pragma unroll
-          for (int wd = 0; wd < WPL; ++wd) {
-            const uint32_t u = q0[j * WPL + wd], v = q1[j * WPL + wd];
-            const int k = k0 + j * G + t * 8 * WPL + 8 * wd;
-            const uint32_t a00 = code_pair<0>(u, zp0), a01 = code_pair<0>(v, zp1);
-            const uint32_t a10 = code_pair<1>(u, zp0), a11 = code_pair<1>(v, zp1);
-            const uint32_t a20 = code_pair<2>(u, zp0), a21 = code_pair<2>(v, zp1);
-            const uint32_t a30 = code_pair<3>(u, zp0), a31 = code_pair<3>(v, zp1);
-#pragma unroll
-            for (int i = 0; i < RT; ++i) {
-              const int r = rb + 8 * i + gr;
-              uint4 xv = make_uint4(0u, 0u, 0u, 0u);
-              if (r < hi && k < a.K)
-                xv = __ldg(reinterpret_cast<const uint4*>(a.x + (size_t)r * a.K + k));
-              mma_bf16(d[i], a00, a01, a10, a11, __byte_perm(xv.x, xv.z, 0x5410),
-                       __byte_perm(xv.x, xv.z, 0x7632));
-              mma_bf16(d[i], a20, a21, a30, a31, __byte_perm(xv.y, xv.w, 0x5410),
-                       __byte_perm(xv.y, xv.w, 0x7632));
-            }
-          }
-#pragma unroll
-          for (int i = 0; i < RT; ++i) {
-            acc[i][0] = fmaf(sc0, d[i][0], acc[i][0]);
-            acc[i][1] = fmaf(sc0, d[i][1], acc[i][1]);
-            acc[i][2] = fmaf(sc1, d[i][2], acc[i][2]);
-            acc[i][3] = fmaf(sc1, d[i][3], acc[i][3]);
-          }
+      for (int c = 0; c < 4; ++c) acc[i][c] = 0.f;
+    while (src.st < steps) {
+      // the step whose values come next: this item's, or the next item's first
+      Source nx = src;
+      nx.st += kGvWarps;
+      const bool last = nx.st >= steps;
+      if (last) {
+        if (it + gridDim.x < items && first < steps) {
+          nx = source(next, first);
+          loaded = true;
+        } else {
+          nx.st = src.st;                      // (none: values that no one uses)
         }
       }
 #pragma unroll
-      for (int i = 0; i < RT; ++i) {
-        red[warp][8 * i + 2 * t][gr] = acc[i][0];
-        red[warp][8 * i + 2 * t + 1][gr] = acc[i][1];
-        red[warp][8 * i + 2 * t][gr + 8] = acc[i][2];
-        red[warp][8 * i + 2 * t + 1][gr + 8] = acc[i][3];
+      for (int c = 0; c < 8; ++c)              // the order of a word's pairs
+        xv[c] = make_uint4(__byte_perm(xv[c].x, xv[c].z, 0x5410),
+                           __byte_perm(xv[c].x, xv[c].z, 0x7632),
+                           __byte_perm(xv[c].y, xv[c].w, 0x5410),
+                           __byte_perm(xv[c].y, xv[c].w, 0x7632));
+      if ((src.st + 1) * kGvStep > a.K) {
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          if (src.st * kGvStep + 8 * t + 32 * c >= a.K) xv[c] = make_uint4(0u, 0u, 0u, 0u);
+      }
+      if (dead < 0 && !warp_wait(full + slot, phase, a.err, kGvErrWait)) dead = got;
+      const uint32_t box = slot * kBox;
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        uint32_t sz[NG / 2];
+#pragma unroll
+        for (int j = 0; j < NG / 2; ++j) sz[j] = rv[j];
+        if (i + 1 < NT) scale_values(src, i + 1);
+        else scale_values(nx, 0);
+        uint32_t f0 = 0u, f1 = 0u, zb0 = 0u, zb1 = 0u, w[4];
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+          if (g % 2 == 0) {
+            f0 = __shfl_sync(0xffffffffu, sz[g / 2], lane & 28);
+            f1 = __shfl_sync(0xffffffffu, sz[g / 2], (lane & 28) | 1);
+          }
+          if (ZERO && g % 4 == 0) {
+            zb0 = __shfl_sync(0xffffffffu, sz[g / 4], (lane & 28) | 2);
+            zb1 = __shfl_sync(0xffffffffu, sz[g / 4], (lane & 28) | 3);
+          }
+          uint32_t z0 = 0xBE00BE00u, z1 = 0xBE00BE00u;   // -8 * 2^-6
+          if (ZERO) {
+            z0 = g % 4 == 0 ? zero_pair<0>(zb0) : g % 4 == 1 ? zero_pair<1>(zb0)
+               : g % 4 == 2 ? zero_pair<2>(zb0) : zero_pair<3>(zb0);
+            z1 = g % 4 == 0 ? zero_pair<0>(zb1) : g % 4 == 1 ? zero_pair<1>(zb1)
+               : g % 4 == 2 ? zero_pair<2>(zb1) : zero_pair<3>(zb1);
+          }
+          float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int c = 0; c < CG; ++c) {
+            const int ch = g * CG + c;
+            if ((ch & 1) == 0) load_words(w, box + i * (kGvUnit * 128) + wa[ch / 2]);
+            uint32_t p[4], q[4];
+            code_pairs(w[2 * (ch & 1)], z0, p);
+            code_pairs(w[2 * (ch & 1) + 1], z1, q);
+            mma_bf16(d, p[0], q[0], p[1], q[1], xv[ch].x, xv[ch].y);
+            mma_bf16(d, p[2], q[2], p[3], q[3], xv[ch].z, xv[ch].w);
+            if (i + 1 == NT) token_value(nx, ch);
+          }
+          const float s0 = __uint_as_float(g % 2 ? f0 & 0xFFFF0000u : f0 << 16);
+          const float s1 = __uint_as_float(g % 2 ? f1 & 0xFFFF0000u : f1 << 16);
+          acc[i][0] = fmaf(s0, d[0], acc[i][0]);
+          acc[i][1] = fmaf(s0, d[1], acc[i][1]);
+          acc[i][2] = fmaf(s1, d[2], acc[i][2]);
+          acc[i][3] = fmaf(s1, d[3], acc[i][3]);
+        }
+      }
+      ++got;
+      if (++slot == kBoxes) {
+        slot = 0;
+        phase ^= 1;
+      }
+      __syncwarp();                            // the box is read: its place is free
+      if (dead < 0) ask();
+      if (last) break;
+      src = nx;
+    }
+    // the warps' sums, four token rows at a time
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int rows = cur.hi - cur.rb - 4 * h;
+      if (rows <= 0) break;
+      if ((t >> 1) == h) {
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            sm.red[warp][2 * (t & 1) + (c & 1)][16 * i + gr + 8 * (c >> 1)] = acc[i][c];
       }
       __syncthreads();
-      for (int i = threadIdx.x; i < 8 * RT * kGvRows; i += kGvThreads) {
-        const int n = i % kGvRows, r = i / kGvRows;
-        float v = red[0][r][n];
+      const int n = threadIdx.x & 63, r = threadIdx.x >> 6;
+      if (r < rows && n < NT * kGvUnit && cur.n0 + n < a.N) {
+        float v = sm.red[0][r][n];
 #pragma unroll
-        for (int q = 1; q < kGvWarps; ++q) v += red[q][r][n];
-        if (n0 + n < a.N && rb + r < hi) {
-          const size_t o = (size_t)(rb + r) * a.N + n0 + n;
-          if (F32) static_cast<float*>(a.y)[o] = v;
-          else static_cast<uint16_t*>(a.y)[o] = float_to_bf16_bits(v);
-        }
+        for (int q = 1; q < kGvWarps; ++q) v += sm.red[q][r][n];
+        const size_t at = (size_t)(cur.rb + 4 * h + r) * a.N + cur.n0 + n;
+        v *= 0x1p6f;
+        if (a.f32) static_cast<float*>(a.y)[at] = v;
+        else static_cast<uint16_t*>(a.y)[at] = float_to_bf16_bits(v);
       }
       __syncthreads();
     }
   }
+  // after a wait that ran out: what was asked for has to have landed before the memory goes
+  if (dead >= 0)
+    for (int i = dead; i < put; ++i)
+      warp_wait(full + i % kBoxes, (i / kBoxes) & 1, a.err, kGvErrWait);
 }
 
 bool valid_gemv_shape(int E, int N, int K, int max_rows) {
@@ -233,29 +445,50 @@ bool valid_gemv_shape(int E, int N, int K, int max_rows) {
          N <= (1 << 24) && K <= (1 << 24) && (long long)E * N < (1LL << 31);
 }
 
-template <int G, bool ZERO, bool F32, int RT>
-int launch_gemv(const GemvArgs& a, cudaStream_t st) {
-  const long long most = (long long)std::min(a.E, a.max_rows) * ceil_div(a.N, kGvRows);
-  const int grid = (int)std::min<long long>(most, 4LL * sm_count());
-  MOE_LAUNCH_PDL((gemv_int4_kernel<G, ZERO, F32, RT>), dim3(grid), dim3(kGvThreads), 0, st, a);
+bool encode_weights(CUtensorMap* m, const uint8_t* w, int E, int N, int K, int rows) {
+  const cuuint64_t row = (cuuint64_t)K / 2;
+  const cuuint64_t dims[3] = {row, (cuuint64_t)N, (cuuint64_t)E};
+  const cuuint64_t strides[2] = {row, row * N};
+  const cuuint32_t box[3] = {kGvStep / 2, (cuuint32_t)rows, 1}, step[3] = {1, 1, 1};
+  auto enc = encode_fn();
+  return enc && enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(w), dims, strides, box,
+                    step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int G, bool ZERO, int NT>
+int launch_gemv(const GemvArgs& a, long long items, const CUtensorMap& tm, cudaStream_t st) {
+  auto kernel = gemv_int4_kernel<G, ZERO, NT>;
+  MOE_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kGvRing));
+  MOE_LAUNCH_PDL(kernel, dim3((unsigned)std::min<long long>(items, 2LL * sm_count())),
+                 dim3(kGvThreads), kGvRing, st, a, tm);
   MOE_COUNT_LAUNCH();
   MOE_LAUNCH_CHECK();
   return MOE_OK;
 }
 
-template <int G, bool ZERO, bool F32>
-int launch_gemv_rows(const GemvArgs& a, cudaStream_t st) {
-  const int rows = ceil_div(a.max_rows, a.E);
-  if (rows <= 8) return launch_gemv<G, ZERO, F32, 1>(a, st);
-  if (rows <= 16) return launch_gemv<G, ZERO, F32, 2>(a, st);
-  return launch_gemv<G, ZERO, F32, 4>(a, st);
-}
-
-template <int G>
-int launch_gemv_types(const GemvArgs& a, bool f32, cudaStream_t st) {
-  if (a.z) return f32 ? launch_gemv_rows<G, true, true>(a, st)
-                      : launch_gemv_rows<G, true, false>(a, st);
-  return f32 ? launch_gemv_rows<G, false, true>(a, st) : launch_gemv_rows<G, false, false>(a, st);
+template <int G, bool ZERO>
+int launch_gemv(const GemvArgs& a, const uint8_t* w, cudaStream_t st) {
+  // passes at most: every expert's last eight token rows may be fewer
+  const long long passes = std::min<long long>(a.max_rows, a.E + a.max_rows / 8);
+  // the height whose rounds cost the least: its rows, and a step's token values (0.4 of a unit)
+  long long items = 0, best = 0;
+  int nt = 0;
+  for (int n = 1; n <= kGvMaxTile; ++n) {
+    const long long c = passes * ceil_div(a.N, n * kGvUnit), slots = 2LL * sm_count();
+    const long long cost = (c + slots - 1) / slots * (10 * n + 4);
+    if (!nt || cost <= best) {
+      nt = n;
+      best = cost;
+      items = c;
+    }
+  }
+  CUtensorMap tm;
+  if (!encode_weights(&tm, w, a.E, a.N, a.K, nt * kGvUnit)) return MOE_ERR_UNSUPPORTED;
+  if (nt == 1) return launch_gemv<G, ZERO, 1>(a, items, tm, st);
+  if (nt == 2) return launch_gemv<G, ZERO, 2>(a, items, tm, st);
+  return launch_gemv<G, ZERO, 3>(a, items, tm, st);
 }
 
 }  // namespace
@@ -278,15 +511,16 @@ int moe_grouped_gemv_int4(const uint16_t* x, const uint8_t* w, const uint16_t* w
   MOE_REQUIRE(group == 32 || group == 64 || group == 128);
   if (max_rows == 0) return MOE_OK;
   MOE_REQUIRE(x && w && w_scale && y && ws);
-  MOE_REQUIRE(aligned16(x) && aligned16(w) && aligned4(w_scale) && aligned16(y) &&
+  MOE_REQUIRE(aligned16(x) && aligned16(w) && aligned2(w_scale) && aligned16(y) &&
               aligned4(offsets) && aligned256(ws));
   MOE_REQUIRE(ws_bytes >= moe_grouped_gemv_int4_workspace_size(max_rows, E, N, K));
-  GemvArgs a{x, w, w_scale, w_zero, offsets, E, N, K, ceil_div(K, group), max_rows, y,
-             static_cast<int32_t*>(ws)};
+  const GemvArgs a{x, w_scale, w_zero, offsets, E, N, K, ceil_div(K, group), max_rows,
+                   out_f32 != 0, K % kGvStep == 0 && aligned16(w_scale) && aligned16(w_zero), y,
+                   static_cast<int32_t*>(ws)};
   cudaStream_t st = (cudaStream_t)stream;
-  if (group == 32) return launch_gemv_types<32>(a, out_f32 != 0, st);
-  if (group == 64) return launch_gemv_types<64>(a, out_f32 != 0, st);
-  return launch_gemv_types<128>(a, out_f32 != 0, st);
+  if (group == 32) return w_zero ? launch_gemv<32, true>(a, w, st) : launch_gemv<32, false>(a, w, st);
+  if (group == 64) return w_zero ? launch_gemv<64, true>(a, w, st) : launch_gemv<64, false>(a, w, st);
+  return w_zero ? launch_gemv<128, true>(a, w, st) : launch_gemv<128, false>(a, w, st);
 }
 
 }  // extern "C"
