@@ -165,89 +165,150 @@ combine_backward_kernel(const uint16_t* __restrict__ dout, const uint16_t* __res
 //   softmax_renorm:       dl_j = scale r_j (dw_j - D)
 //   sigmoid_bias_renorm:  dl_j = scale r_j (dw_j - D) (1 - sigmoid(l_j))
 //   softmax (over all E): dl_e = scale p_e ([e chosen] dw_e - D),  D = sum_j p_j dw_j
-// A warp takes a token: lane j < k the chosen expert j, then every lane its part of the dlogits
-// row, which is put together in shared memory.
+// Writing the dlogits rows bounds it.  SOFTMAX_RENORM and SIGMOID_BIAS_RENORM read the chosen logits
+// only: a warp takes four tokens, eight lanes each for the chosen experts, puts the rows together in
+// shared memory and stores them in 16-byte pieces.  SOFTMAX: a warp a token.
 constexpr int kGateBackWarps = 8;
 
-template <int MODE>
+// row[e] += scale * g of the lanes' experts (id < 0: none); eight lanes a row.  An expert that a row
+// has twice is added in lane order.
+__device__ __forceinline__ void add_chosen(float* row, int id, float g, int lane) {
+  const unsigned group = 0xFFu << (lane & 24);
+  const unsigned same = __match_any_sync(0xffffffffu, id < 0 ? -1 - lane : id + 256 * (lane >> 3));
+  const bool twice = __popc(same & group) > 1;
+  if (id >= 0 && !twice) row[id] += g;
+  if (__any_sync(0xffffffffu, twice)) {
+    for (int j = 0; j < kMaxK; ++j) {
+      if ((lane & 7) == j && id >= 0 && twice) row[id] += g;
+      __syncwarp();
+    }
+  }
+  __syncwarp();
+}
+__device__ __forceinline__ float sum8(float v) {
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+__device__ __forceinline__ float max8(float v) {
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+
+template <bool SIGMOID>
 __global__ void __launch_bounds__(kGateBackWarps * 32)
-gate_backward_kernel(const float* __restrict__ logits, const int32_t* __restrict__ ids,
-                     const float* __restrict__ dw, int T, int E, int k, float scale,
-                     float* __restrict__ dl) {
+gate_backward_chosen_kernel(const float* __restrict__ logits, const int32_t* __restrict__ ids,
+                            const float* __restrict__ dw, int T, int E, int k, float scale,
+                            bool wide, float* __restrict__ dl) {
   pdl_trigger();
+  __shared__ float4 rows_s[kGateBackWarps][4][kMaxExperts / 4];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, j = lane & 7;
+  float* rows = reinterpret_cast<float*>(rows_s[warp]);
+  const int t0 = (blockIdx.x * kGateBackWarps + warp) * 4, t = t0 + (lane >> 3);
+#pragma unroll
+  for (int i = 0; i < kMaxExperts / 32; ++i)
+    reinterpret_cast<float4*>(rows)[lane + 32 * i] = make_float4(0.f, 0.f, 0.f, 0.f);
   pdl_wait();
+  int id = -1;
+  float up = 0.f, l = -CUDART_INF_F;
+  if (t < T && j < k) {
+    id = __ldg(ids + (size_t)t * k + j);
+    const float d = __ldg(dw + (size_t)t * k + j);
+    if ((unsigned)id < (unsigned)E) {
+      up = d;
+      l = __ldg(logits + (size_t)t * E + id);
+    } else {
+      id = -1;
+    }
+  }
+  float v, total;
+  if (!SIGMOID) {
+    const float top = max8(l);
+    v = id >= 0 && top != -CUDART_INF_F ? expf(l - top) : 0.f;
+    total = sum8(v);
+  } else {
+    v = id >= 0 ? 1.f / (1.f + expf(-l)) : 0.f;
+    total = sum8(v);
+    const bool tiny = total < 0x1p-64f;
+    if (__any_sync(0xffffffffu, tiny)) {
+      // sigmoids that fp32 is about to lose: e^l is their ratio to 2^-64, as far as 64 bits hold them
+      // (the weights' own rule); beyond, weights and gradients are zero
+      const float top = max8(l);
+      if (tiny) v = id >= 0 && top > -709.f ? expf(l - top) : 0.f;
+      const float again = sum8(v);
+      if (tiny) total = again;
+    }
+  }
+  const float r = total == 0.f ? 0.f : v / total;
+  const float D = sum8(id >= 0 ? r * up : 0.f);
+  float g = id >= 0 ? scale * (r * (up - D)) : 0.f;
+  if (SIGMOID) g *= 1.f / (1.f + expf(l));
+  __syncwarp();
+  add_chosen(rows + (lane >> 3) * kMaxExperts, id, g, lane);
+  if (wide) {
+    const int nv = E / 4;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      if (t0 + q >= T) break;
+      float4* o = reinterpret_cast<float4*>(dl + (size_t)(t0 + q) * E);
+      for (int e = lane; e < nv; e += 32)
+        __stcs(o + e, reinterpret_cast<const float4*>(rows)[q * (kMaxExperts / 4) + e]);
+    }
+  } else {
+    for (int q = 0; q < 4 && t0 + q < T; ++q)
+      for (int e = lane; e < E; e += 32)
+        dl[(size_t)(t0 + q) * E + e] = rows[q * kMaxExperts + e];
+  }
+}
+
+__global__ void __launch_bounds__(kGateBackWarps * 32)
+gate_backward_softmax_kernel(const float* __restrict__ logits, const int32_t* __restrict__ ids,
+                             const float* __restrict__ dw, int T, int E, int k, float scale,
+                             float* __restrict__ dl) {
+  pdl_trigger();
   __shared__ float row_s[kGateBackWarps][kMaxExperts];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   float* row = row_s[warp];
-  for (long long t = (long long)blockIdx.x * kGateBackWarps + warp; t < T;
-       t += (long long)gridDim.x * kGateBackWarps) {
-    const float* lr = logits + t * E;
-    int id = -1;
-    float up = 0.f, l = -CUDART_INF_F;
-    if (lane < k) {
-      id = __ldg(ids + t * k + lane);
-      if ((unsigned)id < (unsigned)E) {
-        up = __ldg(dw + t * k + lane);
-        l = __ldg(lr + id);
-      } else {
-        id = -1;
-      }
-    }
-    float z[kMaxExperts / 32];
-    float top, v, total;
-    if (MODE == MOE_GATING_SOFTMAX) {
-      top = -CUDART_INF_F;
+  const int t = blockIdx.x * kGateBackWarps + warp;
+  pdl_wait();
+  if (t >= T) return;
+  const float* lr = logits + (size_t)t * E;
+  float z[kMaxExperts / 32], top = -CUDART_INF_F;
 #pragma unroll
-      for (int c = 0; c < kMaxExperts / 32; ++c) {
-        z[c] = lane + 32 * c < E ? __ldg(lr + lane + 32 * c) : -CUDART_INF_F;
-        top = fmaxf(top, z[c]);
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      total = 0.f;
-#pragma unroll
-      for (int c = 0; c < kMaxExperts / 32; ++c) {
-        z[c] = lane + 32 * c < E && top != -CUDART_INF_F ? expf(z[c] - top) : 0.f;
-        total += z[c];
-      }
-      total = reduce_warp(total);
-      v = id >= 0 && top != -CUDART_INF_F ? expf(l - top) : 0.f;
-    } else {
-      top = l;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      if (MODE == MOE_GATING_SOFTMAX_RENORM) {
-        v = id >= 0 && top != -CUDART_INF_F ? expf(l - top) : 0.f;
-        total = reduce_warp(v);
-      } else {
-        v = id >= 0 ? 1.f / (1.f + expf(-l)) : 0.f;
-        total = reduce_warp(v);
-        if (total < 0x1p-64f) {
-          // sigmoids that fp32 is about to lose: e^l is their ratio to 2^-64, as far as 64 bits
-          // hold them (the weights' own rule); beyond, weights and gradients are zero
-          v = id >= 0 && top > -709.f ? expf(l - top) : 0.f;
-          total = reduce_warp(v);
-        }
-      }
-    }
-    const float inv = total == 0.f ? 0.f : 1.f / total;
-    const float r = v * inv;
-    const float D = reduce_warp(id >= 0 ? r * up : 0.f);
-    float g;
-    if (MODE == MOE_GATING_SOFTMAX) g = id >= 0 ? r * up : 0.f;
-    else g = id >= 0 ? r * (up - D) : 0.f;
-    if (MODE == MOE_GATING_SIGMOID_BIAS_RENORM) g *= 1.f / (1.f + expf(l));
-#pragma unroll
-    for (int c = 0; c < kMaxExperts / 32; ++c)
-      row[lane + 32 * c] = MODE == MOE_GATING_SOFTMAX ? -z[c] * inv * D : 0.f;
-    __syncwarp();
-    for (int j = 0; j < k; ++j) {    // (one after the other: an expert may be chosen twice)
-      if (lane == j && id >= 0) row[id] += g;
-      __syncwarp();
-    }
-    for (int e = lane; e < E; e += 32) dl[t * E + e] = scale * row[e];
-    __syncwarp();
+  for (int c = 0; c < kMaxExperts / 32; ++c)
+    z[c] = lane + 32 * c < E ? __ldg(lr + lane + 32 * c) : -CUDART_INF_F;
+  int id = -1;
+  float up = 0.f;
+  if (lane < k) {
+    id = __ldg(ids + (size_t)t * k + lane);
+    up = __ldg(dw + (size_t)t * k + lane);
+    if ((unsigned)id >= (unsigned)E) id = -1;
   }
+#pragma unroll
+  for (int c = 0; c < kMaxExperts / 32; ++c) top = fmaxf(top, z[c]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  float total = 0.f;
+#pragma unroll
+  for (int c = 0; c < kMaxExperts / 32; ++c) {
+    z[c] = lane + 32 * c < E && top != -CUDART_INF_F ? expf(z[c] - top) : 0.f;
+    total += z[c];
+    row[lane + 32 * c] = z[c];
+  }
+  total = reduce_warp(total);
+  const float inv = total == 0.f ? 0.f : 1.f / total;
+  __syncwarp();
+  const float g = id >= 0 ? row[id] * inv * up : 0.f;
+  const float D = reduce_warp(g);
+  __syncwarp();
+#pragma unroll
+  for (int c = 0; c < kMaxExperts / 32; ++c) row[lane + 32 * c] = -scale * (z[c] * inv * D);
+  __syncwarp();
+  add_chosen(row, lane < 8 ? id : -1, scale * g, lane);
+#pragma unroll
+  for (int c = 0; c < kMaxExperts / 32; ++c)
+    if (lane + 32 * c < E) dl[(size_t)t * E + lane + 32 * c] = row[lane + 32 * c];
 }
 
 template <class F>
@@ -329,18 +390,22 @@ int moe_gate_backward(const float* logits, const int32_t* ids, const float* dw, 
   if (T == 0) return MOE_OK;
   MOE_REQUIRE(logits && ids && dw && dlogits && aligned4(logits) && aligned4(ids) &&
               aligned4(dw) && aligned4(dlogits));
-  auto go = [&](auto mode) -> int {
-    MOE_LAUNCH_PDL(gate_backward_kernel<decltype(mode)::value>, dim3(ceil_div(T, kGateBackWarps)),
-                   dim3(kGateBackWarps * 32), 0, (cudaStream_t)stream, logits, ids, dw, T, E, k,
-                   scale, dlogits);
-    MOE_COUNT_LAUNCH();
-    MOE_LAUNCH_CHECK();
-    return MOE_OK;
-  };
-  if (gating == MOE_GATING_SOFTMAX) return go(std::integral_constant<int, MOE_GATING_SOFTMAX>{});
-  if (gating == MOE_GATING_SOFTMAX_RENORM)
-    return go(std::integral_constant<int, MOE_GATING_SOFTMAX_RENORM>{});
-  return go(std::integral_constant<int, MOE_GATING_SIGMOID_BIAS_RENORM>{});
+  cudaStream_t st = (cudaStream_t)stream;
+  const dim3 block(kGateBackWarps * 32);
+  const dim3 four(ceil_div(T, 4 * kGateBackWarps));
+  const bool wide = E % 4 == 0 && aligned16(dlogits);
+  if (gating == MOE_GATING_SOFTMAX)
+    MOE_LAUNCH_PDL(gate_backward_softmax_kernel, dim3(ceil_div(T, kGateBackWarps)), block, 0, st,
+                   logits, ids, dw, T, E, k, scale, dlogits);
+  else if (gating == MOE_GATING_SOFTMAX_RENORM)
+    MOE_LAUNCH_PDL(gate_backward_chosen_kernel<false>, four, block, 0, st, logits, ids, dw, T, E, k,
+                   scale, wide, dlogits);
+  else
+    MOE_LAUNCH_PDL(gate_backward_chosen_kernel<true>, four, block, 0, st, logits, ids, dw, T, E, k,
+                   scale, wide, dlogits);
+  MOE_COUNT_LAUNCH();
+  MOE_LAUNCH_CHECK();
+  return MOE_OK;
 }
 
 }  // extern "C"

@@ -99,11 +99,8 @@ __device__ int active_experts(const GemvArgs& a, GemvSmem& sm) {
   int b = 0, n = 0;
   bool clipped = false;
   if (e < a.E) {
-    int end = a.max_rows;
-    if (a.offsets) {
-      b = __ldg(a.offsets + e);
-      end = __ldg(a.offsets + e + 1);
-    }
+    b = __ldg(a.offsets + e);
+    const int end = __ldg(a.offsets + e + 1);
     const int cb = min(max(b, 0), a.max_rows), ce = min(max(end, 0), a.max_rows);
     clipped = end > b && (cb != b || ce != end);
     b = cb;
@@ -165,16 +162,18 @@ struct GemvItem {
   int e, n0, rb, hi;
 };
 template <int NT>
-__device__ __forceinline__ GemvItem gemv_item(const GemvSmem& sm, long long it, int ntile, int n_act) {
-  const int pass = (int)(it / ntile);
-  int a = 0, b = n_act;                        // the last expert whose passes start at or before it
-  while (b - a > 1) {
-    const int c = (a + b) >> 1;
-    if (sm.passes[c] <= pass) a = c;
-    else b = c;
+__device__ __forceinline__ GemvItem gemv_item(const GemvArgs& a, const GemvSmem& sm, int it, int ntile,
+                                              int n_act) {
+  const int pass = it / ntile, n0 = (it - pass * ntile) * (NT * kGvUnit);
+  if (!a.offsets) return {0, n0, 8 * pass, min(a.max_rows, 8 * pass + 8)};
+  int i = 0, end = n_act;                      // the last expert whose passes start at or before it
+  while (end - i > 1) {
+    const int c = (i + end) >> 1;
+    if (sm.passes[c] <= pass) i = c;
+    else end = c;
   }
-  const int rb = sm.lo[a] + 8 * (pass - sm.passes[a]);
-  return {sm.act[a], (int)(it - (long long)pass * ntile) * (NT * kGvUnit), rb, min(sm.hi[a], rb + 8)};
+  const int rb = sm.lo[i] + 8 * (pass - sm.passes[i]);
+  return {sm.act[i], n0, rb, min(sm.hi[i], rb + 8)};
 }
 
 // G: codes a scale covers; NT: units of an item.
@@ -200,23 +199,30 @@ gemv_int4_kernel(const GemvArgs a, const __grid_constant__ CUtensorMap tm) {
     prefetch_map(&tm);
   }
   pdl_wait();
-  const int n_act = __shfl_sync(0xffffffffu, active_experts(a, sm), 0);
+  int n_act = 1, passes = (a.max_rows + 7) / 8;
+  if (a.offsets) {
+    n_act = __shfl_sync(0xffffffffu, active_experts(a, sm), 0);
+    passes = sm.passes[n_act];
+  } else {
+    if (blockIdx.x == 0 && threadIdx.x == 0) *a.err = 0;
+    __syncwarp();
+  }
   const int ntile = (a.N + NT * kGvUnit - 1) / (NT * kGvUnit);
   const int steps = (a.K + kGvStep - 1) / kGvStep;
-  const long long items = (long long)sm.passes[n_act] * ntile;
+  const int items = passes * ntile;
   // A warp's steps of an item are first, first + 8, ...: dealt out from where the last item's ended.
   auto following = [&](int first) { return (first + kGvWarps - steps % kGvWarps) % kGvWarps; };
 
   // the next box to ask for
-  long long a_it = blockIdx.x;
+  int a_it = blockIdx.x;
   int a_first = warp, a_st = warp, put = 0, place = 0;
   GemvItem ai{0, 0, 0, 0};
-  if (a_it < items) ai = gemv_item<NT>(sm, a_it, ntile, n_act);
+  if (a_it < items) ai = gemv_item<NT>(a, sm, a_it, ntile, n_act);
   auto ask = [&] {
     while (a_st >= steps) {
       a_it += gridDim.x;
       if (a_it >= items) break;
-      ai = gemv_item<NT>(sm, a_it, ntile, n_act);
+      ai = gemv_item<NT>(a, sm, a_it, ntile, n_act);
       a_st = a_first = following(a_first);
     }
     if (a_it >= items) return;
@@ -253,8 +259,9 @@ gemv_int4_kernel(const GemvArgs a, const __grid_constant__ CUtensorMap tm) {
     const int k = f.st * kGvStep + 8 * t;
     xv[c] = __ldg(reinterpret_cast<const uint4*>(f.x + min(k + 32 * c, a.K - 8)));
   };
-  uint32_t rv[NG / 2];
+  uint32_t rvs[NT][NG / 2];
   auto scale_values = [&](const Source& f, int i) {
+    uint32_t(&rv)[NG / 2] = rvs[i];
     const size_t at = f.s + (size_t)((uint32_t)min(16 * i + gr + 8 * (t & 1), f.row) * a.ng);
     const int g0 = f.st * NG;
     if (a.wide) {
@@ -310,15 +317,16 @@ gemv_int4_kernel(const GemvArgs a, const __grid_constant__ CUtensorMap tm) {
   int first = warp;
   bool loaded = false;                         // are the item's first values under way?
   GemvItem next{0, 0, 0, 0};
-  if (blockIdx.x < items) next = gemv_item<NT>(sm, blockIdx.x, ntile, n_act);
-  for (long long it = blockIdx.x; it < items; it += gridDim.x) {
+  if (blockIdx.x < items) next = gemv_item<NT>(a, sm, blockIdx.x, ntile, n_act);
+  for (int it = blockIdx.x; it < items; it += gridDim.x) {
     const GemvItem cur = next;
-    if (it + gridDim.x < items) next = gemv_item<NT>(sm, it + gridDim.x, ntile, n_act);
+    if (it + gridDim.x < items) next = gemv_item<NT>(a, sm, it + gridDim.x, ntile, n_act);
     Source src = source(cur, first);
     if (!loaded && first < steps) {
 #pragma unroll
       for (int c = 0; c < 8; ++c) token_value(src, c);
-      scale_values(src, 0);
+#pragma unroll
+      for (int i = 0; i < NT; ++i) scale_values(src, i);
     }
     first = following(first);
     loaded = false;
@@ -357,9 +365,8 @@ gemv_int4_kernel(const GemvArgs a, const __grid_constant__ CUtensorMap tm) {
       for (int i = 0; i < NT; ++i) {
         uint32_t sz[NG / 2];
 #pragma unroll
-        for (int j = 0; j < NG / 2; ++j) sz[j] = rv[j];
-        if (i + 1 < NT) scale_values(src, i + 1);
-        else scale_values(nx, 0);
+        for (int j = 0; j < NG / 2; ++j) sz[j] = rvs[i][j];
+        scale_values(nx, i);
         uint32_t f0 = 0u, f1 = 0u, zb0 = 0u, zb1 = 0u, w[4];
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
@@ -458,10 +465,10 @@ bool encode_weights(CUtensorMap* m, const uint8_t* w, int E, int N, int K, int r
 }
 
 template <int G, bool ZERO, int NT>
-int launch_gemv(const GemvArgs& a, long long items, const CUtensorMap& tm, cudaStream_t st) {
+int launch_gemv(const GemvArgs& a, int items, const CUtensorMap& tm, cudaStream_t st) {
   auto kernel = gemv_int4_kernel<G, ZERO, NT>;
   MOE_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kGvRing));
-  MOE_LAUNCH_PDL(kernel, dim3((unsigned)std::min<long long>(items, 2LL * sm_count())),
+  MOE_LAUNCH_PDL(kernel, dim3(std::min(items, 2 * sm_count())),
                  dim3(kGvThreads), kGvRing, st, a, tm);
   MOE_COUNT_LAUNCH();
   MOE_LAUNCH_CHECK();
@@ -473,15 +480,16 @@ int launch_gemv(const GemvArgs& a, const uint8_t* w, cudaStream_t st) {
   // passes at most: every expert's last eight token rows may be fewer
   const long long passes = std::min<long long>(a.max_rows, a.E + a.max_rows / 8);
   // the height whose rounds cost the least: its rows, and a step's token values (0.4 of a unit)
-  long long items = 0, best = 0;
-  int nt = 0;
+  long long best = 0;
+  int nt = 0, items = 0;
   for (int n = 1; n <= kGvMaxTile; ++n) {
     const long long c = passes * ceil_div(a.N, n * kGvUnit), slots = 2LL * sm_count();
     const long long cost = (c + slots - 1) / slots * (10 * n + 4);
+    if (c > 0x3fffffff) return MOE_ERR_INVALID_ARG;   // (y alone would not fit on the GPU)
     if (!nt || cost <= best) {
       nt = n;
       best = cost;
-      items = c;
+      items = (int)c;
     }
   }
   CUtensorMap tm;

@@ -20,16 +20,17 @@ namespace moe {
 namespace {
 
 constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32;
-// Slots of a chunk at least.
-constexpr int kSortChunk = 2048;
-constexpr int kSortMaxChunks = 148;
+// One chunk up to this many slots, else chunks of kSortChunk at least.
+constexpr int kSortOne = 8192, kSortChunk = 2048;
+constexpr int kSortMaxChunks = 128;
 
 struct SortPlan {
   int chunk, chunks;
 };
 SortPlan plan_sort(long long n) {
   SortPlan p;
-  p.chunk = (int)std::max<long long>(kSortChunk, (n + kSortMaxChunks - 1) / kSortMaxChunks);
+  p.chunk = n <= kSortOne ? kSortOne
+                          : (int)std::max<long long>(kSortChunk, (n + kSortMaxChunks - 1) / kSortMaxChunks);
   p.chunks = (int)((n + p.chunk - 1) / p.chunk);
   return p;
 }
@@ -76,12 +77,15 @@ sort_rank_kernel(const int32_t* __restrict__ ids, int n, int E, int chunk,
   // slots of each expert in the chunks before this one and in all of them
   const int e = tid & (kMaxExperts - 1), part = tid / kMaxExperts;
   int b = 0, all = 0;
-  if (gridDim.x > 1 && e < E)
-    for (int c = part; c < gridDim.x; c += 4) {
-      const int h = hist[(size_t)c * E + e];
+  if (gridDim.x > 1 && e < E) {
+#pragma unroll
+    for (int i = 0; i < kSortMaxChunks / 4; ++i) {     // (all loads in flight together)
+      const int c = part + 4 * i;
+      const int h = c < gridDim.x ? hist[(size_t)c * E + e] : 0;
       all += h;
       b += c < blockIdx.x ? h : 0;
     }
+  }
   before[part][e] = b;
   total[part][e] = all;
   __syncthreads();
