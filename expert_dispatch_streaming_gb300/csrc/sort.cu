@@ -21,8 +21,8 @@ namespace {
 
 constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32;
 // One chunk up to this many slots, else chunks of kSortChunk at least.
-constexpr int kSortOne = 8192, kSortChunk = 2048;
-constexpr int kSortMaxChunks = 128;
+constexpr int kSortOne = 2560, kSortChunk = 2048;
+constexpr int kSortMaxChunks = 64;
 
 struct SortPlan {
   int chunk, chunks;
@@ -38,11 +38,11 @@ SortPlan plan_sort(long long n) {
 __global__ void __launch_bounds__(kSortThreads)
 sort_histogram_kernel(const int32_t* __restrict__ ids, int n, int E, int chunk,
                       int32_t* __restrict__ hist) {
-  pdl_trigger();
   __shared__ int s[kMaxExperts];
   if (threadIdx.x < kMaxExperts) s[threadIdx.x] = 0;
   __syncthreads();
   pdl_wait();
+  pdl_trigger();   // (after the wait: the ranking kernel may read ids once it runs)
   const int lo = blockIdx.x * chunk, hi = min(n - lo, chunk);
   for (int i = threadIdx.x; i < hi; i += kSortThreads) {
     const int e = __ldg(ids + lo + i);
@@ -52,21 +52,24 @@ sort_histogram_kernel(const int32_t* __restrict__ ids, int n, int E, int chunk,
   if (threadIdx.x < E) hist[(size_t)blockIdx.x * E + threadIdx.x] = s[threadIdx.x];
 }
 
-// hist: [gridDim.x][E] chunk histograms, not read where one chunk holds every slot.
+// hist: [gridDim.x][E] chunk histograms; chained: launched behind sort_histogram_kernel, else one chunk
+// holds every slot.
 __global__ void __launch_bounds__(kSortThreads)
 sort_rank_kernel(const int32_t* __restrict__ ids, int n, int E, int chunk,
                  const int32_t* __restrict__ hist, int32_t* __restrict__ counts,
                  int32_t* __restrict__ offsets, int32_t* __restrict__ pos,
-                 int32_t* __restrict__ src) {
-  __shared__ int base[kSortWarps][kMaxExperts];   // a warp's slots of e, then its next row of e
-  __shared__ int before[4][kMaxExperts], total[4][kMaxExperts];
+                 int32_t* __restrict__ src, bool chained) {
+  constexpr int kParts = kSortThreads / kMaxExperts, kPer = kSortWarps / kParts;
+  __shared__ int base[kSortWarps][kMaxExperts];   // a warp's slots of e, then its next row of e in ...
+  __shared__ int from[kParts][kMaxExperts];       // ... those of eight warps, which start here
+  __shared__ int before[kParts][kMaxExperts], total[kParts][kMaxExperts], own[kParts][kMaxExperts];
   __shared__ int scan[kMaxExperts / 32];
   __shared__ int rows;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_trigger();
   for (int i = tid; i < kSortWarps * kMaxExperts; i += kSortThreads) (&base[0][0])[i] = 0;
   __syncthreads();
-  pdl_wait();
+  if (!chained) pdl_wait();
   const int lo = blockIdx.x * chunk, hi = min(n - lo, chunk);
   const int per = ((chunk + kSortWarps - 1) / kSortWarps + 31) & ~31;
   const int w0 = min(warp * per, hi), w1 = min(w0 + per, hi);
@@ -74,13 +77,14 @@ sort_rank_kernel(const int32_t* __restrict__ ids, int n, int E, int chunk,
     const int e = __ldg(ids + lo + i);
     if ((unsigned)e < (unsigned)E) atomicAdd(&base[warp][e], 1);
   }
+  if (chained) pdl_wait();
   // slots of each expert in the chunks before this one and in all of them
   const int e = tid & (kMaxExperts - 1), part = tid / kMaxExperts;
   int b = 0, all = 0;
-  if (gridDim.x > 1 && e < E) {
+  if (chained && e < E) {
 #pragma unroll
-    for (int i = 0; i < kSortMaxChunks / 4; ++i) {     // (all loads in flight together)
-      const int c = part + 4 * i;
+    for (int i = 0; i < kSortMaxChunks / kParts; ++i) {   // (all loads in flight together)
+      const int c = part + kParts * i;
       const int h = c < gridDim.x ? hist[(size_t)c * E + e] : 0;
       all += h;
       b += c < blockIdx.x ? h : 0;
@@ -89,16 +93,19 @@ sort_rank_kernel(const int32_t* __restrict__ ids, int n, int E, int chunk,
   before[part][e] = b;
   total[part][e] = all;
   __syncthreads();
+  int run = 0;
+#pragma unroll
+  for (int w = part * kPer; w < (part + 1) * kPer; ++w) {
+    const int h = base[w][e];
+    base[w][e] = run;
+    run += h;
+  }
+  own[part][e] = run;
+  __syncthreads();
   int mine = 0, inc = 0;
   if (tid < kMaxExperts) {
-    int run = 0;
-#pragma unroll 8
-    for (int w = 0; w < kSortWarps; ++w) {
-      const int h = base[w][e];
-      base[w][e] = run;
-      run += h;
-    }
-    mine = gridDim.x > 1 ? total[0][e] + total[1][e] + total[2][e] + total[3][e] : run;
+#pragma unroll
+    for (int p = 0; p < kParts; ++p) mine += chained ? total[p][e] : own[p][e];
     inc = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -118,7 +125,13 @@ sort_rank_kernel(const int32_t* __restrict__ ids, int n, int E, int chunk,
       offsets[e] = off;
       if (e == E - 1) offsets[E] = off + mine;
     }
-    before[0][e] = off + before[0][e] + before[1][e] + before[2][e] + before[3][e];
+#pragma unroll
+    for (int p = 0; p < kParts; ++p) off += before[p][e];
+#pragma unroll
+    for (int p = 0; p < kParts; ++p) {
+      from[p][e] = off;
+      off += own[p][e];
+    }
   }
   __syncthreads();
   for (int i0 = w0; i0 < w1; i0 += 32) {
@@ -133,7 +146,7 @@ sort_rank_kernel(const int32_t* __restrict__ ids, int n, int E, int chunk,
     if (has && rank == 0) base[warp][id] = first + __popc(same);
     __syncwarp();
     if (i < w1) {
-      const int p = has ? before[0][id] + first + rank : -1;
+      const int p = has ? from[warp / kPer][id] + first + rank : -1;
       pos[lo + i] = p;
       if (has) src[p] = lo + i;
     }
@@ -180,7 +193,7 @@ int moe_sort_tokens(const int32_t* ids, int T, int E, int k, int32_t* counts, in
     MOE_LAUNCH_CHECK();
   }
   MOE_LAUNCH_NEXT(p.chunks > 1, sort_rank_kernel, dim3(std::max(1, p.chunks)), dim3(kSortThreads),
-                  0, st, ids, n, E, p.chunk, hist, counts, offsets, pos, src);
+                  0, st, ids, n, E, p.chunk, hist, counts, offsets, pos, src, p.chunks > 1);
   MOE_COUNT_LAUNCH();
   MOE_LAUNCH_CHECK();
   return MOE_OK;
