@@ -27,22 +27,141 @@
 // for all its weight rows.  Each warp has a ring of its own in shared memory, filled by TMA
 // (boxes of the item's rows x 128 bytes, swizzled, so that the lanes' words lie in different
 // banks) and running on from one item to the next; token values and scales are loaded ahead of their
-// use.  The warps' sums are added in warp order in shared memory.  More than eight token rows an
-// expert, on average, take gemv_int4_rows.cu's kernel.
-#include "gemv_int4.cuh"
+// use.  The warps' sums are added in warp order in shared memory.
+#include "common.cuh"
+#include "route.cuh"
+#include "tc_ptx.cuh"
+
+#include <type_traits>
 
 namespace moe {
 namespace {
 
+constexpr int kGvWarps = 8, kGvThreads = kGvWarps * 32;
 constexpr int kGvUnit = 16;              // weight rows of a product
 constexpr int kGvMaxTile = 3;            // units of an item at most
+constexpr int kGvStep = 256;             // codes of K of a box (128 bytes a row)
 constexpr int kGvWarpRing = 12288;       // bytes of a warp's ring: 6, 3 or 2 boxes
 constexpr int kGvRing = kGvWarps * kGvWarpRing + 1024;
+constexpr int kGvErrWait = 6;            // error word: a wait for weights ran out of time
+
+struct GemvArgs {
+  const uint16_t* x;
+  const uint16_t* s;
+  const uint8_t* z;
+  const int32_t* offsets;
+  int E, N, K, ng, max_rows;
+  bool f32, wide;                              // wide: a step's scales of a row are one aligned load
+  void* y;
+  int32_t* err;
+};
+
+__device__ __forceinline__ void mma_bf16(float* d, uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The four pairs of a code word as (q - z) 2^-6; nz: -z 2^-6 in both halves.
+__device__ __forceinline__ void code_pairs(uint32_t w, uint32_t nz, uint32_t (&p)[4]) {
+  const uint32_t h = w >> 8;
+  const uint32_t v[4] = {w & 0x000F000Fu, w & 0x00F000F0u, h & 0x000F000Fu, h & 0x00F000F0u};
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;"
+        : "=r"(p[i])
+        : "r"(v[i]), "r"(i & 1 ? 0x7D007D00u : 0x7F007F00u), "r"(nz));
+}
+// -z 2^-6 in both halves, z = byte I of `zeros`, 0..127: 128 + z by its bits, then an exact fma.
+template <int I>
+__device__ __forceinline__ uint32_t zero_pair(uint32_t zeros) {
+  const uint32_t v = __byte_perm(zeros, 0x43434343u, 0x4040 | (I << 8) | I);
+  uint32_t d;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(v), "r"(0xBC80BC80u), "r"(0x40004000u));
+  return d;
+}
+
 struct GemvSmem {
   uint64_t full[kGvWarps][6];
   float red[kGvWarps][4][kGvMaxTile * kGvUnit + 4];   // the warps' sums of four token rows
-  GemvExperts ex;
+  int lo[kMaxExperts], hi[kMaxExperts];        // token rows of the experts that have some
+  int passes[kMaxExperts + 1];                 // eights of token rows of the experts before
+  int16_t act[kMaxExperts];
+  int wsum[2][kGvWarps];
 };
+
+// The experts with rows, ascending, with their ranges; returns how many there are.  CTA 0 records in
+// the error word whether a range was clipped.
+__device__ int active_experts(const GemvArgs& a, GemvSmem& sm) {
+  const int e = threadIdx.x, lane = e & 31, warp = e >> 5;
+  int b = 0, n = 0;
+  bool clipped = false;
+  if (e < a.E) {
+    b = __ldg(a.offsets + e);
+    const int end = __ldg(a.offsets + e + 1);
+    const int cb = min(max(b, 0), a.max_rows), ce = min(max(end, 0), a.max_rows);
+    clipped = end > b && (cb != b || ce != end);
+    b = cb;
+    n = max(ce - cb, 0);
+  }
+  const int mine = (n + 7) / 8;
+  int before = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, before, o);
+    if (lane >= o) before += v;
+  }
+  const unsigned m = __ballot_sync(0xffffffffu, n > 0);
+  if (lane == 31) {
+    sm.wsum[0][warp] = __popc(m);
+    sm.wsum[1][warp] = before;
+  }
+  before -= mine;
+  const int any = __syncthreads_or(clipped);
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.err = any ? 8 : 0;
+  int at = __popc(m & ((1u << lane) - 1u)), total = 0, all = 0;
+#pragma unroll
+  for (int i = 0; i < kGvWarps; ++i) {
+    at += i < warp ? sm.wsum[0][i] : 0;
+    before += i < warp ? sm.wsum[1][i] : 0;
+    total += sm.wsum[0][i];
+    all += sm.wsum[1][i];
+  }
+  if (n > 0) {
+    sm.act[at] = (int16_t)e;
+    sm.lo[at] = b;
+    sm.hi[at] = b + n;
+    sm.passes[at] = before;
+  }
+  if (threadIdx.x == 0) sm.passes[total] = all;
+  __syncthreads();
+  return total;
+}
+
+__device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2,
+                                       uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, "
+      "{%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar))
+      : "memory");
+}
+
+
+// The words of four 8 x 16-byte blocks: a lane gets word t of row gr of each.
+__device__ __forceinline__ void load_words(uint32_t (&w)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+               : "r"(addr)
+               : "memory");
+}
+// A token row's eight values in the order of a word's pairs: (0, 4), (1, 5), (2, 6), (3, 7).
+__device__ __forceinline__ uint4 pair_order(const uint4& v) {
+  return make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632),
+                    __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632));
+}
 
 // An item: weight rows from n0 on of expert e against token rows [rb, hi) (at most eight).
 struct GemvItem {
@@ -53,9 +172,14 @@ __device__ __forceinline__ GemvItem gemv_item(const GemvArgs& a, const GemvSmem&
                                               int n_act) {
   const int pass = it / ntile, n0 = (it - pass * ntile) * (NT * kGvUnit);
   if (!a.offsets) return {0, n0, 8 * pass, min(a.max_rows, 8 * pass + 8)};
-  const int i = find_expert(sm.ex.passes, n_act, pass);
-  const int rb = sm.ex.lo[i] + 8 * (pass - sm.ex.passes[i]);
-  return {sm.ex.act[i], n0, rb, min(sm.ex.hi[i], rb + 8)};
+  int i = 0, end = n_act;                      // the last expert whose passes start at or before it
+  while (end - i > 1) {
+    const int c = (i + end) >> 1;
+    if (sm.passes[c] <= pass) i = c;
+    else end = c;
+  }
+  const int rb = sm.lo[i] + 8 * (pass - sm.passes[i]);
+  return {sm.act[i], n0, rb, min(sm.hi[i], rb + 8)};
 }
 
 // G: codes a scale covers; NT: units of an item.
@@ -83,8 +207,8 @@ gemv_int4_kernel(const GemvArgs a, const __grid_constant__ CUtensorMap tm) {
   pdl_wait();
   int n_act = 1, passes = (a.max_rows + 7) / 8;
   if (a.offsets) {
-    n_act = __shfl_sync(0xffffffffu, active_experts(a, sm.ex, 1, true), 0);
-    passes = sm.ex.passes[n_act];
+    n_act = __shfl_sync(0xffffffffu, active_experts(a, sm), 0);
+    passes = sm.passes[n_act];
   } else {
     if (blockIdx.x == 0 && threadIdx.x == 0) *a.err = 0;
     __syncwarp();
@@ -326,6 +450,23 @@ gemv_int4_kernel(const GemvArgs a, const __grid_constant__ CUtensorMap tm) {
       warp_wait(full + i % kBoxes, (i / kBoxes) & 1, a.err, kGvErrWait);
 }
 
+bool valid_gemv_shape(int E, int N, int K, int max_rows) {
+  return E > 0 && E <= kMaxExperts && N > 0 && K > 0 && K % 32 == 0 && max_rows >= 0 &&
+         N <= (1 << 24) && K <= (1 << 24) && (long long)E * N < (1LL << 31);
+}
+
+bool encode_weights(CUtensorMap* m, const uint8_t* w, int E, int N, int K, int rows) {
+  const cuuint64_t row = (cuuint64_t)K / 2;
+  const cuuint64_t dims[3] = {row, (cuuint64_t)N, (cuuint64_t)E};
+  const cuuint64_t strides[2] = {row, row * N};
+  const cuuint32_t box[3] = {kGvStep / 2, (cuuint32_t)rows, 1}, step[3] = {1, 1, 1};
+  auto enc = encode_fn();
+  return enc && enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(w), dims, strides, box,
+                    step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int G, bool ZERO, int NT>
 int launch_gemv(const GemvArgs& a, int items, const CUtensorMap& tm, cudaStream_t st) {
   auto kernel = gemv_int4_kernel<G, ZERO, NT>;
@@ -361,11 +502,6 @@ int launch_gemv(const GemvArgs& a, const uint8_t* w, cudaStream_t st) {
   return launch_gemv<G, ZERO, 3>(a, items, tm, st);
 }
 
-bool valid_gemv_shape(int E, int N, int K, int max_rows) {
-  return E > 0 && E <= kMaxExperts && N > 0 && K > 0 && K % 32 == 0 && max_rows >= 0 &&
-         N <= (1 << 24) && K <= (1 << 24) && (long long)E * N < (1LL << 31);
-}
-
 }  // namespace
 }  // namespace moe
 
@@ -374,7 +510,7 @@ using namespace moe;
 extern "C" {
 
 size_t moe_grouped_gemv_int4_workspace_size(int max_rows, int E, int N, int K) {
-  return valid_gemv_shape(E, N, K, max_rows) ? 256 + gemv_packed_bytes(max_rows, E, K) : 0;
+  return valid_gemv_shape(E, N, K, max_rows) ? 256 : 0;
 }
 
 int moe_grouped_gemv_int4(const uint16_t* x, const uint8_t* w, const uint16_t* w_scale,
@@ -393,8 +529,6 @@ int moe_grouped_gemv_int4(const uint16_t* x, const uint8_t* w, const uint16_t* w
                    out_f32 != 0, K % kGvStep == 0 && aligned16(w_scale) && aligned16(w_zero), y,
                    static_cast<int32_t*>(ws)};
   cudaStream_t st = (cudaStream_t)stream;
-  if (gemv_packed_bytes(max_rows, E, K))
-    return launch_gemv_rows(a, w, group, static_cast<char*>(ws) + 256, st);
   if (group == 32) return w_zero ? launch_gemv<32, true>(a, w, st) : launch_gemv<32, false>(a, w, st);
   if (group == 64) return w_zero ? launch_gemv<64, true>(a, w, st) : launch_gemv<64, false>(a, w, st);
   return w_zero ? launch_gemv<128, true>(a, w, st) : launch_gemv<128, false>(a, w, st);
