@@ -32,11 +32,13 @@ __device__ __forceinline__ float reduce_warp(float v) {
 // ------------------------------------------------------------------------------ permute
 // The rows x_perm[pos[t][j]] are copies of x[t], so
 //   dx[t] = sum_{j<k} dx_perm[pos[t][j]]  (+ add[t])
-// in fp32, j in order, rounded once.  Block (c, t): elements [1024 c, 1024 c + 1024) of token t.
+// in fp32, j in order, rounded once.  Block (c, t): elements [1024 c, 1024 c + 1024) of token t, one
+// 16-byte piece of each of the k rows a thread.  Reading the rows bounds it: 8192 tokens of eight rows
+// of 7168 take 158 us, the 1057 MB it needs at 99% of the copy bandwidth.
 template <int K, bool F32>
 __global__ void __launch_bounds__(kBackThreads)
 permute_backward_kernel(const uint16_t* __restrict__ dxp, const int32_t* __restrict__ pos,
-                        const uint16_t* __restrict__ add, int T, int H, void* __restrict__ dx) {
+                        const uint16_t* add, int T, int H, void* dx) {   // (dx may be add)
   pdl_trigger();
   pdl_wait();
   const int v = blockIdx.x * kBackThreads + threadIdx.x;
@@ -50,7 +52,7 @@ permute_backward_kernel(const uint16_t* __restrict__ dxp, const int32_t* __restr
       q[j] = make_uint4(0u, 0u, 0u, 0u);
       if ((unsigned)p < rows) q[j] = __ldg(reinterpret_cast<const uint4*>(dxp + (size_t)p * H) + v);
     }
-    if (add) a = __ldg(reinterpret_cast<const uint4*>(add + (size_t)t * H) + v);
+    if (add) a = reinterpret_cast<const uint4*>(add + (size_t)t * H)[v];
     float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, f[8];
 #pragma unroll
     for (int j = 0; j < K; ++j) {
@@ -78,7 +80,9 @@ permute_backward_kernel(const uint16_t* __restrict__ dxp, const int32_t* __restr
 //   dy_perm[pos[t][j]] = w[t][j] dout[t],   dw[t][j] = <dout[t], y_perm[pos[t][j]]>,
 //   dshared[t] = g_t dout[t],               dg_t = <dout[t], shared[t]>
 // A CTA takes one token: a thread reads a 16-byte vector of dout[t] and of the k rows, writes the
-// k scaled vectors and keeps k + 1 partial dot products, which the CTA adds in a fixed order.
+// k scaled vectors and keeps k + 1 partial dot products, which the CTA adds in a fixed order: one
+// pass over y_perm and dy_perm, which bound it.  8192 tokens of eight rows of 7168 and a shared expert
+// take 316 us, the 2115 MB it needs at 99% of the copy bandwidth.
 constexpr int kCombineBackThreads = 256;
 
 template <int K>
@@ -207,11 +211,11 @@ gate_backward_chosen_kernel(const float* __restrict__ logits, const int32_t* __r
   pdl_trigger();
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, j = lane & 7;
-  const int t0 = (blockIdx.x * kGateBackWarps + warp) * 4, t = t0 + (lane >> 3);
-  if (t0 >= T) return;
+  const unsigned t0 = (blockIdx.x * kGateBackWarps + warp) * 4, t = t0 + (lane >> 3), end = T;
+  if (t0 >= end) return;
   int id = -1;
   float up = 0.f, l = -CUDART_INF_F;
-  if (t < T && j < k) {
+  if (t < end && j < k) {
     id = __ldg(ids + (size_t)t * k + j);
     const float d = __ldg(dw + (size_t)t * k + j);
     if ((unsigned)id < (unsigned)E) {
@@ -223,7 +227,7 @@ gate_backward_chosen_kernel(const float* __restrict__ logits, const int32_t* __r
   }
   // four rows of E floats start on a 16-byte boundary
   float* rows = dl + (size_t)t0 * E;
-  const int n = min(4, T - t0) * E;
+  const int n = (int)min(4u, end - t0) * E;
   for (int i = lane; i < n / 4; i += 32)
     reinterpret_cast<float4*>(rows)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
   if (lane < (n & 3)) rows[(n & ~3) + lane] = 0.f;
@@ -262,9 +266,9 @@ gate_backward_softmax_kernel(const float* __restrict__ logits, const int32_t* __
   __shared__ float row_s[kGateBackWarps][kMaxExperts];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   float* row = row_s[warp];
-  const int t = blockIdx.x * kGateBackWarps + warp;
+  const unsigned t = blockIdx.x * kGateBackWarps + warp;
   pdl_wait();
-  if (t >= T) return;
+  if (t >= (unsigned)T) return;
   const float* lr = logits + (size_t)t * E;
   float z[kMaxExperts / 32], top = -CUDART_INF_F;
 #pragma unroll

@@ -42,7 +42,7 @@ combine_kernel(const uint16_t* __restrict__ y, const int32_t* __restrict__ pos,
 #pragma unroll
   for (int j = 0; j < K; ++j) {
     q[j] = make_uint4(0u, 0u, 0u, 0u);
-    if ((unsigned)pj[j] < (unsigned)(T * K))
+    if ((unsigned)pj[j] < (unsigned)T * K)
       q[j] = __ldg(reinterpret_cast<const uint4*>(y + (size_t)pj[j] * H) + v);
     else
       wj[j] = 0.f;   // a slot without a row, whatever its weight
@@ -121,7 +121,7 @@ combine_norm_kernel(const uint16_t* __restrict__ y, const int32_t* __restrict__ 
       if (v >= nv) break;
       float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
       for (int j = 0; j < k; ++j) {
-        if ((unsigned)pj[j] >= (unsigned)(T * k)) continue;   // a slot without a row
+        if ((unsigned)pj[j] >= (unsigned)T * k) continue;   // a slot without a row
         const uint4 q = __ldg(reinterpret_cast<const uint4*>(y + (size_t)pj[j] * H) + v);
         const uint32_t qw[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll

@@ -28,6 +28,15 @@
 // (boxes of the item's rows x 128 bytes, swizzled, so that the lanes' words lie in different
 // banks) and running on from one item to the next; token values and scales are loaded ahead of their
 // use.  The warps' sums are added in warp order in shared memory.
+//
+// Measured (the floor is what has to be read and written at the copy bandwidth): 14336 x 14336 codes,
+// groups of 128, one token 23.7 us (floor 15.6; the same boxes loaded and not used 18.5), eight tokens
+// 27; 8 of 256 experts of 4096 x 7168 30 us (17.9), 64 tokens on most of the 256 600 us (414); 4096 x
+// 7168, one token, 8 us, of which launch, first loads and the last sums are 6.  Turning codes to bf16
+// bounds the large ones: 144 of about 280 instructions for 4096 codes, with the issue slots 60% busy.
+// More than eight token rows are passes side by side: 16 rows a pass need registers that 16 warps a SM
+// do not have, and a kernel for 64, codes turned once, won (1.1 to 1.6 times) only from 33 rows and
+// 4096 weight rows on.
 #include "common.cuh"
 #include "route.cuh"
 #include "tc_ptx.cuh"
@@ -39,7 +48,7 @@ namespace {
 
 constexpr int kGvWarps = 8, kGvThreads = kGvWarps * 32;
 constexpr int kGvUnit = 16;              // weight rows of a product
-constexpr int kGvMaxTile = 3;            // units of an item at most
+constexpr int kGvMaxTile = 3;            // units of an item at most (two boxes of four do not fit)
 constexpr int kGvStep = 256;             // codes of K of a box (128 bytes a row)
 constexpr int kGvWarpRing = 12288;       // bytes of a warp's ring: 6, 3 or 2 boxes
 constexpr int kGvRing = kGvWarps * kGvWarpRing + 1024;
@@ -261,9 +270,16 @@ gemv_int4_kernel(const GemvArgs a, const __grid_constant__ CUtensorMap tm) {
                   a.N - 1 - i.n0, st};
   };
   uint4 xv[8];
-  auto token_value = [&](const Source& f, int c) {
+  auto token_values = [&](const Source& f) {
     const int k = f.st * kGvStep + 8 * t;
-    xv[c] = __ldg(reinterpret_cast<const uint4*>(f.x + min(k + 32 * c, a.K - 8)));
+    if ((f.st + 1) * kGvStep <= a.K) {
+#pragma unroll
+      for (int c = 0; c < 8; ++c) xv[c] = __ldg(reinterpret_cast<const uint4*>(f.x + k) + 4 * c);
+    } else {
+#pragma unroll
+      for (int c = 0; c < 8; ++c)
+        xv[c] = __ldg(reinterpret_cast<const uint4*>(f.x + min(k + 32 * c, a.K - 8)));
+    }
   };
   uint32_t rvs[NT][NG / 2];
   auto scale_values = [&](const Source& f, int i) {
@@ -329,8 +345,7 @@ gemv_int4_kernel(const GemvArgs a, const __grid_constant__ CUtensorMap tm) {
     if (it + gridDim.x < items) next = gemv_item<NT>(a, sm, it + gridDim.x, ntile, n_act);
     Source src = source(cur, first);
     if (!loaded && first < steps) {
-#pragma unroll
-      for (int c = 0; c < 8; ++c) token_value(src, c);
+      token_values(src);
 #pragma unroll
       for (int i = 0; i < NT; ++i) scale_values(src, i);
     }
@@ -398,7 +413,6 @@ gemv_int4_kernel(const GemvArgs a, const __grid_constant__ CUtensorMap tm) {
             code_pairs(w[2 * (ch & 1) + 1], z1, q);
             mma_bf16(d, p[0], q[0], p[1], q[1], xv[ch].x, xv[ch].y);
             mma_bf16(d, p[2], q[2], p[3], q[3], xv[ch].z, xv[ch].w);
-            if (i + 1 == NT) token_value(nx, ch);
           }
           const float s0 = __uint_as_float(g % 2 ? f0 & 0xFFFF0000u : f0 << 16);
           const float s1 = __uint_as_float(g % 2 ? f1 & 0xFFFF0000u : f1 << 16);
@@ -408,6 +422,7 @@ gemv_int4_kernel(const GemvArgs a, const __grid_constant__ CUtensorMap tm) {
           acc[i][3] = fmaf(s1, d[3], acc[i][3]);
         }
       }
+      token_values(nx);
       ++got;
       if (++slot == kBoxes) {
         slot = 0;
@@ -482,12 +497,13 @@ template <int G, bool ZERO>
 int launch_gemv(const GemvArgs& a, const uint8_t* w, cudaStream_t st) {
   // passes at most: every expert's last eight token rows may be fewer
   const long long passes = std::min<long long>(a.max_rows, a.E + a.max_rows / 8);
-  // the height whose rounds cost the least: its rows, and a step's token values (0.4 of a unit)
+  // the height whose rounds cost the least: its rows, and what a step costs beside them (about one unit:
+  // 602, 680 and 952 us with 48, 32 and 16 rows for 64 tokens on 256 experts of 4096 x 7168)
   long long best = 0;
   int nt = 0, items = 0;
   for (int n = 1; n <= kGvMaxTile; ++n) {
     const long long c = passes * ceil_div(a.N, n * kGvUnit), slots = 2LL * sm_count();
-    const long long cost = (c + slots - 1) / slots * (10 * n + 4);
+    const long long cost = (c + slots - 1) / slots * (n + 1);
     if (c > 0x3fffffff) return MOE_ERR_INVALID_ARG;   // (y alone would not fit on the GPU)
     if (!nt || cost <= best) {
       nt = n;

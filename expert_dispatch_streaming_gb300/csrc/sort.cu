@@ -12,7 +12,8 @@
 // histograms in shared memory) and of the warp itself (__match_any_sync, 32 slots at a time).  No
 // result depends on the order of atomics: they only count.
 // It needs 12 bytes a slot (id in, pos and src out), so a call is bound by its launches and the
-// chain of steps within them.
+// chain of steps within them: one token 2.4 us, 32768 tokens of 8 slots on 256 experts 9.5 us (3 MB).
+// One launch with a barrier across the CTAs instead of the two took 10.2.
 #include "common.cuh"
 #include "route.cuh"
 
@@ -20,7 +21,9 @@ namespace moe {
 namespace {
 
 constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32;
-// One chunk up to this many slots, else chunks of kSortChunk at least.
+// One chunk up to this many slots, else chunks of kSortChunk at least (8192 slots: one CTA 11.4 us, four
+// 7.3), and at most kSortMaxChunks, whose histograms every CTA reads (262144 slots: 128 chunks 12.0 us,
+// 64 9.5, 48 10.9).
 constexpr int kSortOne = 2560, kSortChunk = 2048;
 constexpr int kSortMaxChunks = 64;
 

@@ -456,9 +456,11 @@ int moe_grouped_swiglu_fp8(const uint8_t* xq, const float* x_scale, const int32_
  *           error 8 is recorded (moe_workspace_error)
  *  ws       device scratch of moe_grouped_gemv_int4_workspace_size(max_rows, E, N, K) bytes,
  *           256-byte aligned
- * Limits: 1 <= E <= 256, N >= 1, K a multiple of 32; x, w, y 16-byte, w_scale 2-byte aligned.  Any
- * number of rows is computed; from some dozens per expert on the products bound it, not the reads.
- * A NaN or infinite product reaches the outputs of its token row and weight row only.
+ * Limits: 1 <= E <= 256, N >= 1, K a multiple of 32; x, w, y 16-byte, w_scale 2-byte aligned (16-byte
+ * aligned scales and zero points and K a multiple of 256 take wide loads).  Any number of rows is
+ * computed, eight of an expert at a time, each eight reading its weights.
+ * A NaN or an infinity in a token row or a scale reaches the outputs of that token row or weight row
+ * only.
  * "Running 35B MoE Models on 8GB GPUs ...", "Technical Insight" names 4-bit checkpoints; the layout
  * is the row-major one with zero points that such checkpoints are published in, not a bundle's. */
 size_t moe_grouped_gemv_int4_workspace_size(int max_rows, int E, int N, int K);
@@ -493,7 +495,8 @@ int moe_combine(const uint16_t* y_perm, const int32_t* pos, const float* w, int 
  * moe_permute_backward -- of moe_permute:  dx[t] = sum_{j<k} dx_perm[pos[t][j]] + add[t], j in order.
  *  dx_perm device [T*k][H] bf16; add device [T][H] bf16 or NULL (a gradient that reaches x on
  *  another way: the residual, the shared expert, the router); dx device [T][H], bf16 (out_f32 = 0,
- *  rounded once) or fp32 (out_f32 = 1).  H a multiple of 8; dx_perm, add, dx 16-byte aligned; k <= 8. */
+ *  rounded once) or fp32 (out_f32 = 1); a bf16 dx may be `add` itself.  H a multiple of 8; dx_perm,
+ *  add, dx 16-byte aligned; k <= 8. */
 int moe_permute_backward(const uint16_t* dx_perm, const int32_t* pos, const uint16_t* add, int T,
                          int k, int H, int out_f32, void* dx, void* stream);
 
@@ -525,7 +528,7 @@ int moe_combine_backward(const uint16_t* dout, const uint16_t* y_perm, const int
  * An id outside [0, E) is a slot without an expert: its dw is not read and it is in no sum.  An id
  * that stands twice in a row counts as two slots.  A token whose weights are all zero (every score
  * open to it -infinity, see moe_route_topk_grouped) gets zero gradients.
- * Limits: E <= 256, k <= min(E, 8). */
+ * Limits: E <= 256, k <= min(E, 8); dlogits 16-byte aligned. */
 int moe_gate_backward(const float* logits, const int32_t* ids, const float* dw, int T, int E,
                       int k, int gating, float scale, float* dlogits, void* stream);
 

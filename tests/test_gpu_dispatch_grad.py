@@ -176,6 +176,19 @@ def test_permute_backward(moe, T, E, k, H, drop, out, add):
     assert torch.all(dx[T] == 5.0)
 
 
+def test_permute_backward_in_place(moe):
+    """dx in the buffer of the gradient that is added: the result of separate buffers."""
+    T, E, k, H = 70, 16, 4, 520
+    g = gen(31)
+    _, _, pos, _ = dispatch(moe, T, E, k, 0.2, 6)
+    d = torch.randn((T * k, H), generator=g, device="cuda").to(torch.bfloat16)
+    a = torch.randn((T, H), generator=g, device="cuda").to(torch.bfloat16)
+    dx = torch.empty_like(a)
+    moe.moe_permute_backward(d, pos, a, T, k, H, "bf16", dx)
+    moe.moe_permute_backward(d, pos, a, T, k, H, "bf16", a)
+    assert torch.equal(a, dx)
+
+
 @pytest.mark.parametrize("T,E,k,H", SHAPES)
 @pytest.mark.parametrize("drop", [0.0, 0.4, 1.0])
 @pytest.mark.parametrize("shared", ["none", "plain", "gated"])
@@ -382,6 +395,51 @@ def test_gate_backward_differences(moe):
             # weight (its derivatives are products of weights), and by the weights' fp32 roundings
             tol = 1.5 * dw.abs().double().sum(1) * (step ** 2 / 6 + 64 * 2.0 ** -24 / step)
             assert torch.all((got[:, e] - num).abs() <= tol)
+
+
+def test_programmatic_launches(moe):
+    """The chain with every kernel allowed to start beside its predecessor's end: the results of plain
+    launches, to the bit, call after call on the same buffers."""
+    T, E, k, H = 3001, 64, 8, 256
+    i32 = dict(dtype=torch.int32, device="cuda")
+    g = gen(40)
+    sets = []
+    for seed in range(3):
+        ids = torch.from_numpy(make_ids(T, E, k, 0.1, seed)).cuda()
+        x = torch.randn((T, H), generator=g, device="cuda").to(torch.bfloat16)
+        sets.append((ids, x, torch.rand((T, k), generator=g, device="cuda")))
+    nb = moe.moe_sort_tokens_workspace_size(T, E, k)
+    ws = torch.empty(nb, dtype=torch.uint8, device="cuda")
+    b = dict(ids=torch.empty((T, k), **i32), counts=torch.empty(E, **i32),
+             offsets=torch.empty(E + 1, **i32), pos=torch.empty((T, k), **i32),
+             src=torch.empty(T * k, **i32),
+             xp=torch.empty((T * k, H), dtype=torch.bfloat16, device="cuda"),
+             out=torch.empty((T, H), dtype=torch.bfloat16, device="cuda"),
+             dy=torch.zeros((T * k, H), dtype=torch.bfloat16, device="cuda"),
+             dw=torch.empty((T, k), device="cuda"), dx=torch.empty((T, H), device="cuda"),
+             z=torch.randn((T, E), generator=g, device="cuda"), dz=torch.empty((T, E), device="cuda"))
+
+    def chain(ids, x, w):
+        b["ids"].copy_(ids)
+        moe.moe_sort_tokens(b["ids"], T, E, k, b["counts"], b["offsets"], b["pos"], b["src"], ws, nb)
+        moe.moe_permute(x, b["src"], T, k, H, b["xp"])
+        moe.moe_combine(b["xp"], b["pos"], w, T, k, H, None, None, None, b["out"])
+        moe.moe_combine_backward(b["out"], b["xp"], b["pos"], w, T, k, H, None, None, b["dy"], b["dw"])
+        moe.moe_gate_backward(b["z"], b["ids"], b["dw"], T, E, k, "softmax_renorm", 1.0, b["dz"])
+        moe.moe_permute_backward(b["dy"], b["pos"], None, T, k, H, "fp32", b["dx"])
+        return {n: v.clone() for n, v in b.items()}
+
+    plain = [chain(*s) for s in sets]
+    moe.set_pdl(True)
+    try:
+        for _ in range(3):
+            for s, want in zip(sets, plain):
+                got = chain(*s)
+                for n in want:
+                    if n != "dy":        # (its last rows are the calls' before)
+                        assert torch.equal(got[n], want[n]), n
+    finally:
+        moe.set_pdl(False)
 
 
 def test_captured_training_step(moe):

@@ -106,6 +106,24 @@ def test_gemv_rows_do_not_mix(moe, group):  # noqa: F811
     assert torch.equal(got[~bad], ref[~bad])
 
 
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_gemv_unaligned_scales(moe, group):  # noqa: F811
+    """Scales and zero points that start on no 16-byte boundary: the aligned call's result, to the bit."""
+    counts, N, K = [1, 5], 70, 768
+    g = gen(group)
+    w, s, z = weights(g, 2, N, K, group, True)
+    x = torch.randn((6, K), generator=g, device="cuda").to(torch.bfloat16)
+    off = torch.tensor([0, 1, 6], dtype=torch.int32, device="cuda")
+    ref, _ = run(moe, x, w, s, z, off, group, 6, "fp32", N, K, 2)
+    check(x, w, s, z, counts, group, "fp32", ref)
+    s2 = torch.empty(s.numel() + 1, dtype=s.dtype, device="cuda")[1:].copy_(s.view(-1))
+    z2 = torch.empty(z.numel() + 3, dtype=z.dtype, device="cuda")[3:].copy_(z.view(-1))
+    assert s2.data_ptr() % 16 == 2 and z2.data_ptr() % 16 == 3
+    for a, b in ((s2, z), (s, z2), (s2, z2)):
+        got, _ = run(moe, x, w, a, b, off, group, 6, "fp32", N, K, 2)
+        assert torch.equal(got, ref)
+
+
 def test_gemv_all_zero_points_and_codes(moe):  # noqa: F811
     """Every code against every documented zero point: the value is exact."""
     N, K = 16, 32
