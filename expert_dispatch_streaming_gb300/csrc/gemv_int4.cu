@@ -249,7 +249,6 @@ gemv_int4_kernel(const GemvArgs a, const __grid_constant__ CUtensorMap tm) {
     place = place + 1 == kBoxes ? 0 : place + 1;
     a_st += kGvWarps;
   };
-  for (int i = 0; i < kBoxes; ++i) ask();
   int got = 0, dead = -1;                      // boxes used; the first that did not come in time
   int slot = 0;
   uint32_t phase = 0;
@@ -337,9 +336,18 @@ gemv_int4_kernel(const GemvArgs a, const __grid_constant__ CUtensorMap tm) {
     wa[c] = ring + (lane & 15) * 128 + (((2 * c + (lane >> 4)) ^ (lane & 7)) << 4);
 
   int first = warp;
-  bool loaded = false;                         // are the item's first values under way?
-  GemvItem next{0, 0, 0, 0};
-  if (blockIdx.x < items) next = gemv_item<NT>(a, sm, blockIdx.x, ntile, n_act);
+  GemvItem next = ai;
+  // The first item's first values ahead of the first boxes (one token on 4096 x 7168 8.8 -> 8.5 us), but
+  // where that costs more registers than there are.
+  constexpr bool kEarly = NT < 3 || !ZERO;
+  bool loaded = kEarly && blockIdx.x < items && first < steps;   // are the item's first values under way?
+  if (loaded) {
+    const Source src = source(next, first);
+#pragma unroll
+    for (int i = 0; i < NT; ++i) scale_values(src, i);
+    token_values(src);
+  }
+  for (int i = 0; i < kBoxes; ++i) ask();
   for (int it = blockIdx.x; it < items; it += gridDim.x) {
     const GemvItem cur = next;
     if (it + gridDim.x < items) next = gemv_item<NT>(a, sm, it + gridDim.x, ntile, n_act);
@@ -495,20 +503,22 @@ int launch_gemv(const GemvArgs& a, int items, const CUtensorMap& tm, cudaStream_
 
 template <int G, bool ZERO>
 int launch_gemv(const GemvArgs& a, const uint8_t* w, cudaStream_t st) {
-  // passes at most: every expert's last eight token rows may be fewer
-  const long long passes = std::min<long long>(a.max_rows, a.E + a.max_rows / 8);
+  // passes at most, and as many as there will be when the experts' last eights are half full
+  const long long most = std::min<long long>(a.max_rows, a.E + a.max_rows / 8);
+  const long long passes = a.offsets ? std::min<long long>(most, (a.E + 1) / 2 + a.max_rows / 8)
+                                     : ceil_div(a.max_rows, 8);
   // the height whose rounds cost the least: its rows, and what a step costs beside them (about one unit:
   // 602, 680 and 952 us with 48, 32 and 16 rows for 64 tokens on 256 experts of 4096 x 7168)
   long long best = 0;
   int nt = 0, items = 0;
   for (int n = 1; n <= kGvMaxTile; ++n) {
-    const long long c = passes * ceil_div(a.N, n * kGvUnit), slots = 2LL * sm_count();
-    const long long cost = (c + slots - 1) / slots * (n + 1);
-    if (c > 0x3fffffff) return MOE_ERR_INVALID_ARG;   // (y alone would not fit on the GPU)
+    const long long tiles = ceil_div(a.N, n * kGvUnit), slots = 2LL * sm_count();
+    const long long cost = (std::max(1LL, passes) * tiles + slots - 1) / slots * (n + 1);
+    if (most * tiles > 0x3fffffff) return MOE_ERR_INVALID_ARG;   // (y alone would not fit on the GPU)
     if (!nt || cost <= best) {
       nt = n;
       best = cost;
-      items = (int)c;
+      items = (int)(most * tiles);
     }
   }
   CUtensorMap tm;
