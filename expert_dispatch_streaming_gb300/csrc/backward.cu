@@ -346,10 +346,10 @@ int moe_permute_backward(const uint16_t* dx_perm, const int32_t* pos, const uint
   return by_k(k, [&](auto kc) -> int {
     constexpr int K = decltype(kc)::value;
     if (out_f32)
-      MOE_LAUNCH_PDL((permute_backward_kernel<K, true>), grid, block, 0, (cudaStream_t)stream,
+      MOE_LAUNCH_NEXT(true, (permute_backward_kernel<K, true>), grid, block, 0, (cudaStream_t)stream,
                      dx_perm, pos, add, T, H, dx);
     else
-      MOE_LAUNCH_PDL((permute_backward_kernel<K, false>), grid, block, 0, (cudaStream_t)stream,
+      MOE_LAUNCH_NEXT(true, (permute_backward_kernel<K, false>), grid, block, 0, (cudaStream_t)stream,
                      dx_perm, pos, add, T, H, dx);
     MOE_COUNT_LAUNCH();
     MOE_LAUNCH_CHECK();
@@ -372,7 +372,7 @@ int moe_combine_backward(const uint16_t* dout, const uint16_t* y_perm, const int
   const int threads = std::min(kCombineBackThreads, (int)round_up((size_t)H / 8, 32));
   return by_k(k, [&](auto kc) -> int {
     constexpr int K = decltype(kc)::value;
-    MOE_LAUNCH_PDL(combine_backward_kernel<K>, dim3(T), dim3(threads), 0, (cudaStream_t)stream,
+    MOE_LAUNCH_NEXT(true, combine_backward_kernel<K>, dim3(T), dim3(threads), 0, (cudaStream_t)stream,
                    dout, y_perm, pos, w, T, H, shared, shared_gate, dy_perm, dw, dshared,
                    dshared_gate);
     MOE_COUNT_LAUNCH();
@@ -392,13 +392,13 @@ int moe_gate_backward(const float* logits, const int32_t* ids, const float* dw, 
   const dim3 block(kGateBackWarps * 32);
   const dim3 four(ceil_div(T, 4 * kGateBackWarps));
   if (gating == MOE_GATING_SOFTMAX)
-    MOE_LAUNCH_PDL(gate_backward_softmax_kernel, dim3(ceil_div(T, kGateBackWarps)), block, 0, st,
+    MOE_LAUNCH_NEXT(true, gate_backward_softmax_kernel, dim3(ceil_div(T, kGateBackWarps)), block, 0, st,
                    logits, ids, dw, T, E, k, scale, dlogits);
   else if (gating == MOE_GATING_SOFTMAX_RENORM)
-    MOE_LAUNCH_PDL(gate_backward_chosen_kernel<false>, four, block, 0, st, logits, ids, dw, T, E, k,
+    MOE_LAUNCH_NEXT(true, gate_backward_chosen_kernel<false>, four, block, 0, st, logits, ids, dw, T, E, k,
                    scale, dlogits);
   else
-    MOE_LAUNCH_PDL(gate_backward_chosen_kernel<true>, four, block, 0, st, logits, ids, dw, T, E, k,
+    MOE_LAUNCH_NEXT(true, gate_backward_chosen_kernel<true>, four, block, 0, st, logits, ids, dw, T, E, k,
                    scale, dlogits);
   MOE_COUNT_LAUNCH();
   MOE_LAUNCH_CHECK();

@@ -494,7 +494,7 @@ template <int G, bool ZERO, int NT>
 int launch_gemv(const GemvArgs& a, int items, const CUtensorMap& tm, cudaStream_t st) {
   auto kernel = gemv_int4_kernel<G, ZERO, NT>;
   MOE_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kGvRing));
-  MOE_LAUNCH_PDL(kernel, dim3(std::min(items, 2 * sm_count())),
+  MOE_LAUNCH_NEXT(true, kernel, dim3(std::min(items, 2 * sm_count())),
                  dim3(kGvThreads), kGvRing, st, a, tm);
   MOE_COUNT_LAUNCH();
   MOE_LAUNCH_CHECK();

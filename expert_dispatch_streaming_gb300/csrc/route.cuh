@@ -89,6 +89,10 @@ struct RouteArgs {
 // launch_pdl, with programmatic stream serialization whatever MOE_OPT_PDL says when `chained`: for
 // a kernel whose predecessor on the stream is one of the library's that the same call launched
 // (group-limited routing's five launches, 60 experts and 333 tokens: 37 us plain, 31 chained).
+// The slot sort, the gradients and the 4-bit products launch so whatever came before them (they
+// touch nothing before they have waited for it): behind a kernel that lets them, as all of theirs do,
+// a call in a row of them costs about 2 us less (32768 x 8 slots sorted 12.4 -> 9.8 us, one token on
+// 4096 x 7168 codes 10.4 -> 8.7).
 template <typename... KArgs, typename... Args>
 cudaError_t launch_next(bool chained, void (*kernel)(KArgs...), dim3 grid, dim3 block,
                         size_t smem, cudaStream_t st, Args&&... args) {

@@ -190,12 +190,12 @@ int moe_sort_tokens(const int32_t* ids, int T, int E, int k, int32_t* counts, in
   }
   int32_t* hist = static_cast<int32_t*>(ws);
   if (p.chunks > 1) {
-    MOE_LAUNCH_PDL(sort_histogram_kernel, dim3(p.chunks), dim3(kSortThreads), 0, st, ids, n, E,
+    MOE_LAUNCH_NEXT(true, sort_histogram_kernel, dim3(p.chunks), dim3(kSortThreads), 0, st, ids, n, E,
                    p.chunk, hist);
     MOE_COUNT_LAUNCH();
     MOE_LAUNCH_CHECK();
   }
-  MOE_LAUNCH_NEXT(p.chunks > 1, sort_rank_kernel, dim3(std::max(1, p.chunks)), dim3(kSortThreads),
+  MOE_LAUNCH_NEXT(true, sort_rank_kernel, dim3(std::max(1, p.chunks)), dim3(kSortThreads),
                   0, st, ids, n, E, p.chunk, hist, counts, offsets, pos, src, p.chunks > 1);
   MOE_COUNT_LAUNCH();
   MOE_LAUNCH_CHECK();
