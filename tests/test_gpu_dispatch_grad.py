@@ -261,6 +261,58 @@ def test_combine_backward_one_output(moe, which):
     assert all(torch.all(one[n] == 0) for n in one if n != which)
 
 
+def test_permute_is_the_adjoint(moe):
+    """<dx_perm, permute(x)> = <permute_backward(dx_perm), x>, on small whole numbers, where both are exact."""
+    T, E, k, H = 45, 12, 5, 136
+    g = gen(51)
+    _, _, pos, src = dispatch(moe, T, E, k, 0.3, 8)
+    x, d = (torch.randint(-8, 9, s, generator=g, device="cuda").to(torch.bfloat16)
+            for s in ((T, H), (T * k, H)))
+    xp, dx = torch.empty_like(d), torch.empty((T, H), device="cuda")
+    moe.moe_permute(x, src, T, k, H, xp)
+    moe.moe_permute_backward(d, pos, None, T, k, H, "fp32", dx)
+    assert (d.double() * xp.double()).sum() == (dx.double() * x.double()).sum()
+
+
+def test_combine_backward_differences(moe):
+    """The gradients of <dout, combine(...)> are its differences: the sum is linear in each of y_perm, w,
+    shared and shared_gate, and the values are chosen so that nothing rounds (whole numbers and halves
+    whose sums stay below 2^7)."""
+    T, E, k, H = 9, 6, 3, 16
+    g = gen(52)
+    _, _, pos, _ = dispatch(moe, T, E, k, 0.2, 9)
+    live = pos >= 0
+
+    def whole(*shape):
+        return torch.randint(-3, 4, shape, generator=g, device="cuda").float()
+    y, sh, dout = whole(T * k, H), whole(T, H), whole(T, H)
+    w, gate = whole(T, k) * 0.5, whole(T) * 0.5
+
+    def loss(y, w, sh, gate):
+        out = torch.empty((T, H), dtype=torch.bfloat16, device="cuda")
+        moe.moe_combine(y.to(torch.bfloat16), pos, w, T, k, H, sh.to(torch.bfloat16), gate, None, out)
+        return (out.double() * dout.double()).sum()
+
+    bf = torch.bfloat16
+    dy, dsh = torch.zeros((T * k, H), dtype=bf, device="cuda"), torch.empty((T, H), dtype=bf, device="cuda")
+    dw, dg = torch.empty((T, k), device="cuda"), torch.empty(T, device="cuda")
+    moe.moe_combine_backward(dout.to(bf), y.to(bf), pos, w, T, k, H, sh.to(bf), gate, dy, dw, dsh, dg)
+    base = loss(y, w, sh, gate)
+
+    def moved(v, at, by=1.0):
+        v = v.clone()
+        v[at] += by
+        return v
+    for t in range(T):
+        assert loss(y, w, sh, moved(gate, t)) - base == dg[t]
+        assert loss(y, w, moved(sh, (t, 5)), gate) - base == dsh[t, 5]
+        for j in range(k):
+            assert loss(y, moved(w, (t, j)), sh, gate) - base == dw[t, j]
+            if live[t, j]:
+                at = (int(pos[t, j]), 11)
+                assert loss(moved(y, at), w, sh, gate) - base == dy[at]
+
+
 def gate_weights(z, ids, gating, scale):
     """w [T][k] in 64 bits, zero at slots without an expert."""
     has = (ids >= 0) & (ids < z.shape[1])
