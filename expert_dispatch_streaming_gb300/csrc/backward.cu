@@ -250,8 +250,9 @@ gate_backward_chosen_kernel(const float* __restrict__ logits, const int32_t* __r
     }
   }
   const float r = total == 0.f ? 0.f : v / total;
-  const float D = sum8(id >= 0 ? r * up : 0.f);
-  float g = id >= 0 ? scale * (r * (up - D)) : 0.f;
+  const bool live = r != 0.f;                  // (a slot of weight zero is in no sum, whatever its dw)
+  const float D = sum8(live ? r * up : 0.f);
+  float g = live ? scale * (r * (up - D)) : 0.f;
   if (SIGMOID) g *= 1.f / (1.f + expf(l));
   merge_chosen(id, g, lane);
   __syncwarp();                                // (the zeros come first)
@@ -295,7 +296,8 @@ gate_backward_softmax_kernel(const float* __restrict__ logits, const int32_t* __
   total = reduce_warp(total);
   const float inv = total == 0.f ? 0.f : 1.f / total;
   __syncwarp();
-  float g = id >= 0 ? row[id] * inv * up : 0.f;
+  const float p = id >= 0 ? row[id] * inv : 0.f;
+  float g = p != 0.f ? p * up : 0.f;           // (a slot of weight zero is in no sum, whatever its dw)
   const float D = reduce_warp(g);
   merge_chosen(id, g, lane);
   __syncwarp();

@@ -526,8 +526,9 @@ int moe_combine_backward(const uint16_t* dout, const uint16_t* y_perm, const int
  *  int32, dw device [T][k] fp32; dlogits device [T][E] fp32, every element written; gating: enum
  *  moe_gating without MOE_GATING_GROUPED.
  * An id outside [0, E) is a slot without an expert: its dw is not read and it is in no sum.  An id
- * that stands twice in a row counts as two slots.  A token whose weights are all zero (every score
- * open to it -infinity, see moe_route_topk_grouped) gets zero gradients.
+ * that stands twice in a row counts as two slots.  A slot whose weight is zero (a logit of -infinity)
+ * is in no sum either, whatever its dw; a token whose weights are all zero (every score open to it
+ * -infinity, see moe_route_topk_grouped) gets zero gradients.
  * Limits: E <= 256, k <= min(E, 8); dlogits 16-byte aligned. */
 int moe_gate_backward(const float* logits, const int32_t* ids, const float* dw, int T, int E,
                       int k, int gating, float scale, float* dlogits, void* stream);

@@ -410,6 +410,25 @@ def test_gate_backward_masked_scores(moe, gating):
     assert torch.all((got - want).abs() <= mag * (3 * 2 + E + 210) * 2.0 ** -23)
 
 
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("gating", GATING)
+def test_gate_backward_weights_of_zero(moe, gating, bad):
+    """What stands in dw for a chosen expert whose logit is -infinity, or for a token all of whose
+    logits are, reaches nothing."""
+    E, k, T = 37, 3, 6
+    g = gen(11)
+    z = torch.randn((T, E), generator=g, device="cuda")
+    ids = torch.tensor([[1, 30, 36]] * T, dtype=torch.int32, device="cuda")
+    dw = torch.randn((T, k), generator=g, device="cuda")
+    z[0, 30], z[2, 1], z[2, 36] = [-float("inf")] * 3
+    z[4] = -float("inf")
+    off = torch.isinf(z.gather(1, ids.long()))
+    got = run_gate(moe, z, ids, torch.where(off, bad, dw), gating, 1.5)
+    want = run_gate(moe, z, ids, torch.where(off, 0.0, dw), gating, 1.5)
+    assert torch.equal(got, want) and torch.all(torch.isfinite(got))
+    assert torch.all(got[4] == 0) and got[0, 30] == 0
+
+
 def test_gate_backward_differences(moe):
     """The gradient against central differences of the library's own gating weights: w of
     moe_route_topk with an identity router, whose logits are the tokens' values."""
