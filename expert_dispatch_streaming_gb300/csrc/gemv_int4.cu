@@ -257,8 +257,8 @@ gemv_int4_kernel(const GemvArgs a, const __grid_constant__ CUtensorMap tm) {
   // codes meet; rows past the item's last read that one (their sums are not stored), and what lies
   // past the end of K is set to zero when it is used.  A step's scales of the weight rows gr and gr + 8 of
   // a unit: lanes t = 0 and 1, two in a register; their zero points: lanes t = 2 and 3, four in a
-  // register.  Rows and groups past the end read the last ones (those rows are not stored, those
-  // groups' products are zero).
+  // register.  Rows past the end read the last one (they are not stored); the scales of groups past the
+  // end are zero, so that an infinite last scale meets no product that is zero there.
   struct Source {
     const uint16_t* x;
     size_t s;
@@ -316,8 +316,9 @@ gemv_int4_kernel(const GemvArgs a, const __grid_constant__ CUtensorMap tm) {
     } else if (t < 2) {
 #pragma unroll
       for (int j = 0; j < NG / 2; ++j) {
-        const uint32_t lo = __ldg(a.s + at + min(g0 + 2 * j, a.ng - 1));
-        rv[j] = lo | (uint32_t)__ldg(a.s + at + min(g0 + 2 * j + 1, a.ng - 1)) << 16;
+        const int g = g0 + 2 * j;
+        const uint32_t lo = g < a.ng ? __ldg(a.s + at + g) : 0u;
+        rv[j] = lo | (g + 1 < a.ng ? (uint32_t)__ldg(a.s + at + g + 1) << 16 : 0u);
       }
     } else if (ZERO) {
 #pragma unroll

@@ -106,6 +106,25 @@ def test_gemv_rows_do_not_mix(moe, group):  # noqa: F811
     assert torch.equal(got[~bad], ref[~bad])
 
 
+@pytest.mark.parametrize("zero", [False, True])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("K", [32, 288, 1440, 2048])
+def test_gemv_infinite_last_scale(moe, K, group, zero):  # noqa: F811
+    """An infinite scale of a row's last group: infinity with the sign of that group's sum."""
+    N, rows = 70, 5
+    g = gen(K + group)
+    w, s, z = weights(g, 1, N, K, group, zero)
+    x = torch.randn((rows, K), generator=g, device="cuda").to(torch.bfloat16)
+    s[0, 33, -1] = float("inf")
+    y, _ = run(moe, x, w, s, z, None, group, rows, "fp32", N, K, 1)
+    one = torch.ones_like(s)
+    one[0, :, :-1] = 0
+    last = x.double() @ values(w[0], one[0], None if z is None else z[0], group).T
+    assert torch.all(last[:, 33] != 0)
+    assert torch.equal(y[:rows, 33].double(), torch.sign(last[:, 33]) * float("inf"))
+    assert torch.all(torch.isfinite(y[:rows, :33])) and torch.all(torch.isfinite(y[:rows, 34:]))
+
+
 @pytest.mark.parametrize("group", [32, 64, 128])
 def test_gemv_unaligned_scales(moe, group):  # noqa: F811
     """Scales and zero points that start on no 16-byte boundary: the aligned call's result, to the bit."""
