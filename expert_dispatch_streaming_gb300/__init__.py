@@ -198,12 +198,13 @@ def _current_stream() -> int | None:
     try:
         import torch
         handle = torch.cuda.current_stream().cuda_stream
-        raw, device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
-        if raw(device()) == handle:
-            _current_stream = lambda: raw(device())  # noqa: E731
-        return handle
     except Exception:
         return None
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    device = getattr(torch._C, "_cuda_getDevice", None)
+    if raw and device and raw(device()) == handle:
+        _current_stream = lambda: raw(device())  # noqa: E731
+    return handle
 
 
 def stream_handle(s) -> int | None:
