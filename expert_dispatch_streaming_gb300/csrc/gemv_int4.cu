@@ -504,10 +504,10 @@ int launch_gemv(const GemvArgs& a, int items, const CUtensorMap& tm, cudaStream_
 
 template <int G, bool ZERO>
 int launch_gemv(const GemvArgs& a, const uint8_t* w, cudaStream_t st) {
-  // passes at most, and as many as there will be when the experts' last eights are half full
-  const long long most = std::min<long long>(a.max_rows, a.E + a.max_rows / 8);
-  const long long passes = a.offsets ? std::min<long long>(most, (a.E + 1) / 2 + a.max_rows / 8)
-                                     : ceil_div(a.max_rows, 8);
+  // passes at most (an expert's last eight has one row at least), and as many as there will be when the
+  // experts' last eights are half full
+  const long long most = (a.max_rows + 7LL * std::min(a.E, a.max_rows)) / 8;
+  const long long passes = std::min<long long>(most, (a.E + 1) / 2 + a.max_rows / 8);
   // the height whose rounds cost the least: its rows, and what a step costs beside them (about one unit:
   // 602, 680 and 952 us with 48, 32 and 16 rows for 64 tokens on 256 experts of 4096 x 7168)
   long long best = 0;
