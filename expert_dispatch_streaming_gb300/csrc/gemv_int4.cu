@@ -30,10 +30,11 @@
 // use.  The warps' sums are added in warp order in shared memory.
 //
 // Measured (the floor is what has to be read and written at the copy bandwidth): 14336 x 14336 codes,
-// groups of 128, one token 23.7 us (floor 15.6; the same boxes loaded and not used 18.5), eight tokens
-// 27; 8 of 256 experts of 4096 x 7168 30 us (17.9), 64 tokens on most of the 256 600 us (414); 4096 x
-// 7168, one token, 8 us, of which launch, first loads and the last sums are 6.  Turning codes to bf16
-// bounds the large ones: 144 of about 280 instructions for 4096 codes, with the issue slots 60% busy.
+// groups of 128, one token 22.9 us (floor 15.6; the same boxes loaded and not used 18.5), eight tokens
+// 24.9; 8 of 256 experts of 4096 x 7168 30.6 us (17.9), 64 tokens on most of the 256 588 us (414); 4096 x
+// 7168, one token, 8.3 us, eight 9.1, of which launch, first loads and the last sums are 6.  Turning
+// codes to bf16 bounds the large ones: 144 of about 280 instructions for 4096 codes, with the issue slots
+// 60% busy.
 // More than eight token rows are passes side by side: 16 rows a pass need registers that 16 warps a SM
 // do not have, and a kernel for 64, codes turned once, won (1.1 to 1.6 times) only from 33 rows and
 // 4096 weight rows on.

@@ -334,6 +334,7 @@ int moe_route_static_error(int32_t* code, void* stream);
  *          slot's row in expert order, stable in t * k + j, or -1; src [T*k]: src[pos[t][j]] =
  *          t*k + j, and -1 in the entries from offsets[E] on.
  *  ws      device scratch of moe_sort_tokens_workspace_size(T, E, k) bytes, 4-byte aligned
+ * No output overlaps ids.
  * moe_permute, moe_quantize_fp8, moe_combine and the gradients below take such pos and src.
  * Limits: 1 <= E <= 256, 1 <= k <= 8, T >= 0 (T == 0 writes zero counts and offsets; ids, pos, src
  * and ws may be NULL then), T * k < 2^31.  The dispatch is that of "NovaLLM ...", "3. Optimization
@@ -490,7 +491,8 @@ int moe_combine(const uint16_t* y_perm, const int32_t* pos, const float* w, int 
  * Of the way into expert order, of the weighted way back and of the gating: what training a router
  * (or experts of one's own) around this layer's dispatch needs.  pos as moe_route_topk or
  * moe_sort_tokens give it; a slot whose pos lies outside [0, T*k) has no row.  All sums in fp32 and
- * in a fixed order.  The pages describe inference only.
+ * in a fixed order.  No output overlaps an input, but where it says so.  The pages describe inference
+ * only.
  *
  * moe_permute_backward -- of moe_permute:  dx[t] = sum_{j<k} dx_perm[pos[t][j]] + add[t], j in order.
  *  dx_perm device [T*k][H] bf16; add device [T][H] bf16 or NULL (a gradient that reaches x on
@@ -509,7 +511,7 @@ int moe_permute_backward(const uint16_t* dx_perm, const int32_t* pos, const uint
  *  dout, shared, dshared device [T][H] bf16; y_perm, dy_perm device [T*k][H] bf16; w, dw device
  *  [T][k] fp32; shared_gate, dshared_gate device [T] fp32.  Any of the four outputs may be NULL
  *  (not all); y_perm is read for dw only, shared for dshared_gate only (which needs shared and
- *  shared_gate).  dy_perm must not overlap the inputs.
+ *  shared_gate).
  *  H a multiple of 8; bf16 rows 16-byte aligned; k <= 8. */
 int moe_combine_backward(const uint16_t* dout, const uint16_t* y_perm, const int32_t* pos,
                          const float* w, int T, int k, int H, const uint16_t* shared,
