@@ -300,9 +300,11 @@ gate_backward_softmax_kernel(const float* __restrict__ logits, const int32_t* __
   float g = p != 0.f ? p * up : 0.f;           // (a slot of weight zero is in no sum, whatever its dw)
   const float D = reduce_warp(g);
   merge_chosen(id, g, lane);
+  // (a token without an expert is in no loss: zeros, whatever its logits hold)
+  const bool some = __any_sync(0xffffffffu, id >= 0);
   __syncwarp();
 #pragma unroll
-  for (int c = 0; c < kMaxExperts / 32; ++c) row[lane + 32 * c] = -scale * (z[c] * inv * D);
+  for (int c = 0; c < kMaxExperts / 32; ++c) row[lane + 32 * c] = some ? -scale * (z[c] * inv * D) : 0.f;
   __syncwarp();
   if (id >= 0) row[id] += scale * g;
   __syncwarp();
