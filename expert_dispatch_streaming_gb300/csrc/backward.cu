@@ -234,7 +234,9 @@ gate_backward_chosen_kernel(const float* __restrict__ logits, const int32_t* __r
   float v, total;
   if (!SIGMOID) {
     const float top = max8(l);
-    v = id >= 0 && top != -CUDART_INF_F ? expf(l - top) : 0.f;
+    // (zero by the logit, not by the largest: fmaxf drops NaNs, and those of a row with nothing else would
+    // be lost; so they make every weight of the token NaN, as they do in routing)
+    v = id >= 0 && l != -CUDART_INF_F ? expf(l - top) : 0.f;
     total = sum8(v);
   } else {
     v = id >= 0 ? 1.f / (1.f + expf(-l)) : 0.f;
@@ -289,7 +291,7 @@ gate_backward_softmax_kernel(const float* __restrict__ logits, const int32_t* __
   float total = 0.f;
 #pragma unroll
   for (int c = 0; c < kMaxExperts / 32; ++c) {
-    z[c] = lane + 32 * c < E && top != -CUDART_INF_F ? expf(z[c] - top) : 0.f;
+    z[c] = z[c] != -CUDART_INF_F ? expf(z[c] - top) : 0.f;   // (a NaN stays one; past E: -infinity)
     total += z[c];
     row[lane + 32 * c] = z[c];
   }

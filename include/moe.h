@@ -531,6 +531,8 @@ int moe_combine_backward(const uint16_t* dout, const uint16_t* y_perm, const int
  * that stands twice in a row counts as two slots.  A slot whose weight is zero (a logit of -infinity)
  * is in no sum either, whatever its dw; a token whose weights are all zero (every score open to it
  * -infinity, see moe_route_topk_grouped) gets zero gradients.
+ * A NaN logit that makes weights NaN (a chosen expert's; SOFTMAX: any of the row) makes the chosen
+ * experts' gradients (SOFTMAX: the row's) NaN; a token without an expert in any slot gets zeros.
  * Limits: E <= 256, k <= min(E, 8); dlogits 16-byte aligned. */
 int moe_gate_backward(const float* logits, const int32_t* ids, const float* dw, int T, int E,
                       int k, int gating, float scale, float* dlogits, void* stream);
