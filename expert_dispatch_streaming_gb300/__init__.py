@@ -462,7 +462,8 @@ def moe_combine_backward(dout, y_perm, pos, w, T, k, H, shared, shared_gate, dy_
 
 
 def moe_gate_backward(logits, ids, dw, T, E, k, gating, scale, dlogits, stream=None) -> None:
-    """dlogits [T][E] of the weights' gradient dw [T][k] at the chosen ids."""
+    """dlogits [T][E] of the weights' gradient dw [T][k] at the ids that the weights were normalised
+    over: routing's own, also where the dispatch dropped some of their slots (dw is 0 there)."""
     _check(_lib.moe_gate_backward(ptr(logits), ptr(ids), ptr(dw), T, E, k,
                                   GATING.get(gating, gating), float(scale), ptr(dlogits),
                                   stream_handle(stream)), "moe_gate_backward")

@@ -334,7 +334,8 @@ int moe_route_static_error(int32_t* code, void* stream);
  *          slot's row in expert order, stable in t * k + j, or -1; src [T*k]: src[pos[t][j]] =
  *          t*k + j, and -1 in the entries from offsets[E] on.
  *  ws      device scratch of moe_sort_tokens_workspace_size(T, E, k) bytes, 4-byte aligned
- * No output overlaps ids.
+ * No output overlaps ids.  Where ids are routing's with slots dropped, keep routing's own as well: the
+ * gradient of its weights (moe_gate_backward) is that of all k slots.
  * moe_permute, moe_quantize_fp8, moe_combine and the gradients below take such pos and src.
  * Limits: 1 <= E <= 256, 1 <= k <= 8, T >= 0 (T == 0 writes zero counts and offsets; ids, pos, src
  * and ws may be NULL then), T * k < 2^31.  The dispatch is that of "NovaLLM ...", "3. Optimization
@@ -527,7 +528,12 @@ int moe_combine_backward(const uint16_t* dout, const uint16_t* y_perm, const int
  *  logits device [T][E] fp32 (incl. logit_bias, as moe_route_topk writes them); ids device [T][k]
  *  int32, dw device [T][k] fp32; dlogits device [T][E] fp32, every element written; gating: enum
  *  moe_gating without MOE_GATING_GROUPED.
- * An id outside [0, E) is a slot without an expert: its dw is not read and it is in no sum.  An id
+ * ids are those that the weights were made for.  moe_route_topk and moe_route_topk_grouped normalise
+ * over all k of them: where single slots are dropped between routing and the experts (-1 in the ids that
+ * moe_sort_tokens gets), give this call the ids as routing wrote them.  A dropped slot's dw is 0
+ * (moe_combine_backward writes that), and its logit has a gradient still, through the other weights.
+ * An id outside [0, E) is a slot that the weights themselves left out (a router that normalises over
+ * what it keeps; a token that is all padding): its dw is not read and it is in no sum.  An id
  * that stands twice in a row counts as two slots.  A slot whose weight is zero (a logit of -infinity)
  * is in no sum either, whatever its dw; a token whose weights are all zero (every score open to it
  * -infinity, see moe_route_topk_grouped) gets zero gradients.

@@ -1,5 +1,7 @@
 """GPU tests of moe_gate_backward on rows that routing leaves in an odd state: padding, NaN logits,
 masked scores, slots that are dropped between routing and the experts."""
+import os
+
 import pytest
 import torch
 
@@ -59,3 +61,84 @@ def test_nan_logits_reach_the_gradient(moe, gating, k):  # noqa: F811
         assert torch.all(torch.isnan(got[5]))
     else:
         assert torch.equal(got[5], want[5])
+
+
+def readme_example():
+    """The training example of README.md: its block of calls."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    with open(os.path.join(root, "README.md")) as f:
+        lines = f.read().split("\n")
+    first = next(i for i, line in enumerate(lines) if line.startswith("    moe.moe_sort_tokens("))
+    block = []
+    for line in lines[first:]:
+        if not line.startswith("    "):
+            break
+        block.append(line[4:])
+    return "\n".join(block)
+
+
+@pytest.mark.parametrize("gating,scale", [("softmax_renorm", 1.0), ("softmax", 1.0),
+                                          ("sigmoid_bias_renorm", 2.5)])
+def test_dropped_slots_through_the_documented_calls(moe, gating, scale):  # noqa: F811
+    """README's training example, run as it stands, on a batch whose single slots are dropped between
+    routing and the experts: the gradient of the library's own weights, which are normalised over all k
+    slots, against 64-bit differentiation of them.  A dropped expert's logit has a gradient through the
+    weights of the others."""
+    T, H, N, E, k = 61, 256, 192, 20, 4
+    g = gen(33)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    bf = torch.bfloat16
+    x = torch.randn((T, H), generator=g, device="cuda").to(bf)
+    w_r = torch.randn((H, E), generator=g, device="cuda") * 0.1
+    ids, w, logits = torch.empty((T, k), **i32), torch.empty((T, k), device="cuda"), torch.empty(
+        (T, E), device="cuda")
+    disp = [torch.empty(E, **i32), torch.empty(E + 1, **i32), torch.empty((T, k), **i32),
+            torch.empty(T * k, **i32)]
+    nb = moe.moe_route_workspace_size(T, H, E, k)
+    moe.moe_route_topk(x, w_r, None, None, None, None, T, H, E, k, gating, scale, ids, w, *disp, logits,
+                       None, None, torch.empty(nb, dtype=torch.uint8, device="cuda"), nb)
+    drop = torch.rand((T, k), generator=g, device="cuda") < 0.25
+    drop[7], drop[8] = True, False
+    kept = torch.where(drop, -1, ids)
+    ws_bytes = moe.moe_sort_tokens_workspace_size(T, E, k)
+    n4 = moe.moe_grouped_gemv_int4_workspace_size(T * k, E, N, H)
+    u8 = dict(dtype=torch.uint8, device="cuda")
+    names = dict(
+        moe=moe, T=T, E=E, k=k, H=H, N=N, ids=ids, kept=kept, x=x, w=w, logits=logits,
+        counts=torch.empty(E, **i32), offsets=torch.empty(E + 1, **i32), pos=torch.empty((T, k), **i32),
+        src=torch.empty(T * k, **i32), ws=torch.empty(max(ws_bytes, 4), **u8), ws_bytes=ws_bytes,
+        x_perm=torch.empty((T * k, H), dtype=bf, device="cuda"),
+        w4=torch.randint(0, 256, (E, N, H // 2), generator=g, **u8),
+        scales=(torch.rand((E, N, H // 128), generator=g, device="cuda") * 0.02).to(bf),
+        zeros=torch.randint(0, 17, (E, N, H // 128), generator=g, **u8),
+        y=torch.empty((T * k, N), dtype=bf, device="cuda"), ws4=torch.empty(n4, **u8), n4=n4,
+        out=torch.empty((T, N), dtype=bf, device="cuda"),
+        dout=torch.randn((T, N), generator=g, device="cuda").to(bf),
+        dy=torch.zeros((T * k, N), dtype=bf, device="cuda"), dw=torch.empty((T, k), device="cuda"),
+        dlogits=torch.empty((T, E), device="cuda"),
+        dx_perm=torch.randn((T * k, H), generator=g, device="cuda").to(bf),
+        dx=torch.empty((T, H), device="cuda"))
+    code = readme_example().replace('"softmax_renorm", 1.0', "gating, scale")
+    exec(code, names | dict(gating=gating, scale=scale))
+    assert int(names["offsets"][-1]) == int((~drop).sum())
+    assert torch.all(names["dw"][drop] == 0)
+    # the framework's own weights in 64 bits: over all k slots, whatever the dispatch drops
+    z = logits.double().requires_grad_(True)
+    zj = z.gather(1, ids.long())
+    if gating == "softmax":
+        w64 = torch.softmax(z, 1).gather(1, ids.long()) * scale
+    else:
+        v = torch.sigmoid(zj) if gating == "sigmoid_bias_renorm" else torch.exp(zj)
+        w64 = v / v.sum(1, keepdim=True) * scale
+    assert torch.all((w64.detach() - w.double()).abs() <= w64.detach() * (E + 40) * 2.0 ** -23)
+    y, pos = names["y"], names["pos"]
+    yt = torch.where(drop[:, :, None], 0.0, y[pos.clamp_min(0).long()].double())
+    dots = torch.einsum("th,tkh->tk", names["dout"].double(), yt)
+    (want,) = torch.autograd.grad((w64 * dots).sum(), z)
+    # dw is off by (N + 2) 2^-24 of its terms' magnitudes, the gating by (E + 64) 2^-23 of its own; both
+    # reach an element with a factor of at most 2 scale
+    size = torch.einsum("th,tkh->tk", names["dout"].abs().double(), yt.abs()).sum(1, keepdim=True)
+    got = names["dlogits"].double()
+    assert torch.all((got - want).abs() <= 2 * scale * size * (N + E + 66) * 2.0 ** -23)
+    part = drop & ~drop.all(1, keepdim=True)
+    assert torch.all(got.gather(1, ids.long())[part] != 0) and torch.all(got[7] == 0)
