@@ -96,70 +96,67 @@ combine_backward_kernel(const uint16_t* __restrict__ dout, const uint16_t* __res
   pdl_wait();
   __shared__ float red[kCombineBackThreads / 32][K + 1];
   const unsigned rows = (unsigned)T * K;
-  const int nv = H / 8, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int t = blockIdx.x; t < T; t += gridDim.x) {
-    int p[K];
-    float wj[K], dot[K + 1];
+  const int nv = H / 8, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, t = blockIdx.x;
+  int p[K];
+  float wj[K], dot[K + 1];
+#pragma unroll
+  for (int j = 0; j < K; ++j) {
+    p[j] = __ldg(pos + (size_t)t * K + j);
+    wj[j] = __ldg(w + (size_t)t * K + j);
+  }
+#pragma unroll
+  for (int j = 0; j <= K; ++j) dot[j] = 0.f;
+  const float gs = shared_gate ? __ldg(shared_gate + t) : 1.f;
+  for (int v = threadIdx.x; v < nv; v += blockDim.x) {
+    const uint4 dq = __ldg(reinterpret_cast<const uint4*>(dout + (size_t)t * H) + v);
+    uint4 q[K], sq = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
     for (int j = 0; j < K; ++j) {
-      p[j] = __ldg(pos + (size_t)t * K + j);
-      wj[j] = __ldg(w + (size_t)t * K + j);
+      q[j] = make_uint4(0u, 0u, 0u, 0u);
+      if (dw && (unsigned)p[j] < rows)
+        q[j] = __ldg(reinterpret_cast<const uint4*>(y + (size_t)p[j] * H) + v);
     }
+    if (dgate) sq = __ldg(reinterpret_cast<const uint4*>(shared + (size_t)t * H) + v);
+    float d[8], f[8];
+    unpack8(dq, d);
 #pragma unroll
-    for (int j = 0; j <= K; ++j) dot[j] = 0.f;
-    const float gs = shared_gate ? __ldg(shared_gate + t) : 1.f;
-    for (int v = threadIdx.x; v < nv; v += blockDim.x) {
-      const uint4 dq = __ldg(reinterpret_cast<const uint4*>(dout + (size_t)t * H) + v);
-      uint4 q[K], sq = make_uint4(0u, 0u, 0u, 0u);
+    for (int j = 0; j < K; ++j) {
+      unpack8(q[j], f);
 #pragma unroll
-      for (int j = 0; j < K; ++j) {
-        q[j] = make_uint4(0u, 0u, 0u, 0u);
-        if (dw && (unsigned)p[j] < rows)
-          q[j] = __ldg(reinterpret_cast<const uint4*>(y + (size_t)p[j] * H) + v);
-      }
-      if (dgate) sq = __ldg(reinterpret_cast<const uint4*>(shared + (size_t)t * H) + v);
-      float d[8], f[8];
-      unpack8(dq, d);
+      for (int i = 0; i < 8; ++i) dot[j] = fmaf(d[i], f[i], dot[j]);
+      if (dy && (unsigned)p[j] < rows) {
 #pragma unroll
-      for (int j = 0; j < K; ++j) {
-        unpack8(q[j], f);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) dot[j] = fmaf(d[i], f[i], dot[j]);
-        if (dy && (unsigned)p[j] < rows) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) f[i] = wj[j] * d[i];
-          reinterpret_cast<uint4*>(dy + (size_t)p[j] * H)[v] = pack8(f);
-        }
-      }
-      if (dgate) {
-        unpack8(sq, f);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) dot[K] = fmaf(d[i], f[i], dot[K]);
-      }
-      if (dshared) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = gs * d[i];
-        reinterpret_cast<uint4*>(dshared + (size_t)t * H)[v] = pack8(f);
+        for (int i = 0; i < 8; ++i) f[i] = wj[j] * d[i];
+        reinterpret_cast<uint4*>(dy + (size_t)p[j] * H)[v] = pack8(f);
       }
     }
+    if (dgate) {
+      unpack8(sq, f);
 #pragma unroll
-    for (int j = 0; j <= K; ++j) {
-      const float s = reduce_warp(dot[j]);
-      if (lane == 0) red[warp][j] = s;
+      for (int i = 0; i < 8; ++i) dot[K] = fmaf(d[i], f[i], dot[K]);
     }
-    __syncthreads();
-    if (threadIdx.x <= K) {
-      float s = 0.f;
-      for (int i = 0; i < (int)blockDim.x / 32; ++i) s += red[i][threadIdx.x];
-      if (threadIdx.x == K) {
-        if (dgate) dgate[t] = s;
-      } else if (dw) {
-        // (a slot without a row has no term in out[t], whatever dout[t] holds)
-        const int pj = __ldg(pos + (size_t)t * K + threadIdx.x);
-        dw[(size_t)t * K + threadIdx.x] = (unsigned)pj < rows ? s : 0.f;
-      }
+    if (dshared) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = gs * d[i];
+      reinterpret_cast<uint4*>(dshared + (size_t)t * H)[v] = pack8(f);
     }
-    __syncthreads();
+  }
+#pragma unroll
+  for (int j = 0; j <= K; ++j) {
+    const float s = reduce_warp(dot[j]);
+    if (lane == 0) red[warp][j] = s;
+  }
+  __syncthreads();
+  if (threadIdx.x <= K) {
+    float s = 0.f;
+    for (int i = 0; i < (int)blockDim.x / 32; ++i) s += red[i][threadIdx.x];
+    if (threadIdx.x == K) {
+      if (dgate) dgate[t] = s;
+    } else if (dw) {
+      // (a slot without a row has no term in out[t], whatever dout[t] holds)
+      const int pj = __ldg(pos + (size_t)t * K + threadIdx.x);
+      dw[(size_t)t * K + threadIdx.x] = (unsigned)pj < rows ? s : 0.f;
+    }
   }
 }
 

@@ -1,0 +1,51 @@
+"""GPU tests of the dispatch and its gradients at batches whose sizes come near 2^31, with the smallest
+rows: index arithmetic has to hold up to the documented limit T * k < 2^31.  Values are compared in pieces;
+a test that does not find the memory it needs is skipped."""
+import pytest
+import torch
+
+from test_gpu_dispatch_grad import gen, moe  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+BF, F32, I32 = torch.bfloat16, torch.float32, torch.int32
+PIECE = 1 << 26
+
+
+def need(gigabytes):
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < (gigabytes + 8) << 30:
+        pytest.skip(f"needs {gigabytes} GB")
+
+
+@pytest.fixture(autouse=True)
+def free_again():
+    yield
+    torch.cuda.empty_cache()
+
+
+def rows_of(n, H, seed):
+    """[n][H] bf16 of small whole numbers, a different row for any two neighbours."""
+    x = torch.empty((n, H), dtype=BF, device="cuda")
+    g = gen(seed)
+    for lo in range(0, n, PIECE):
+        m = min(PIECE, n - lo)
+        x[lo:lo + m] = torch.randint(-8, 9, (m, H), generator=g, device="cuda", dtype=torch.int8)
+    return x
+
+
+def pieces(n):
+    return [(lo, min(lo + PIECE, n)) for lo in range(0, n, PIECE)]
+
+
+def test_combine_backward_of_more_than_two_to_the_thirtieth_tokens(moe):  # noqa: F811
+    """A token a CTA: the index of the last ones passes 2^30.  Sums of whole numbers are exact."""
+    need(50)
+    T, H = (1 << 30) + 5, 8
+    dout, y = rows_of(T, H, 1), rows_of(T, H, 2)
+    pos = torch.arange(T - 1, -1, -1, dtype=I32, device="cuda")
+    w, dw = torch.ones(T, device="cuda"), torch.full((T,), 5.5, device="cuda")
+    moe.moe_combine_backward(dout, y, pos, w, T, 1, H, None, None, None, dw)
+    for lo, hi in pieces(T):
+        want = (dout[lo:hi].float() * y[T - hi:T - lo].flip(0).float()).sum(1)
+        assert torch.equal(dw[lo:hi], want)
