@@ -44,7 +44,7 @@ permute_backward_kernel(const uint16_t* __restrict__ dxp, const int32_t* __restr
   const int v = blockIdx.x * kBackThreads + threadIdx.x;
   if (v >= H / 8) return;
   const unsigned rows = (unsigned)T * K;
-  for (int t = blockIdx.y; t < T; t += gridDim.y) {
+  for (unsigned t = blockIdx.y; t < (unsigned)T; t += gridDim.y) {   // (the last step passes 2^31)
     uint4 q[K], a = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
     for (int j = 0; j < K; ++j) {

@@ -30,7 +30,7 @@ combine_kernel(const uint16_t* __restrict__ y, const int32_t* __restrict__ pos,
   pdl_wait();
   const int v = blockIdx.x * kCombineThreads + threadIdx.x;
   if (v >= H / 8) return;
-  for (int t = blockIdx.y; t < T; t += gridDim.y) {
+  for (unsigned t = blockIdx.y; t < (unsigned)T; t += gridDim.y) {   // (the last step passes 2^31)
   int pj[K];
   float wj[K];
 #pragma unroll
@@ -104,7 +104,7 @@ combine_norm_kernel(const uint16_t* __restrict__ y, const int32_t* __restrict__ 
   pdl_wait();
   __shared__ float red[32];
   const int nv = H / 8;
-  for (int t = blockIdx.x; t < T; t += gridDim.x) {
+  for (unsigned t = blockIdx.x; t < (unsigned)T; t += gridDim.x) {
     int pj[kMaxK];
     float wj[kMaxK];
 #pragma unroll

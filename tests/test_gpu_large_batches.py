@@ -49,3 +49,27 @@ def test_combine_backward_of_more_than_two_to_the_thirtieth_tokens(moe):  # noqa
     for lo, hi in pieces(T):
         want = (dout[lo:hi].float() * y[T - hi:T - lo].flip(0).float()).sum(1)
         assert torch.equal(dw[lo:hi], want)
+
+
+def test_permute_backward_and_combine_of_the_largest_batch(moe):  # noqa: F811
+    """T * k = 2^31 - 1, rows in reverse order: a block's steps over the tokens end past 2^31."""
+    need(125)
+    T, H = (1 << 31) - 1, 8
+    y, pos = rows_of(T, H, 3), torch.arange(T - 1, -1, -1, dtype=I32, device="cuda")
+    out = torch.full((T, H), 5.5, dtype=BF, device="cuda")
+    moe.moe_permute_backward(y, pos, None, T, 1, H, "bf16", out)
+    for lo, hi in pieces(T):
+        assert torch.equal(out[lo:hi], y[T - hi:T - lo].flip(0))
+    w = torch.full((T,), 0.5, device="cuda")
+    moe.moe_combine(y, pos, w, T, 1, H, None, None, None, out)
+    for lo, hi in pieces(T):
+        assert torch.equal(out[lo:hi], y[T - hi:T - lo].flip(0) * 0.5)
+    # whole rows of equal values: their root mean square is the value
+    w[:] = 2.0
+    for lo, hi in pieces(T):
+        y[lo:hi] = y[lo:hi, :1] + 9
+    normed = torch.full((T, H), 5.5, dtype=BF, device="cuda")
+    moe.moe_combine(y, pos, w, T, 1, H, None, None, None, out, out_normed=normed, norm_eps=0.0)
+    for lo, hi in pieces(T):
+        assert torch.equal(out[lo:hi], y[T - hi:T - lo].flip(0) * 2.0)
+        assert torch.all(normed[lo:hi] == 1.0)
