@@ -34,7 +34,7 @@ inline bool aligned2(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 1
 inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 inline bool aligned256(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 255u) == 0; }
 inline size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
-inline int ceil_div(int a, int b) { return (a + b - 1) / b; }
+inline int ceil_div(int a, int b) { return a / b + (a % b > 0); }   // (also where a + b passes 2^31)
 
 // A bump allocator over a caller-provided workspace.
 struct WsCursor {

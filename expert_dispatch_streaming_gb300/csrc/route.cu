@@ -367,10 +367,11 @@ gather_rows_kernel(const uint16_t* __restrict__ x, const int32_t* __restrict__ s
                    int k, int H, uint16_t* __restrict__ x_perm) {
   pdl_trigger();
   pdl_wait();
-  const int warp = (blockIdx.x * blockDim.x + threadIdx.x) >> 5, lane = threadIdx.x & 31;
-  if (warp >= rows) return;
-  const int nvec = H / 8, from = src[warp];
-  uint4* d = reinterpret_cast<uint4*>(x_perm + (size_t)warp * H);
+  // (row by row: threads in all pass 2^32 from 2^27 rows on)
+  const unsigned row = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  if (row >= (unsigned)rows) return;
+  const int lane = threadIdx.x & 31, nvec = H / 8, from = src[row];
+  uint4* d = reinterpret_cast<uint4*>(x_perm + (size_t)row * H);
   if ((unsigned)from >= (unsigned)rows) {   // a row that no slot takes: zeros
     for (int v = lane; v < nvec; v += 32) d[v] = make_uint4(0u, 0u, 0u, 0u);
     return;
@@ -603,8 +604,8 @@ int launch_route(const RouteArgs& a, const RoutePlan& r, const RouteScratch& s,
 int launch_gather(const uint16_t* x, const int32_t* src, int rows, int k, int H,
                   uint16_t* x_perm, cudaStream_t st) {
   if (rows <= 0) return MOE_OK;
-  MOE_LAUNCH_PDL(gather_rows_kernel, dim3(ceil_div(rows * 32, 256)), dim3(256), 0, st, x, src,
-                 rows, k, H, x_perm);
+  MOE_LAUNCH_PDL(gather_rows_kernel, dim3(ceil_div(rows, 8)), dim3(256), 0, st, x, src, rows, k,
+                 H, x_perm);
   MOE_COUNT_LAUNCH();
   MOE_LAUNCH_CHECK();
   return MOE_OK;

@@ -73,3 +73,19 @@ def test_permute_backward_and_combine_of_the_largest_batch(moe):  # noqa: F811
     for lo, hi in pieces(T):
         assert torch.equal(out[lo:hi], y[T - hi:T - lo].flip(0) * 2.0)
         assert torch.all(normed[lo:hi] == 1.0)
+
+
+@pytest.mark.parametrize("T,k", [((1 << 26) + 3, 1), ((1 << 26) + 1, 2), ((1 << 31) - 1, 1)])
+def test_permute_of_large_batches(moe, T, k):  # noqa: F811
+    """One warp a row: the threads in all pass 2^31 and 2^32."""
+    rows, H = T * k, 8
+    need(90 if rows > 1 << 30 else 8)
+    x = rows_of(T, H, 4)
+    src = torch.arange(rows - 1, -1, -1, dtype=I32, device="cuda")
+    src[::5] = -1
+    xp = torch.full((rows, H), 5.5, dtype=BF, device="cuda")
+    moe.moe_permute(x, src, T, k, H, xp)
+    for lo, hi in pieces(rows):
+        s = src[lo:hi].long()
+        want = x[s.clamp_min(0) // k] * (s >= 0)[:, None]
+        assert torch.equal(xp[lo:hi], want)
