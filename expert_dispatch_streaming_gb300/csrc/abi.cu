@@ -456,7 +456,7 @@ int moe_route_topk_grouped(const uint16_t* x, const float* w_r, const float* log
 
 int moe_permute(const uint16_t* x, const int32_t* src, int T, int k, int H, uint16_t* x_perm,
                 void* stream) {
-  MOE_REQUIRE(T >= 0 && k >= 1 && H > 0 && H % 8 == 0);
+  MOE_REQUIRE(T >= 0 && k >= 1 && H > 0 && H % 8 == 0 && (long long)T * k <= 0x7fffffffLL);
   if (T == 0) return MOE_OK;
   MOE_REQUIRE(x && src && x_perm && aligned16(x) && aligned16(x_perm));
   return launch_gather(x, src, T * k, k, H, x_perm, (cudaStream_t)stream);
@@ -529,7 +529,8 @@ int moe_grouped_swiglu(const uint16_t* x_perm, const int32_t* offsets,
 int moe_combine(const uint16_t* y_perm, const int32_t* pos, const float* w, int T, int k, int H,
                 const uint16_t* shared, const float* shared_gate, const uint16_t* residual,
                 uint16_t* out, uint16_t* out_normed, float norm_eps, void* stream) {
-  MOE_REQUIRE(T >= 0 && k >= 1 && k <= kMaxK && H > 0 && H % 8 == 0);
+  MOE_REQUIRE(T >= 0 && k >= 1 && k <= kMaxK && H > 0 && H % 8 == 0 &&
+              (long long)T * k <= 0x7fffffffLL);
   MOE_REQUIRE(!out_normed || (H <= kMaxNormH && norm_eps >= 0.f));
   if (T == 0) return MOE_OK;
   MOE_REQUIRE(y_perm && pos && w && out && aligned16(y_perm) && aligned16(out));

@@ -348,7 +348,7 @@ int moe_sort_tokens(const int32_t* ids, int T, int E, int k, int32_t* counts, in
  * x_perm[p][:] = x[src[p] / k][:] for p in [0, T*k).
  *  x device [T][H] bf16, src device [T*k] int32, x_perm device [T*k][H] bf16.
  * A row whose src lies outside [0, T*k) is written as zeros.
- * H a multiple of 8.  The pages define no permutation step: it is the gather that puts each
+ * H a multiple of 8, T*k < 2^31.  The pages define no permutation step: it is the gather that puts each
  * expert's tokens next to each other so that every selected expert's weights are read once per
  * batch ("NovaLLM ...", "3. Optimization #1 -- Expert-Level Streaming" asks only that the
  * experts a batch hits be loaded and run). */
@@ -481,6 +481,7 @@ int moe_grouped_gemv_int4(const uint16_t* x, const uint8_t* w, const uint16_t* w
  * computed from the bf16 values of out[t] (sum of squares in fp32); H <= 32768 then.
  *  y_perm device [T*k][H] bf16; pos, w device [T][k]; shared, residual, out device [T][H].
  * A slot whose pos lies outside [0, T*k) has no term, whatever its weight.
+ * T*k < 2^31.
  * The pages define no combine step: it is the gate-weighted sum that undoes the permutation,
  * the usual form of a top-k MoE layer's output. */
 int moe_combine(const uint16_t* y_perm, const int32_t* pos, const float* w, int T, int k,
