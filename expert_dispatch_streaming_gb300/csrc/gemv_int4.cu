@@ -475,8 +475,10 @@ gemv_int4_kernel(const GemvArgs a, const __grid_constant__ CUtensorMap tm) {
       warp_wait(full + i % kBoxes, (i / kBoxes) & 1, a.err, kGvErrWait);
 }
 
+// (an item's rows are counted in eights, in 32 bits: the last eight of max_rows ends below 2^31)
 bool valid_gemv_shape(int E, int N, int K, int max_rows) {
   return E > 0 && E <= kMaxExperts && N > 0 && K > 0 && K % 32 == 0 && max_rows >= 0 &&
+         max_rows <= 0x7fffffff - 8 &&
          N <= (1 << 24) && K <= (1 << 24) && (long long)E * N < (1LL << 31);
 }
 
@@ -516,7 +518,7 @@ int launch_gemv(const GemvArgs& a, const uint8_t* w, cudaStream_t st) {
   for (int n = 1; n <= kGvMaxTile; ++n) {
     const long long tiles = ceil_div(a.N, n * kGvUnit), slots = 2LL * sm_count();
     const long long cost = (std::max(1LL, passes) * tiles + slots - 1) / slots * (n + 1);
-    if (most * tiles > 0x3fffffff) return MOE_ERR_INVALID_ARG;   // (y alone would not fit on the GPU)
+    if (most * tiles > 0x3fffffff) return MOE_ERR_INVALID_ARG;   // (items are counted in 32 bits)
     if (!nt || cost <= best) {
       nt = n;
       best = cost;

@@ -460,7 +460,8 @@ int moe_grouped_swiglu_fp8(const uint8_t* xq, const float* x_scale, const int32_
  *           256-byte aligned
  * Limits: 1 <= E <= 256, N >= 1, K a multiple of 32; x, w, y 16-byte, w_scale 2-byte aligned (16-byte
  * aligned scales and zero points and K a multiple of 256 take wide loads).  Any number of rows is
- * computed, eight of an expert at a time, each eight reading its weights.
+ * computed, eight of an expert at a time, each eight reading its weights; max_rows <= 2^31 - 9, and the
+ * eights there can be, (max_rows + 7 min(E, max_rows)) / 8, times ceil(N / 16) stay below 2^30.
  * A NaN or an infinity in a token row or a scale reaches the outputs of that token row or weight row
  * only.
  * "Running 35B MoE Models on 8GB GPUs ...", "Technical Insight" names 4-bit checkpoints; the layout
