@@ -21,6 +21,7 @@ namespace moe {
 namespace {
 
 constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32;
+constexpr int kSortParts = kSortThreads / kMaxExperts;   // threads an expert
 // One chunk up to this many slots, else chunks of kSortChunk at least (8192 slots: one CTA 11.4 us, four
 // 7.3), and at most kSortMaxChunks, whose histograms every CTA reads (262144 slots: 128 chunks 12.0 us,
 // 64 9.5, 48 10.9).
@@ -55,6 +56,16 @@ sort_histogram_kernel(const int32_t* __restrict__ ids, int n, int E, int chunk,
   if (threadIdx.x < E) hist[(size_t)blockIdx.x * E + threadIdx.x] = s[threadIdx.x];
 }
 
+struct SortSmem {
+  int base[kSortWarps][kMaxExperts];     // a warp's slots of e, then its next row of e in ...
+  int before[kSortParts][kMaxExperts];   // slots of e in earlier chunks, by parts; then the row where ...
+                                         // ... those of eight warps start
+  int total[kSortParts][kMaxExperts], own[kSortParts][kMaxExperts];
+  int scan[kMaxExperts / 32];
+  int rows;
+};
+static_assert(sizeof(SortSmem) <= 48 * 1024, "static shared memory");
+
 // hist: [gridDim.x][E] chunk histograms; chained: launched behind sort_histogram_kernel, else one chunk
 // holds every slot.
 __global__ void __launch_bounds__(kSortThreads)
@@ -62,12 +73,12 @@ sort_rank_kernel(const int32_t* __restrict__ ids, int n, int E, int chunk,
                  const int32_t* __restrict__ hist, int32_t* __restrict__ counts,
                  int32_t* __restrict__ offsets, int32_t* __restrict__ pos,
                  int32_t* __restrict__ src, bool chained) {
-  constexpr int kParts = kSortThreads / kMaxExperts, kPer = kSortWarps / kParts;
-  __shared__ int base[kSortWarps][kMaxExperts];   // a warp's slots of e, then its next row of e in ...
-  __shared__ int from[kParts][kMaxExperts];       // ... those of eight warps, which start here
-  __shared__ int before[kParts][kMaxExperts], total[kParts][kMaxExperts], own[kParts][kMaxExperts];
-  __shared__ int scan[kMaxExperts / 32];
-  __shared__ int rows;
+  constexpr int kParts = kSortParts, kPer = kSortWarps / kParts;
+  __shared__ SortSmem sm;
+  auto& base = sm.base;
+  auto& before = sm.before;
+  auto& total = sm.total;
+  auto& own = sm.own;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_trigger();
   for (int i = tid; i < kSortWarps * kMaxExperts; i += kSortThreads) (&base[0][0])[i] = 0;
@@ -115,14 +126,14 @@ sort_rank_kernel(const int32_t* __restrict__ ids, int n, int E, int chunk,
       const int v = __shfl_up_sync(0xffffffffu, inc, o);
       if (lane >= o) inc += v;
     }
-    if (lane == 31) scan[warp] = inc;
+    if (lane == 31) sm.scan[warp] = inc;
   }
   __syncthreads();
   if (tid < kMaxExperts) {
     int off = inc - mine;
 #pragma unroll
-    for (int w = 0; w < kMaxExperts / 32; ++w) off += w < warp ? scan[w] : 0;
-    if (tid == kMaxExperts - 1) rows = off + mine;
+    for (int w = 0; w < kMaxExperts / 32; ++w) off += w < warp ? sm.scan[w] : 0;
+    if (tid == kMaxExperts - 1) sm.rows = off + mine;
     if (blockIdx.x == 0 && e < E) {
       counts[e] = mine;
       offsets[e] = off;
@@ -132,7 +143,7 @@ sort_rank_kernel(const int32_t* __restrict__ ids, int n, int E, int chunk,
     for (int p = 0; p < kParts; ++p) off += before[p][e];
 #pragma unroll
     for (int p = 0; p < kParts; ++p) {
-      from[p][e] = off;
+      before[p][e] = off;                  // (this thread's alone until the barrier)
       off += own[p][e];
     }
   }
@@ -149,12 +160,12 @@ sort_rank_kernel(const int32_t* __restrict__ ids, int n, int E, int chunk,
     if (has && rank == 0) base[warp][id] = first + __popc(same);
     __syncwarp();
     if (i < w1) {
-      const int p = has ? from[warp / kPer][id] + first + rank : -1;
+      const int p = has ? before[warp / kPer][id] + first + rank : -1;
       pos[lo + i] = p;
       if (has) src[p] = lo + i;
     }
   }
-  for (long long i = (long long)rows + blockIdx.x * kSortThreads + tid; i < n;
+  for (long long i = (long long)sm.rows + blockIdx.x * kSortThreads + tid; i < n;
        i += (long long)gridDim.x * kSortThreads)
     src[i] = -1;
 }

@@ -89,3 +89,27 @@ def test_permute_of_large_batches(moe, T, k):  # noqa: F811
         s = src[lo:hi].long()
         want = x[s.clamp_min(0) // k] * (s >= 0)[:, None]
         assert torch.equal(xp[lo:hi], want)
+
+
+def test_sort_of_the_most_slots(moe):  # noqa: F811
+    """2^31 - 1 slots, experts in turn and every fifth slot without one."""
+    need(40)
+    n, E = (1 << 31) - 1, 4
+    ids = torch.empty(n, dtype=I32, device="cuda")
+    for lo, hi in pieces(n):
+        ids[lo:hi] = torch.arange(lo, hi, device="cuda") % 5          # 4: no expert
+    i32 = dict(dtype=I32, device="cuda")
+    counts, offsets = torch.full((E,), 7, **i32), torch.full((E + 1,), 7, **i32)
+    pos, src = torch.full((n,), 7, **i32), torch.full((n,), 7, **i32)
+    nb = moe.moe_sort_tokens_workspace_size(n, E, 1)
+    moe.moe_sort_tokens(ids, n, E, 1, counts, offsets, pos, src,
+                        torch.empty(nb, dtype=torch.uint8, device="cuda"), nb)
+    per = [(n - e + 4) // 5 for e in range(E)]
+    at = [sum(per[:e]) for e in range(E + 1)]
+    assert counts.tolist() == per and offsets.tolist() == at
+    start = torch.tensor(at[:E] + [0], device="cuda")
+    for lo, hi in pieces(n):
+        s = torch.arange(lo, hi, device="cuda")
+        assert torch.equal(pos[lo:hi].long(), torch.where(s % 5 < 4, start[s % 5] + s // 5, -1))
+        e = (s[:, None] >= torch.tensor(at[1:], device="cuda")).sum(1)
+        assert torch.equal(src[lo:hi].long(), torch.where(e < 4, 5 * (s - start[e]) + e, -1))
