@@ -70,6 +70,10 @@ int moe_version(void);
  *    is scheduled while its predecessor finishes and waits in-kernel for its results); 0
  *    (default) = plain stream-ordered launches, which measured as fast or faster on GB300 at
  *    every workload tried.  Results are identical either way.
+ *    (Not under the option: group-limited routing's kernels after its first, FP8 products behind the
+ *    clearing of their control words, the slot sort, the gradients and the 4-bit products are always
+ *    launched programmatically.  They wait, as all kernels here do, for what precedes them on the
+ *    stream before they touch memory.)
  *  MOE_OPT_DECODE_KERNEL: 2 = moe_layer_forward runs a batch of at most 16 tokens with every
  *    bundle resident (no cache) as one cooperative launch that routes, runs the shared and
  *    routed experts and combines; 1 (default) = the same except for INT4 weights with more
