@@ -241,7 +241,7 @@ gate_backward_chosen_kernel(const float* __restrict__ logits, const int32_t* __r
     const bool tiny = total < 0x1p-64f;
     if (__any_sync(0xffffffffu, tiny)) {
       // sigmoids that fp32 is about to lose: e^l is their ratio to 2^-64, as far as 64 bits hold them
-      // (the weights' own rule); beyond, weights and gradients are zero
+      // (group-limited routing's rule for the weights); beyond, weights and gradients are zero
       const float top = max8(l);
       if (tiny) v = id >= 0 && top > -709.f ? expf(l - top) : 0.f;
       const float again = sum8(v);

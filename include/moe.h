@@ -542,7 +542,10 @@ int moe_combine_backward(const uint16_t* dout, const uint16_t* y_perm, const int
  * what it keeps; a token that is all padding): its dw is not read and it is in no sum.  An id
  * that stands twice in a row counts as two slots.  A slot whose weight is zero (a logit of -infinity)
  * is in no sum either, whatever its dw; a token whose weights are all zero (every score open to it
- * -infinity, see moe_route_topk_grouped) gets zero gradients.
+ * -infinity, see moe_route_topk_grouped) gets zero gradients, and sigmoids below fp32's range keep their
+ * ratios: moe_route_topk_grouped's rules.  moe_route_topk has neither; where all chosen logits are
+ * -infinity, or all chosen sigmoids zero in fp32 (logits below -88), its weights are NaN and this
+ * gradient is not theirs.
  * A NaN logit that makes weights NaN (a chosen expert's; SOFTMAX: any of the row) makes the chosen
  * experts' gradients (SOFTMAX: the row's) NaN; a token without an expert in any slot gets zeros.
  * Limits: E <= 256, k <= min(E, 8); dlogits 16-byte aligned. */

@@ -142,3 +142,45 @@ def test_dropped_slots_through_the_documented_calls(moe, gating, scale):  # noqa
     assert torch.all((got - want).abs() <= 2 * scale * size * (N + E + 66) * 2.0 ** -23)
     part = drop & ~drop.all(1, keepdim=True)
     assert torch.all(got.gather(1, ids.long())[part] != 0) and torch.all(got[7] == 0)
+
+
+@pytest.mark.parametrize("gating", GATING)
+@pytest.mark.parametrize("low", [-60.0, -100.0, -300.0, -INF])
+def test_weights_and_gradient_of_low_scores(moe, gating, low):  # noqa: F811
+    """Group-limited routing and the gradient follow one rule where scores are so low that nothing, or
+    next to nothing, is left: logits (the bias alone) around `low`, every weight finite and its gradient
+    that of the weights as routing made them."""
+    T, H, E, k, scale = 5, 64, 32, 4, 1.5
+    g = gen(17)
+    x = torch.zeros((T, H), dtype=torch.bfloat16, device="cuda")
+    w_r = torch.zeros((H, E), device="cuda")
+    bias = torch.randn(E, generator=g, device="cuda") + low
+    i32 = dict(dtype=torch.int32, device="cuda")
+    ids, w, z = torch.empty((T, k), **i32), torch.empty((T, k), device="cuda"), torch.empty(
+        (T, E), device="cuda")
+    disp = [torch.empty(E, **i32), torch.empty(E + 1, **i32), torch.empty((T, k), **i32),
+            torch.empty(T * k, **i32)]
+    nb = moe.moe_route_workspace_size(T, H, E, k)
+    moe.moe_route_topk_grouped(x, w_r, bias, None, None, T, H, E, k, 4, 2, gating, scale, ids, w, *disp, z,
+                               None, None, torch.empty(nb, dtype=torch.uint8, device="cuda"), nb)
+    assert torch.all(torch.isfinite(w))
+    dw = torch.randn((T, k), generator=g, device="cuda")
+    got = run_gate(moe, z, ids, dw, gating, scale)
+    if low == -INF:
+        assert torch.all(w == 0) and torch.all(got == 0)
+        return
+    assert torch.all(z[0] == bias)
+    r = w.double() / scale
+    D = (r * dw.double()).sum(1, keepdim=True)
+    if gating == "softmax":
+        want = -scale * torch.softmax(z.double(), 1) * D
+        want.scatter_add_(1, ids.long(), scale * r * dw.double())
+    else:
+        want = torch.zeros_like(z, dtype=torch.float64)
+        slope = torch.sigmoid(-z.double()).gather(1, ids.long()) if "sigmoid" in gating else 1.0
+        want.scatter_(1, ids.long(), scale * r * (dw.double() - D) * slope)
+    # both the weights and the gradient are off by the rounding of exponents of at most 2 |low| and a
+    # few products: (2 |low| + E + 16) 2^-23 of the terms each
+    mag = scale * dw.double().abs().sum(1, keepdim=True)
+    assert torch.all((got.double() - want).abs() <= 4 * mag * (2 * abs(low) + E + 16) * 2.0 ** -23)
+    assert torch.any(got != 0)
