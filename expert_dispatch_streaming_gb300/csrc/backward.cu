@@ -34,7 +34,7 @@ __device__ __forceinline__ float reduce_warp(float v) {
 //   dx[t] = sum_{j<k} dx_perm[pos[t][j]]  (+ add[t])
 // in fp32, j in order, rounded once.  Block (c, t): elements [1024 c, 1024 c + 1024) of token t, one
 // 16-byte piece of each of the k rows a thread.  Reading the rows bounds it: 8192 tokens of eight rows
-// of 7168 take 158 us, the 1057 MB it needs at 99% of the copy bandwidth.
+// of 7168 take 156 us, the 1057 MB it needs at the copy bandwidth.
 template <int K, bool F32>
 __global__ void __launch_bounds__(kBackThreads)
 permute_backward_kernel(const uint16_t* __restrict__ dxp, const int32_t* __restrict__ pos,
@@ -82,7 +82,7 @@ permute_backward_kernel(const uint16_t* __restrict__ dxp, const int32_t* __restr
 // A CTA takes one token: a thread reads a 16-byte vector of dout[t] and of the k rows, writes the
 // k scaled vectors and keeps k + 1 partial dot products, which the CTA adds in a fixed order: one
 // pass over y_perm and dy_perm, which bound it.  8192 tokens of eight rows of 7168 and a shared expert
-// take 316 us, the 2115 MB it needs at 99% of the copy bandwidth.
+// take 311 us, the 2115 MB it needs at the copy bandwidth.
 constexpr int kCombineBackThreads = 256;
 
 template <int K>
@@ -166,11 +166,14 @@ combine_backward_kernel(const uint16_t* __restrict__ dout, const uint16_t* __res
 //   softmax_renorm:       dl_j = scale r_j (dw_j - D)
 //   sigmoid_bias_renorm:  dl_j = scale r_j (dw_j - D) (1 - sigmoid(l_j))
 //   softmax (over all E): dl_e = scale p_e ([e chosen] dw_e - D),  D = sum_j p_j dw_j
-// Writing the dlogits rows bounds it.  SOFTMAX_RENORM and SIGMOID_BIAS_RENORM read the chosen logits
-// only: a warp takes four tokens, eight lanes each for the chosen experts.  It stores zeros to the four
+// where the ids are those that w was normalised over.  SOFTMAX_RENORM and SIGMOID_BIAS_RENORM read the chosen
+// logits only: a warp takes four tokens, eight lanes each for the chosen experts.  It stores zeros to the four
 // rows, which lie next to each other, while the chosen logits are on their way, and then the chosen
-// experts' values over them (32768 tokens of 256 experts: 8.4 us with the rows put together in shared
-// memory first, which also kept CTAs off the SMs, 7.4 so).  SOFTMAX: a warp a token.
+// experts' values over them.  The chain of ids, gathered logits, exponentials and stores bounds it, each
+// warp once: 32768 tokens of 256 experts, eight chosen, take 10.9 us in graphs of calls whose inputs change
+// (5.4 at the copy bandwidth, 8.5 with the 64 bytes fetched for a gathered logit) and 7.7 on the same
+// inputs again, where putting the rows together in shared memory first cost 1 us more.  SOFTMAX: a warp a
+// token, 16.7 us (10.2) and 12.8.
 constexpr int kGateBackWarps = 8;
 
 // g of an expert that stands more than once in the lane's eight: the sum, in lane order, on the first

@@ -22,22 +22,24 @@
 // and the token row's eight values come from one 16-byte load.
 //
 // An item is 16, 32 or 48 weight rows of one expert against eight token rows, over the whole of K, so
-// that no sum crosses CTAs; the height is the one that leaves the fewest CTAs without work.  A CTA's
+// that no sum crosses CTAs; the height is the one whose rounds of items cost the least (launch_gemv).  A CTA's
 // eight warps share an item's K, 256 codes at a time, and keep a step's token values in registers
 // for all its weight rows.  Each warp has a ring of its own in shared memory, filled by TMA
 // (boxes of the item's rows x 128 bytes, swizzled, so that the lanes' words lie in different
 // banks) and running on from one item to the next; token values and scales are loaded ahead of their
 // use.  The warps' sums are added in warp order in shared memory.
 //
-// Measured (the floor is what has to be read and written at the copy bandwidth): 14336 x 14336 codes,
-// groups of 128, one token 22.9 us (floor 15.6; the same boxes loaded and not used 18.5), eight tokens
-// 24.9; 8 of 256 experts of 4096 x 7168 30.6 us (17.9), 64 tokens on most of the 256 588 us (414); 4096 x
-// 7168, one token, 8.3 us, eight 9.1, of which launch, first loads and the last sums are 6.  Turning
-// codes to bf16 bounds the large ones: 144 of about 280 instructions for 4096 codes, with the issue slots
-// 60% busy.
-// More than eight token rows are passes side by side: 16 rows a pass need registers that 16 warps a SM
-// do not have, and a kernel for 64, codes turned once, won (1.1 to 1.6 times) only from 33 rows and
-// 4096 weight rows on.
+// Measured, groups of 128, in graphs of calls whose inputs change from call to call (the floor is what has
+// to be read and written at the copy bandwidth): 14336 x 14336 codes, one token 22.6 us (floor 15.6; the
+// same boxes loaded and not used 18.5), eight tokens 24.7; one row each on 8 experts of 4096 x 7168 30.9 us
+// (17.9), two rows each on 256 of them, zero points, 762 us (581); 4096 x 7168, one token, 7.6 us, eight 8.6,
+// of which launch, first loads and the last sums are about 6.  No pipe is full in the large ones: of about
+// 280 instructions for 4096 codes 144 turn codes to bf16 and 20 are products and their loads, the issue slots
+// are 60% busy with four warps a scheduler, the copy bandwidth 65 to 75%.  K that is no multiple of 256 takes
+// scales one by one: 14304 x 14336, one token, 31.3 us.
+// More than eight token rows are passes side by side, an expert's whole weights after one another in each: 64
+// rows on 14336 x 14336 146 us.  16 rows a pass need registers that 16 warps a SM do not have, and a kernel
+// for 64, codes turned once, won (1.1 to 1.6 times) only from 33 rows and 4096 weight rows on.
 #include "common.cuh"
 #include "route.cuh"
 #include "tc_ptx.cuh"
@@ -512,7 +514,8 @@ int launch_gemv(const GemvArgs& a, const uint8_t* w, cudaStream_t st) {
   const long long most = (a.max_rows + 7LL * std::min(a.E, a.max_rows)) / 8;
   const long long passes = std::min<long long>(most, (a.E + 1) / 2 + a.max_rows / 8);
   // the height whose rounds cost the least: its rows, and what a step costs beside them (about one unit:
-  // 602, 680 and 952 us with 48, 32 and 16 rows for 64 tokens on 256 experts of 4096 x 7168)
+  // 602, 680 and 952 us with 48, 32 and 16 rows for 64 tokens on 256 experts of 4096 x 7168); ties to
+  // the higher
   long long best = 0;
   int nt = 0, items = 0;
   for (int n = 1; n <= kGvMaxTile; ++n) {

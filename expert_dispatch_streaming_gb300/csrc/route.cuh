@@ -91,8 +91,8 @@ struct RouteArgs {
 // (group-limited routing's five launches, 60 experts and 333 tokens: 37 us plain, 31 chained).
 // The slot sort, the gradients and the 4-bit products launch so whatever came before them (they
 // touch nothing before they have waited for it): behind a kernel that lets them, as all of theirs do,
-// a call in a row of them costs about 2 us less (32768 x 8 slots sorted 12.4 -> 9.8 us, one token on
-// 4096 x 7168 codes 10.4 -> 8.7).
+// a call in a row of them costs 3 us less (32768 x 8 slots sorted 12.3 -> 9.2 us, one token on
+// 4096 x 7168 codes 10.2 -> 6.9).
 template <typename... KArgs, typename... Args>
 cudaError_t launch_next(bool chained, void (*kernel)(KArgs...), dim3 grid, dim3 block,
                         size_t smem, cudaStream_t st, Args&&... args) {

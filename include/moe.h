@@ -84,7 +84,7 @@ enum moe_option { MOE_OPT_FFN_KERNEL = 1, MOE_OPT_PDL = 2, MOE_OPT_DECODE_KERNEL
 int moe_set_option(int option, int value);
 
 /* Reads the device error word kept in the first 4 bytes of a moe_layer_forward,
- * moe_grouped_swiglu or moe_route_topk workspace into *code (host) and waits for `stream`.
+ * moe_grouped_swiglu, grouped product's or moe_route_topk workspace into *code (host) and waits for `stream`.
  * 0 = no error; otherwise the last call on that workspace produced invalid outputs:
  *   1-7  a bounded wait inside a tensor-core kernel ran out of time;
  *   9    a bounded wait inside the fused decode kernel ran out of time;
@@ -518,7 +518,8 @@ int moe_permute_backward(const uint16_t* dx_perm, const int32_t* pos, const uint
  *  dout, shared, dshared device [T][H] bf16; y_perm, dy_perm device [T*k][H] bf16; w, dw device
  *  [T][k] fp32; shared_gate, dshared_gate device [T] fp32.  Any of the four outputs may be NULL
  *  (not all); y_perm is read for dw only, shared for dshared_gate only (which needs shared and
- *  shared_gate).
+ *  shared_gate).  Where the rows past offsets[E] are read after all (a weight gradient over all T*k),
+ *  clear dy_perm before the call: they may hold another dispatch's.
  *  H a multiple of 8; bf16 rows 16-byte aligned; k <= 8. */
 int moe_combine_backward(const uint16_t* dout, const uint16_t* y_perm, const int32_t* pos,
                          const float* w, int T, int k, int H, const uint16_t* shared,

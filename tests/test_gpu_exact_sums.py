@@ -122,3 +122,16 @@ def test_permute_backward_whole_numbers(moe, T, E, k, H):  # noqa: F811
         dx = torch.empty((T, H), device="cuda", dtype=t)
         moe.moe_permute_backward(d, pos, add, T, k, H, out, dx)
         assert torch.equal(dx.double(), want)        # (|sums| <= 72: whole numbers that bf16 holds)
+
+
+@pytest.mark.parametrize("rows", [1, 40])
+def test_gemv_of_no_rows(moe, rows):  # noqa: F811
+    """Offsets that give no expert a row: nothing is written, and no error recorded."""
+    N, K, E = 50, 320, 5
+    g = gen(1)
+    w = torch.randint(0, 256, (E, N, K // 2), generator=g, device="cuda", dtype=torch.uint8)
+    s = torch.ones((E, N, K // 32), dtype=torch.bfloat16, device="cuda")
+    x = torch.ones((rows, K), dtype=torch.bfloat16, device="cuda")
+    off = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    y, ws = run(moe, x, w, s, None, off, 32, rows, "fp32", N, K, E)
+    assert torch.all(y == 5.0) and moe.moe_workspace_error(ws) == 0
