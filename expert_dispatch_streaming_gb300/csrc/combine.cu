@@ -38,14 +38,25 @@ combine_kernel(const uint16_t* __restrict__ y, const int32_t* __restrict__ pos,
     pj[j] = __ldg(pos + (size_t)t * K + j);
     wj[j] = __ldg(w + (size_t)t * K + j);
   }
-  uint4 q[K];
+  // (from three rows on, a test before each load takes the loads out of flight together: 8192 tokens of
+  // eight rows of 7168 166 us, 155 so; a token with all its rows, the usual one, has none)
+  bool every = K > 2;
 #pragma unroll
-  for (int j = 0; j < K; ++j) {
-    q[j] = make_uint4(0u, 0u, 0u, 0u);
-    if ((unsigned)pj[j] < (unsigned)T * K)
+  for (int j = 0; j < K; ++j) every &= (unsigned)pj[j] < (unsigned)T * K;
+  uint4 q[K];
+  if (every) {
+#pragma unroll
+    for (int j = 0; j < K; ++j)
       q[j] = __ldg(reinterpret_cast<const uint4*>(y + (size_t)pj[j] * H) + v);
-    else
-      wj[j] = 0.f;   // a slot without a row, whatever its weight
+  } else {
+#pragma unroll
+    for (int j = 0; j < K; ++j) {
+      q[j] = make_uint4(0u, 0u, 0u, 0u);
+      if ((unsigned)pj[j] < (unsigned)T * K)
+        q[j] = __ldg(reinterpret_cast<const uint4*>(y + (size_t)pj[j] * H) + v);
+      else
+        wj[j] = 0.f;   // a slot without a row, whatever its weight
+    }
   }
   float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -91,26 +102,36 @@ combine_kernel(const uint16_t* __restrict__ y, const int32_t* __restrict__ pos,
 //   out_n[t] = bf16( out[t] / sqrt(mean_h(out[t][h]^2) + eps) )
 // from the bf16 values of out[t] (sum of squares in fp32, block reduction in fixed order), the
 // input of the next layer of a pre-norm stack.  Each thread keeps its up to kNormVec vectors of
-// the row in registers between the two passes.
+// the row in registers between the two passes, and the loads of up to four of a vector's K rows in flight
+// together (eight take registers that cost CTAs: 8192 tokens of eight rows of 7168 184 us, 200 so).
 constexpr int kNormVec = 4;
 
+template <int K>
 __global__ void __launch_bounds__(1024)
 combine_norm_kernel(const uint16_t* __restrict__ y, const int32_t* __restrict__ pos,
-                    const float* __restrict__ w, int T, int k, int H,
+                    const float* __restrict__ w, int T, int H,
                     const uint16_t* __restrict__ shared, const float* __restrict__ shared_gate,
                     const uint16_t* __restrict__ residual, uint16_t* __restrict__ out,
                     uint16_t* __restrict__ out_n, float eps) {
+  constexpr int kBatch = K <= 4 ? K : 4;
   pdl_trigger();
   pdl_wait();
   __shared__ float red[32];
   const int nv = H / 8;
   for (unsigned t = blockIdx.x; t < (unsigned)T; t += gridDim.x) {
-    int pj[kMaxK];
-    float wj[kMaxK];
+    int pj[K];
+    float wj[K];
+    bool every = K > 2;   // (see combine_kernel)
 #pragma unroll
-    for (int j = 0; j < kMaxK; ++j) {
-      pj[j] = j < k ? __ldg(pos + (size_t)t * k + j) : 0;
-      wj[j] = j < k ? __ldg(w + (size_t)t * k + j) : 0.f;
+    for (int j = 0; j < K; ++j) {
+      pj[j] = __ldg(pos + (size_t)t * K + j);
+      wj[j] = __ldg(w + (size_t)t * K + j);
+      every &= (unsigned)pj[j] < (unsigned)T * K;
+    }
+    if (!every) {
+#pragma unroll
+      for (int j = 0; j < K; ++j)
+        if ((unsigned)pj[j] >= (unsigned)T * K) wj[j] = 0.f;   // a slot without a row, whatever its weight
     }
     const float gs = (shared && shared_gate) ? __ldg(shared_gate + t) : 1.f;
     uint32_t o[kNormVec][4];
@@ -120,15 +141,32 @@ combine_norm_kernel(const uint16_t* __restrict__ y, const int32_t* __restrict__ 
       const int v = threadIdx.x + i * blockDim.x;
       if (v >= nv) break;
       float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      for (int j = 0; j < k; ++j) {
-        if ((unsigned)pj[j] >= (unsigned)T * k) continue;   // a slot without a row
-        const uint4 q = __ldg(reinterpret_cast<const uint4*>(y + (size_t)pj[j] * H) + v);
-        const uint32_t qw[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const float2 f = bf16x2_to_float2(qw[c]);
-          acc[2 * c] = fmaf(wj[j], f.x, acc[2 * c]);
-          acc[2 * c + 1] = fmaf(wj[j], f.y, acc[2 * c + 1]);
+      for (int j0 = 0; j0 < K; j0 += kBatch) {
+        uint4 q[kBatch];
+        if (every) {
+#pragma unroll
+          for (int j = 0; j < kBatch; ++j)
+            if (j0 + j < K)
+              q[j] = __ldg(reinterpret_cast<const uint4*>(y + (size_t)pj[j0 + j] * H) + v);
+        } else {
+#pragma unroll
+          for (int j = 0; j < kBatch; ++j) {
+            q[j] = make_uint4(0u, 0u, 0u, 0u);
+            if (j0 + j < K && (unsigned)pj[j0 + j] < (unsigned)T * K)
+              q[j] = __ldg(reinterpret_cast<const uint4*>(y + (size_t)pj[j0 + j] * H) + v);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+          if (j0 + j >= K) break;
+          const uint32_t qw[4] = {q[j].x, q[j].y, q[j].z, q[j].w};
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const float2 f = bf16x2_to_float2(qw[c]);
+            acc[2 * c] = fmaf(wj[j0 + j], f.x, acc[2 * c]);
+            acc[2 * c + 1] = fmaf(wj[j0 + j], f.y, acc[2 * c + 1]);
+          }
         }
       }
       if (shared) {
@@ -192,22 +230,19 @@ int launch_combine(const uint16_t* y, const int32_t* pos, const float* w, int T,
                    const uint16_t* shared, const float* shared_gate, const uint16_t* residual,
                    uint16_t* out, uint16_t* out_n, float eps, cudaStream_t st) {
   if (T <= 0) return MOE_OK;
-  if (out_n) {
-    const int nv = H / 8;
-    const int threads = std::min(1024, (int)round_up((size_t)ceil_div(nv, kNormVec), 32));
-    if (ceil_div(nv, threads) > kNormVec) return MOE_ERR_INVALID_ARG;
-    MOE_LAUNCH_PDL(combine_norm_kernel, dim3(std::min(T, 65535)), dim3(threads), 0, st, y, pos,
-                   w, T, k, H, shared, shared_gate, residual, out, out_n, eps);
-    MOE_COUNT_LAUNCH();
-    MOE_LAUNCH_CHECK();
-    return MOE_OK;
-  }
-  dim3 grid(ceil_div(H / 8, kCombineThreads), std::min(T, 65535));
-  const dim3 block(kCombineThreads);
+  const int nv = H / 8;
+  const int threads = std::min(1024, (int)round_up((size_t)ceil_div(nv, kNormVec), 32));
+  if (out_n && ceil_div(nv, threads) > kNormVec) return MOE_ERR_INVALID_ARG;
+  const dim3 grid(ceil_div(nv, kCombineThreads), std::min(T, 65535)), block(kCombineThreads);
+  const dim3 norm_grid(std::min(T, 65535)), norm_block(threads);
   auto go = [&](auto kc) -> int {
     constexpr int K = decltype(kc)::value;
-    MOE_LAUNCH_PDL(combine_kernel<K>, grid, block, 0, st, y, pos, w, T, H, shared, shared_gate,
-                   residual, out);
+    if (!out_n)
+      MOE_LAUNCH_PDL(combine_kernel<K>, grid, block, 0, st, y, pos, w, T, H, shared, shared_gate,
+                     residual, out);
+    else
+      MOE_LAUNCH_PDL(combine_norm_kernel<K>, norm_grid, norm_block, 0, st, y, pos, w, T, H, shared,
+                     shared_gate, residual, out, out_n, eps);
     return MOE_OK;
   };
   int r = MOE_ERR_INVALID_ARG;
